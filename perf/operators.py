@@ -1,0 +1,488 @@
+"""Cases of the serving path over an MX key/value cache: rotary tables, rotation,
+appending to the paged cache and attention over it.
+
+``run`` computes a case either with elementary torch operations in 32 bits (64 for
+the angles of far positions), or, where ``own`` is true, through the library's
+entry points.  The cache holds MXFP8 codes in blocks of 32 along the head
+dimension with one E8M0 scale each:
+
+    keys    codes [pages][heads][page][dim],         scales [pages][heads][page][dim / 32]
+    values  codes [pages][heads][page / 16][dim][16], scales [pages][heads][page / 16][dim / 32][16]
+
+Codes are returned as float8 and scales as E8M0 tensors, the values they stand for.
+Sizes follow the transformer layers the library is benchmarked on: 32 query heads,
+8 key/value heads, 128 channels a head, width 4096, sequences of 8192 tokens.
+"""
+
+import math
+
+import torch
+
+own = False
+
+
+def listed():
+    heads = {"heads": 32, "kv_heads": 8, "dim": 128}
+    return [
+        # the table of a model with 8192 positions, built when the model is loaded
+        {"name": "table 8k", "op": "table", "rows": 8192, "rot": 128, "base": 5e5, "scaling": "none", "factor": 1.0,
+         "orig_len": 8192},
+        # the same model stretched to a 131072-token context, frequencies blended by bands
+        {"name": "table 128k yarn", "op": "table", "rows": 131072, "rot": 128, "base": 5e5, "scaling": "yarn",
+         "factor": 16.0, "orig_len": 8192},
+        # forward rotation of the queries of one training sequence
+        {"name": "rope 8192x32 half", "op": "rope", "tokens": 8192, "heads": 32, "dim": 128, "rot": 128,
+         "layout": "half", "inverse": False, "dtype": "bf16", "fused": False},
+        # backward pass of a rotation of half the head, gradients a slice of a fused projection's, odd token count
+        {"name": "rope grad 1021x8 part", "op": "rope", "tokens": 1021, "heads": 8, "dim": 128, "rot": 64,
+         "layout": "interleaved", "inverse": True, "dtype": "f32", "fused": True},
+        # one decoding step of one request: launch latency
+        {"name": "append 1 token", "op": "append", "tokens": 1, "page": 64, "layout": "half", "rot": 128,
+         "dtype": "bf16", "chunk": False, **heads},
+        # one decoding step of a batch of requests, each at its own place in the cache
+        {"name": "append 256 tokens", "op": "append", "tokens": 256, "page": 64, "layout": "half", "rot": 128,
+         "dtype": "bf16", "chunk": False, **heads},
+        # a prompt of 8192 tokens entering the cache at once
+        {"name": "append 8192 prompt", "op": "append", "tokens": 8192, "page": 64, "layout": "half", "rot": 128,
+         "dtype": "bf16", "chunk": True, **heads},
+        # one request's next token over a short context: launch latency
+        {"name": "decode 1x1k", "op": "attention", "chunks": 0, "q_len": 1, "decoders": 1, "kv": 1021, "spread": 0.0,
+         "page": 64, "window": 0, "dtype": "bf16", **heads},
+        # a batch of requests of uneven lengths, one new token each
+        {"name": "decode 64x8k ragged", "op": "attention", "chunks": 0, "q_len": 1, "decoders": 64, "kv": 8192,
+         "spread": 0.8, "page": 64, "window": 0, "dtype": "bf16", **heads},
+        # few requests with very long contexts
+        {"name": "decode 4x128k", "op": "attention", "chunks": 0, "q_len": 1, "decoders": 4, "kv": 131072,
+         "spread": 0.1, "page": 64, "window": 0, "dtype": "bf16", **heads},
+        # prompts entering in chunks beside requests that decode, small pages
+        {"name": "mixed 2x250 + 14", "op": "attention", "chunks": 2, "q_len": 250, "decoders": 14, "kv": 4000,
+         "spread": 0.7, "page": 16, "window": 0, "dtype": "bf16", **heads},
+        # a chunk of a long prompt
+        {"name": "chunk 2048 over 32k", "op": "attention", "chunks": 1, "q_len": 2048, "decoders": 0, "kv": 32768,
+         "spread": 0.0, "page": 64, "window": 0, "dtype": "bf16", **heads},
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["table", "rope", "append", "decode", "decode", "chunk", "chunk"])
+    if op == "table":
+        return {"op": op, "rows": _log(rng, 512, 131072), "rot": 2 * rng.randint(16, 64),
+                "base": rng.choice([1e4, 5e5, 1e6]), "scaling": rng.choice(["none", "linear", "ntk", "yarn", "bands"]),
+                "factor": rng.choice([2.0, 4.0, 16.0]), "orig_len": rng.choice([2048, 8192])}
+    if op == "rope":
+        dim = rng.choice([64, 96, 128, 192, 256])
+        return {"op": op, "tokens": _log(rng, 1, 8192), "heads": rng.choice([1, 4, 8, 16, 32]), "dim": dim,
+                "rot": rng.choice([dim, dim, dim // 2, 20]), "layout": rng.choice(["half", "interleaved"]),
+                "inverse": rng.random() < 0.5, "dtype": rng.choice(["bf16", "f16", "f32"]), "fused": rng.random() < 0.5}
+    kv_heads = rng.choice([1, 2, 4, 8])
+    shape = {"heads": kv_heads * rng.choice([1, 2, 4, 7, 8]), "kv_heads": kv_heads,
+             "dim": rng.choice([64, 96, 128, 128, 192, 256]), "page": rng.choice([16, 32, 64, 128])}
+    if op == "append":
+        return {"op": op, "tokens": _log(rng, 1, 4096), "layout": rng.choice(["half", "interleaved"]),
+                "rot": rng.choice([shape["dim"], shape["dim"] // 2]), "dtype": rng.choice(["bf16", "f16", "f32"]),
+                "chunk": rng.random() < 0.5, **shape}
+    shape["dtype"] = rng.choice(["bf16", "bf16", "f16"])
+    shape["window"] = rng.choice([0, 0, 0, _log(rng, 64, 4096)])
+    shape["spread"] = rng.choice([0.0, 0.5, 0.9])
+    if op == "decode":
+        n = _log(rng, 1, 64)
+        return {"op": "attention", "chunks": 0, "q_len": 1, "decoders": n, "kv": _log(rng, 1, 131072 // n), **shape}
+    q = _log(rng, 2, 1024)
+    return {"op": "attention", "chunks": rng.randint(1, 3), "q_len": q, "decoders": rng.randint(0, 6),
+            "kv": _log(rng, q, 4096), **shape}
+
+
+# ------------------------------------------------------------------ sizes that a case stands for
+_DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def _lengths(c):
+    """New tokens and cached tokens (the new ones among them) of every request of an attention case."""
+    part = lambda b: 1.0 - c["spread"] * ((b * 0.6180339887) % 1.0)  # noqa: E731
+    q = [max(1, int(c["q_len"] * part(b))) for b in range(c["chunks"])] + [1] * c["decoders"]
+    return q, [max(n, int(c["kv"] * part(b))) for b, n in enumerate(q)]
+
+
+def _pairs(q, kv, window):
+    """Query-key pairs that the causal mask and the window leave."""
+    total = 0
+    for i in range(q):
+        seen = kv - q + i + 1
+        total += min(seen, window) if window else seen
+    return total
+
+
+def work(c):
+    if c["op"] == "table":
+        n = c["rows"] * c["rot"]
+        return {"bytes": 4 * n, "flops": 10 * n}
+    size = {"bf16": 2, "f16": 2, "f32": 4}[c["dtype"]]
+    if c["op"] == "rope":
+        n = c["tokens"] * c["heads"]
+        return {"bytes": 2 * n * c["dim"] * size + c["tokens"] * (4 + 4 * c["rot"]), "flops": 3 * n * c["rot"]}
+    if c["op"] == "append":
+        t, h, hk, d = c["tokens"], c["heads"], c["kv_heads"], c["dim"]
+        return {"bytes": t * (2 * h * d * size + 2 * hk * d * size + 2 * hk * (d + d // 32) + 12 + 4 * c["rot"]),
+                "flops": t * (h + hk) * c["rot"] * 3 + t * hk * d * 8}
+    q, kv = _lengths(c)
+    d, h, hk, w = c["dim"], c["heads"], c["kv_heads"], c["window"]
+    read = sum(min(n, w + m - 1) if w else n for m, n in zip(q, kv))
+    return {"bytes": 2 * read * hk * (d + d // 32) + 2 * sum(q) * h * d * size + 4 * sum(q) * h,
+            "flops": 4 * d * h * sum(_pairs(m, n, w) for m, n in zip(q, kv))}
+
+
+# ------------------------------------------------------------------ inputs
+def _gen(seed, device="cuda"):
+    g = torch.Generator(device=device)
+    g.manual_seed(seed * 7919 + 17)
+    return g
+
+
+def _table(rows, rot, base, device):
+    """cos / sin pairs [rows][rot / 2][2] of positions 0 .. rows - 1, as a program keeps them."""
+    f = torch.pow(torch.tensor(base, dtype=torch.float64, device=device),
+                  torch.arange(rot // 2, dtype=torch.float64, device=device) * (-2.0 / rot))
+    a = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * f
+    return torch.stack([a.cos(), a.sin()], -1).float()
+
+
+def _rows(gen, shape, dtype, spread=2.0):
+    """Activations: normal, with a scale of its own for every channel."""
+    ch = torch.exp2((torch.rand(shape[-1], generator=gen, device="cuda") - 0.5) * 2 * spread)
+    return (torch.randn(shape, generator=gen, device="cuda") * ch).to(dtype)
+
+
+def _encode(x):
+    """MX blocks of 32 along the last axis, round-up rule: E4M3 codes and E8M0 scale codes."""
+    b = x.float().unflatten(-1, (-1, 32))
+    amax = b.abs().amax(-1)
+    m, e = torch.frexp(amax)
+    e = (e - 9 + (m > 0.875).int()).clamp(-127, 127)
+    e = torch.where(amax > 0, e, -127)
+    codes = torch.ldexp(b, -e.unsqueeze(-1)).to(torch.float8_e4m3fn)
+    return codes.flatten(-2), (e + 127).to(torch.uint8)
+
+
+def _cache_of(k, v, page):
+    """Cache tensors that hold keys and values of all slots [slots][heads][dim], page after page."""
+    n, h, d = k.shape
+    kq, ks = _encode(k)
+    vq, vs = _encode(v)
+    lay = lambda t: t.view(torch.uint8).unflatten(0, (n // page, page)).transpose(1, 2)  # noqa: E731
+    return (lay(kq).contiguous(), lay(ks).contiguous(),
+            lay(vq).unflatten(2, (page // 16, 16)).transpose(3, 4).contiguous(),
+            lay(vs).unflatten(2, (page // 16, 16)).transpose(3, 4).contiguous())
+
+
+def prepare(c, seed):
+    g = _gen(seed)
+    dev = torch.device("cuda")
+    if c["op"] == "table":
+        # base and stretch are the user's numbers; a slightly different base for every seed
+        return {"c": c, "base": c["base"] * (1.0 + (seed % 1009) / 8192.0)}
+    if c["op"] == "rope":
+        t, h, d = c["tokens"], c["heads"], c["dim"]
+        x = _rows(g, (t, h + (4 if c["fused"] else 0), d), _DT[c["dtype"]])[:, :h]
+        rows = max(8192, t)
+        pos = (torch.arange(t, device=dev) + int(torch.randint(0, rows - t + 1, (1,), generator=g, device=dev))).int()
+        return {"c": c, "x": x, "pos": pos, "table": _table(rows, c["rot"], 1e4, dev)}
+    if c["op"] == "append":
+        t, h, hk, d, page = c["tokens"], c["heads"], c["kv_heads"], c["dim"], c["page"]
+        rows = 16384
+        qkv = _rows(g, (t, h + 2 * hk, d), _DT[c["dtype"]])          # one fused projection's output
+        pages = -(-t // page) + 1 if c["chunk"] else max(4, t)
+        order = torch.randperm(pages, generator=g, device=dev)
+        if c["chunk"]:      # consecutive tokens from some place inside a page on
+            start = int(torch.randint(0, page, (1,), generator=g, device=dev))
+            at = torch.arange(t, device=dev) + start
+            pos = at + 64 * int(torch.randint(0, 64, (1,), generator=g, device=dev))
+        else:               # one token of each request, each in a page of its own
+            at = torch.arange(t, device=dev) * page + torch.randint(0, page, (t,), generator=g, device=dev)
+            pos = torch.randint(0, rows, (t,), generator=g, device=dev)
+        slots = order[at // page] * page + at % page
+        cache = [torch.zeros(s, dtype=torch.uint8, device=dev) for s in (
+            (pages, hk, page, d), (pages, hk, page, d // 32), (pages, hk, page // 16, d, 16),
+            (pages, hk, page // 16, d // 32, 16))]
+        return {"c": c, "q": qkv[:, :h], "k": qkv[:, h:h + hk], "v": qkv[:, h + hk:], "slots": slots,
+                "pos": pos.int(), "table": _table(rows, c["rot"], 1e4, dev), "cache": tuple(cache)}
+    q, kv = _lengths(c)
+    page, hk, d = c["page"], c["kv_heads"], c["dim"]
+    need = [-(-n // page) for n in kv]
+    pages = sum(need) + 3
+    order = torch.randperm(pages, generator=g, device=dev).int()
+    table = torch.zeros((len(kv), max(need)), dtype=torch.int32, device=dev)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    # keys with a few strong channels, values plain
+    k = _rows(g, (pages * page, hk, d), torch.bfloat16, 1.5)
+    v = _rows(g, (pages * page, hk, d), torch.bfloat16, 0.5)
+    cache = _cache_of(k, v, page)
+    del k, v
+    x = _rows(g, (sum(q), c["heads"], d), _DT[c["dtype"]], 0.5)
+    cu = torch.tensor([sum(q[:b]) for b in range(len(q) + 1)], dtype=torch.int32, device=dev)
+    return {"c": c, "q": x, "cache": cache, "pages": table, "cu": cu, "max_q": max(q), "max_kv": max(kv),
+            "lens": torch.tensor(kv, dtype=torch.int32, device=dev)}
+
+
+# ------------------------------------------------------------------ plain forms
+def _freqs(rot, base, scaling, factor, orig_len, device):
+    """Angle per position of every pair, and the factor on cos and sin."""
+    i = torch.arange(rot // 2, dtype=torch.float64, device=device)
+    if scaling == "ntk":
+        base = base * factor ** (rot / (rot - 2))
+    f = torch.exp(i * (-2.0 / rot * math.log(base)))
+    if scaling == "linear":
+        f = f / factor
+    if scaling == "yarn":
+        turn = lambda n: rot * math.log(orig_len / (n * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+        lo, hi = max(math.floor(turn(32.0)), 0), min(math.ceil(turn(1.0)), rot - 1)
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        return f / factor * ramp + f * (1 - ramp), 0.1 * math.log(factor) + 1.0
+    if scaling == "bands":
+        s = ((orig_len * f / (2 * math.pi) - 1.0) / (4.0 - 1.0)).clamp(0, 1)
+        f = (1 - s) * f / factor + s * f
+    return f, 1.0
+
+
+def _rotated(x, pos, table, rot, layout, inverse):
+    """Rotation of the first `rot` channels, 32 bits."""
+    x = x.float()
+    cs = table[pos.long()][:, None]
+    cos, sin = cs[..., 0], cs[..., 1]
+    if inverse:
+        sin = -sin
+    head = x[..., :rot]
+    if layout == "half":
+        a, b = head[..., : rot // 2], head[..., rot // 2:]
+        y = torch.cat([a * cos - b * sin, b * cos + a * sin], -1)
+    else:
+        a, b = head[..., 0::2], head[..., 1::2]
+        y = torch.stack([a * cos - b * sin, b * cos + a * sin], -1).flatten(-2)
+    return torch.cat([y, x[..., rot:]], -1)
+
+
+def _values(codes, scales):
+    """What MX codes [..][dim] and scales [..][dim / 32] stand for."""
+    s = torch.ldexp(torch.ones((), device=codes.device), scales.int() - 127)
+    return (codes.view(torch.float8_e4m3fn).float().unflatten(-1, (-1, 32)) * s.unsqueeze(-1)).flatten(-2)
+
+
+def _as_values(cache):
+    return [t.view(torch.float8_e8m0fnu if i & 1 else torch.float8_e4m3fn) for i, t in enumerate(cache)]
+
+
+def _plain_append(s):
+    c = s["c"]
+    q = _rotated(s["q"], s["pos"], s["table"], c["rot"], c["layout"], False).to(s["q"].dtype)
+    k = _rotated(s["k"], s["pos"], s["table"], c["rot"], c["layout"], False)
+    kq, ks = _encode(k)
+    vq, vs = _encode(s["v"])
+    page, off = s["slots"] // c["page"], s["slots"] % c["page"]
+    kc, ksc, vc, vsc = s["cache"]
+    kc[page, :, off] = kq.view(torch.uint8)
+    ksc[page, :, off] = ks
+    vc[page, :, off // 16, :, off % 16] = vq.view(torch.uint8)
+    vsc[page, :, off // 16, :, off % 16] = vs
+    return [q, *_as_values(s["cache"])]
+
+
+def _gathered(s, to):
+    """Keys and values of every request, padded to the longest: [requests][kv heads][tokens][dim]."""
+    c = s["c"]
+    at = s["pages"].long()
+    kc, ksc, vc, vsc = s["cache"]
+    k = to(kc[at], ksc[at]).transpose(1, 2).flatten(2, 3)
+    v = to(vc[at].transpose(-1, -2), vsc[at].transpose(-1, -2)).transpose(1, 2).flatten(2, 4)
+    return k[:, :, : s["max_kv"]], v[:, :, : s["max_kv"]]
+
+
+def _seen(s, q_lens):
+    """Which key each padded query sees: [requests][queries][tokens]."""
+    dev = s["lens"].device
+    i = torch.arange(s["max_q"], device=dev)[None, :, None]
+    j = torch.arange(s["max_kv"], device=dev)[None, None, :]
+    p = (s["lens"] - q_lens)[:, None, None] + i
+    seen = (j <= p) & (i < q_lens[:, None, None]) & (p >= 0)
+    return seen & (j > p - s["c"]["window"]) if s["c"]["window"] else seen
+
+
+def _plain_attention(s):
+    c = s["c"]
+    k, v = _gathered(s, _values)
+    h, hk, d = c["heads"], c["kv_heads"], c["dim"]
+    q_lens = s["cu"][1:] - s["cu"][:-1]
+    i = torch.arange(s["max_q"], device=k.device)
+    real = i < q_lens[:, None]
+    at = (s["cu"][:-1, None] + torch.where(real, i, 0)).long()
+    x = s["q"][at].float().unflatten(2, (hk, h // hk)).permute(0, 2, 3, 1, 4)     # [r][kv head][group][queries][dim]
+    r, n = x.shape[0], h // hk * s["max_q"]
+    a = torch.matmul(x.reshape(r, hk, n, d), k.transpose(-1, -2).contiguous()).view(r, hk, h // hk, s["max_q"], -1)
+    a = a * (1.0 / math.sqrt(d))
+    a = a.masked_fill(~_seen(s, q_lens)[:, None, None], -math.inf)
+    top = a.amax(-1, keepdim=True)
+    top = torch.where(torch.isfinite(top), top, 0.0)
+    a = torch.exp(a - top)
+    total = a.sum(-1, keepdim=True)
+    o = torch.matmul(a.view(r, hk, n, -1), v.contiguous()).view(r, hk, h // hk, s["max_q"], d)
+    o = o / torch.where(total > 0, total, 1.0)
+    lse = (top + total.log()).squeeze(-1)
+    o = o.permute(0, 3, 1, 2, 4).flatten(2, 3)[real]
+    return [o.to(s["q"].dtype), lse.permute(0, 3, 1, 2).flatten(2, 3)[real]]
+
+
+# ------------------------------------------------------------------ the library's calls
+def _own_run(s):
+    import mx_block_scaled_quantize_amd as mxa
+    c = s["c"]
+    if c["op"] == "table":
+        return mxa.mx_rope_table(c["rows"], c["rot"], s["base"], c["scaling"], factor=c["factor"],
+                                 orig_len=c["orig_len"])
+    if c["op"] == "rope":
+        return mxa.mx_rope(s["x"], s["pos"], s["table"], layout=c["layout"], inverse=c["inverse"])
+    cache = mxa.KVCache(*s["cache"])
+    if c["op"] == "append":
+        q = mxa.mx_kv_append(s["k"], s["v"], cache, s["slots"], s["pos"], s["table"], layout=c["layout"], q=s["q"])
+        return [q, *_as_values(s["cache"])]
+    return list(mxa.mx_paged_attention(s["q"], cache, s["pages"], s["cu"], s["lens"], window=c["window"], lse=True,
+                                       max_q=s["max_q"], max_kv=s["max_kv"]))
+
+
+def run(s):
+    if own:
+        return _own_run(s)
+    c = s["c"]
+    if c["op"] == "table":
+        f, m = _freqs(c["rot"], s["base"], c["scaling"], c["factor"], c["orig_len"], "cuda")
+        a = torch.arange(c["rows"], dtype=torch.float64, device="cuda")[:, None] * f
+        return (torch.stack([a.cos(), a.sin()], -1) * m).float()
+    if c["op"] == "rope":
+        return _rotated(s["x"], s["pos"], s["table"], c["rot"], c["layout"], c["inverse"]).to(s["x"].dtype)
+    return _plain_append(s) if c["op"] == "append" else _plain_attention(s)
+
+
+# ------------------------------------------------------------------ 64 bits, from the definitions
+def _exact_table(c, base):
+    rot, rows = c["rot"], c["rows"]
+    f, m = [], 1.0
+    for i in range(rot // 2):
+        b = base
+        if c["scaling"] == "ntk":
+            b = base * c["factor"] ** (rot / (rot - 2.0))
+        x = b ** (-2.0 * i / rot)
+        if c["scaling"] == "linear":
+            x /= c["factor"]
+        elif c["scaling"] == "yarn":
+            # channels that turn more than 32 times over the original length stay, those that turn less than once
+            # are stretched, a straight ramp over the channel index between
+            of = lambda turns: rot * math.log(c["orig_len"] / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
+            lo, hi = max(math.floor(of(32)), 0), min(math.ceil(of(1)), rot - 1)
+            share = min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3)))
+            x = x * (1 - share) + x / c["factor"] * share
+            m = 1.0 + 0.1 * math.log(c["factor"])
+        elif c["scaling"] == "bands":
+            turns = c["orig_len"] * x / (2 * math.pi)
+            if turns < 1:
+                x = x / c["factor"]
+            elif turns <= 4:
+                keep = (turns - 1) / 3
+                x = keep * x + (1 - keep) * x / c["factor"]
+        f.append(x)
+    a = torch.arange(rows, device="cuda", dtype=torch.float64).outer(torch.tensor(f, dtype=torch.float64, device="cuda"))
+    return torch.polar(torch.full_like(a, m), a).view(torch.float64).view(rows, rot // 2, 2)
+
+
+def _exact_rotation(x, s, inverse):
+    """Channel pairs as complex numbers, times e^(i angle)."""
+    c = s["c"]
+    z = torch.view_as_complex(s["table"].double()[s["pos"].long()])[:, None]
+    z = z.conj() if inverse else z
+    x = x.double()
+    part, rest = x[..., : c["rot"]], x[..., c["rot"]:]
+    if c["layout"] == "interleaved":
+        y = torch.view_as_real(torch.view_as_complex(part.unflatten(-1, (-1, 2)).contiguous()) * z).flatten(-2)
+    else:
+        p = torch.view_as_complex(part.unflatten(-1, (2, -1)).transpose(-1, -2).contiguous())
+        y = torch.view_as_real(p * z).transpose(-1, -2).flatten(-2)
+    return torch.cat([y, rest], -1)
+
+
+def _exact_blocks(x):
+    """Element values and scale values of MX blocks, round-up rule: the smallest power of two whose 448-fold holds the block."""
+    b = x.double().reshape(*x.shape[:-1], -1, 32)
+    top = b.abs().amax(-1)
+    e = torch.ceil(torch.log2(top.clamp_min(1e-300) / 448.0))
+    e = torch.where(top > 448.0 * torch.exp2(e), e + 1, e)
+    e = torch.where(top <= 448.0 * torch.exp2(e - 1), e - 1, e).clamp(-127, 127)
+    e = torch.where(top > 0, e, -127.0)
+    y = b / torch.exp2(e).unsqueeze(-1)
+    # E4M3: 3 mantissa bits down to 2^-6, then steps of 2^-9; halves to even
+    step = torch.exp2(torch.floor(torch.log2(y.abs().clamp_min(2.0 ** -6))) - 3)
+    return (torch.round(y / step) * step).flatten(-2), torch.exp2(e)
+
+
+def _exact_append(s):
+    c = s["c"]
+    q = _exact_rotation(s["q"], s, False)
+    outs = []
+    for x in (_exact_rotation(s["k"], s, False), s["v"].double()):
+        outs += list(_exact_blocks(x))
+    pages, hk, page, d = s["cache"][0].shape
+    put = []
+    for n, (width, x) in enumerate(zip((d, d // 32, d, d // 32), outs)):
+        # a slot that holds nothing has code 0, value 0, and scale code 0, value 2^-127
+        t = torch.full((pages * page, hk, width), 2.0 ** -127 if n & 1 else 0.0, dtype=torch.float64, device="cuda")
+        t[s["slots"]] = x
+        t = t.view(pages, page, hk, width).transpose(1, 2)
+        put.append(t if n < 2 else t.reshape(pages, hk, page // 16, 16, width).transpose(3, 4))
+    return [q, *[t.contiguous() for t in put]]
+
+
+def _exact_attention(s):
+    c = s["c"]
+    d, h, hk, page = c["dim"], c["heads"], c["kv_heads"], c["page"]
+    q_lens, kv = _lengths(c)
+    kc, ksc, vc, vsc = s["cache"]
+    val = torch.arange(256, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).double()
+    two = torch.exp2(torch.arange(256, dtype=torch.float64, device="cuda") - 127)
+    out = torch.empty(sum(q_lens), h, d, dtype=torch.float64, device="cuda")
+    lse = torch.empty(sum(q_lens), h, dtype=torch.float64, device="cuda")
+    at = 0
+    for b, (m, n) in enumerate(zip(q_lens, kv)):
+        ids = s["pages"][b, : -(-n // page)].long()
+        first = max(0, n - m - c["window"] + 1) if c["window"] else 0
+        j = torch.arange(first, n, device="cuda")
+        for g in range(hk):
+            k = kc[ids, g].reshape(-1, d)[first:n]
+            k = val[k.int()] * two[ksc[ids, g].reshape(-1, d // 32)[first:n].int()].repeat_interleave(32, -1)
+            v = vc[ids, g].transpose(-1, -2).reshape(-1, d)[first:n]
+            w = vsc[ids, g].transpose(-1, -2).reshape(-1, d // 32)[first:n]
+            v = val[v.int()] * two[w.int()].repeat_interleave(32, -1)
+            for lo in range(0, m, 512):
+                hi = min(m, lo + 512)
+                p = n - m + torch.arange(lo, hi, device="cuda")
+                seen = j <= p[:, None]
+                if c["window"]:
+                    seen &= j > p[:, None] - c["window"]
+                for e in range(g * (h // hk), (g + 1) * (h // hk)):
+                    a = s["q"][at + lo:at + hi, e].double() @ k.T / math.sqrt(d)
+                    a = torch.where(seen, a, -math.inf)
+                    z = torch.logsumexp(a, -1)
+                    out[at + lo:at + hi, e] = torch.exp(a - z[:, None]) @ v
+                    lse[at + lo:at + hi, e] = z
+        at += m
+    return [out, lse]
+
+
+def exact(c, seed):
+    s = prepare(c, seed)
+    if c["op"] == "table":
+        return _exact_table(c, s["base"])
+    if c["op"] == "rope":
+        return _exact_rotation(s["x"], s, c["inverse"])
+    return _exact_append(s) if c["op"] == "append" else _exact_attention(s)
