@@ -6,8 +6,7 @@ the angles of far positions), or, where ``own`` is true, through the library's
 entry points.  The cache holds MXFP8 codes in blocks of 32 along the head
 dimension with one E8M0 scale each:
 
-    keys    codes [pages][heads][page][dim],         scales [pages][heads][page][dim / 32]
-    values  codes [pages][heads][page / 16][dim][16], scales [pages][heads][page / 16][dim / 32][16]
+    keys and values  codes [pages][heads][page][dim], scales [pages][heads][page][dim / 32]
 
 Codes are returned as float8 and scales as E8M0 tensors, the values they stand for.
 Sizes follow the transformer layers the library is benchmarked on: 32 query heads,
@@ -173,9 +172,7 @@ def _cache_of(k, v, page):
     kq, ks = _encode(k)
     vq, vs = _encode(v)
     lay = lambda t: t.view(torch.uint8).unflatten(0, (n // page, page)).transpose(1, 2)  # noqa: E731
-    return (lay(kq).contiguous(), lay(ks).contiguous(),
-            lay(vq).unflatten(2, (page // 16, 16)).transpose(3, 4).contiguous(),
-            lay(vs).unflatten(2, (page // 16, 16)).transpose(3, 4).contiguous())
+    return tuple(lay(t).contiguous() for t in (kq, ks, vq, vs))
 
 
 def prepare(c, seed):
@@ -204,9 +201,7 @@ def prepare(c, seed):
             at = torch.arange(t, device=dev) * page + torch.randint(0, page, (t,), generator=g, device=dev)
             pos = torch.randint(0, rows, (t,), generator=g, device=dev)
         slots = order[at // page] * page + at % page
-        cache = [torch.zeros(s, dtype=torch.uint8, device=dev) for s in (
-            (pages, hk, page, d), (pages, hk, page, d // 32), (pages, hk, page // 16, d, 16),
-            (pages, hk, page // 16, d // 32, 16))]
+        cache = [torch.zeros((pages, hk, page, n), dtype=torch.uint8, device=dev) for n in (d, d // 32, d, d // 32)]
         return {"c": c, "q": qkv[:, :h], "k": qkv[:, h:h + hk], "v": qkv[:, h + hk:], "slots": slots,
                 "pos": pos.int(), "table": _table(rows, c["rot"], 1e4, dev), "cache": tuple(cache)}
     q, kv = _lengths(c)
@@ -287,8 +282,8 @@ def _plain_append(s):
     kc, ksc, vc, vsc = s["cache"]
     kc[page, :, off] = kq.view(torch.uint8)
     ksc[page, :, off] = ks
-    vc[page, :, off // 16, :, off % 16] = vq.view(torch.uint8)
-    vsc[page, :, off // 16, :, off % 16] = vs
+    vc[page, :, off] = vq.view(torch.uint8)
+    vsc[page, :, off] = vs
     return [q, *_as_values(s["cache"])]
 
 
@@ -298,7 +293,7 @@ def _gathered(s, to):
     at = s["pages"].long()
     kc, ksc, vc, vsc = s["cache"]
     k = to(kc[at], ksc[at]).transpose(1, 2).flatten(2, 3)
-    v = to(vc[at].transpose(-1, -2), vsc[at].transpose(-1, -2)).transpose(1, 2).flatten(2, 4)
+    v = to(vc[at], vsc[at]).transpose(1, 2).flatten(2, 3)
     return k[:, :, : s["max_kv"]], v[:, :, : s["max_kv"]]
 
 
@@ -438,9 +433,8 @@ def _exact_append(s):
         # a slot that holds nothing has code 0, value 0, and scale code 0, value 2^-127
         t = torch.full((pages * page, hk, width), 2.0 ** -127 if n & 1 else 0.0, dtype=torch.float64, device="cuda")
         t[s["slots"]] = x
-        t = t.view(pages, page, hk, width).transpose(1, 2)
-        put.append(t if n < 2 else t.reshape(pages, hk, page // 16, 16, width).transpose(3, 4))
-    return [q, *[t.contiguous() for t in put]]
+        put.append(t.view(pages, page, hk, width).transpose(1, 2).contiguous())
+    return [q, *put]
 
 
 def _exact_attention(s):
@@ -460,8 +454,8 @@ def _exact_attention(s):
         for g in range(hk):
             k = kc[ids, g].reshape(-1, d)[first:n]
             k = val[k.int()] * two[ksc[ids, g].reshape(-1, d // 32)[first:n].int()].repeat_interleave(32, -1)
-            v = vc[ids, g].transpose(-1, -2).reshape(-1, d)[first:n]
-            w = vsc[ids, g].transpose(-1, -2).reshape(-1, d // 32)[first:n]
+            v = vc[ids, g].reshape(-1, d)[first:n]
+            w = vsc[ids, g].reshape(-1, d // 32)[first:n]
             v = val[v.int()] * two[w.int()].repeat_interleave(32, -1)
             for lo in range(0, m, 512):
                 hi = min(m, lo + 512)
