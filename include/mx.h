@@ -342,6 +342,126 @@ mx_status_t mm_fp8(const uint8_t* a, const uint8_t* b, mx_elem_t fmt, int64_t ba
                    int trans_a, int trans_b, const float* scale, const uint16_t* bias,
                    uint16_t* c, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions and attention over a paged MXFP8 key/value cache
+ *
+ * The cache keeps every token's key and value as MXFP8 (E4M3 elements, blocks of
+ * 32 along the head dimension, round-up scale rule; [UE8M0] MX definition
+ * paragraph), in pages of `page` tokens:
+ *   codes  [pages][kv_heads][page][dim], 16-byte aligned;
+ *   scales [pages][kv_heads][page][dim / 32].
+ * Slot s of the cache is token s % page of page s / page.  A request's tokens lie
+ * in the pages that its row of the page table lists, in order.
+ * dim is 64, 96, 128, 192 or 256; page a multiple of 16 in 16 .. 65536;
+ * pages * kv_heads * page <= 2^34 (else MX_ERR_SHAPE). */
+typedef struct {
+  uint8_t* k;          /* key codes    */
+  uint8_t* k_scales;
+  uint8_t* v;          /* value codes  */
+  uint8_t* v_scales;
+  int64_t pages;
+  int32_t kv_heads;
+  int32_t page;
+  int32_t dim;
+} mx_kv_cache_t;
+
+/* Which channels a rotation pairs: MX_ROPE_HALF pairs channel i with i + rot / 2,
+ * MX_ROPE_INTERLEAVED pairs 2i with 2i + 1 (i < rot / 2). */
+typedef enum { MX_ROPE_HALF = 0, MX_ROPE_INTERLEAVED = 1 } mx_rope_layout_t;
+
+/* How the frequencies f_i = base^(-2i / rot) are stretched for a context `factor`
+ * times longer than the `orig_len` tokens the model was trained on:
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   NTK     base replaced by base * factor^(rot / (rot - 2))
+ *   YARN    (1 - r_i) f_i + r_i f_i / factor with r_i = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *           d(n) = rot ln(orig_len / (2 pi n)) / (2 ln base), lo = max(floor d(32), 0),
+ *           hi = min(ceil d(1), rot - 1); cos and sin times m = 1 + ln(factor) / 10
+ *   BANDS   s_i f_i + (1 - s_i) f_i / factor with s_i = clamp((orig_len f_i / (2 pi) - 1) / 3, 0, 1) */
+typedef enum { MX_ROPE_NONE = 0, MX_ROPE_LINEAR = 1, MX_ROPE_NTK = 2, MX_ROPE_YARN = 3, MX_ROPE_BANDS = 4 } mx_rope_scaling_t;
+
+/* Rotary table: table[p][i] = m * (cos(p f_i), sin(p f_i)) for p < rows, i < rot / 2,
+ * FP32 pairs [rows][rot / 2][2] (8-byte aligned), angles and products in FP64, one
+ * rounding to FP32.  rot even, 2 .. 1024 (NTK: >= 4); rows <= 2^31; base finite > 1;
+ * factor finite >= 1 and orig_len >= 1 where the scaling uses them.
+ * Errors: MX_ERR_UNSUPPORTED (scaling), MX_ERR_SHAPE, MX_ERR_ARG, MX_ERR_NULL, MX_ERR_ALIGN. */
+mx_status_t mx_rope_table(int64_t rows, int rot, double base, mx_rope_scaling_t scaling, double factor,
+                          int64_t orig_len, float* table, hipStream_t stream);
+
+/* Rotation of the first `rot` of `dim` channels of every head by the table row of
+ * its token's position (c, s = table[pos[t]][i]):
+ *   (a, b) -> (a c - b s, b c + a s); inverse != 0: s negated, which is the
+ * transposed map and so the backward pass (table entries are not learned).
+ * FP32 products and sums, each rounded once, then one rounding to `dtype`; channels
+ * from rot on are copied.
+ *   x, y   [tokens][heads][dim] with the given strides in elements (channel stride
+ *          1); y may be x itself, and must not overlap it otherwise.
+ *   pos    int32 [tokens]; a position outside [0, rows) gives NaN in the rotated channels.
+ *   table  [rows][rot / 2][2], 16-byte aligned.
+ * rot even, 2 .. dim; dim <= 65536; any alignment of x and y that their type has.
+ * Errors: MX_ERR_UNSUPPORTED (dtype, layout), MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */
+mx_status_t mx_rope(const void* x, mx_dtype_t dtype, int64_t tokens, int heads, int dim, int64_t x_token_stride,
+                    int64_t x_head_stride, const int32_t* pos, const float* table, int64_t rows, int rot,
+                    mx_rope_layout_t layout, int inverse, void* y, int64_t y_token_stride, int64_t y_head_stride,
+                    hipStream_t stream);
+
+/* Appends tokens to the cache: k rotated as by mx_rope (kept in FP32) and encoded,
+ * v encoded, both stored at slots[t], exactly the codes and scales that mx_quantize
+ * (E4M3, round-up) gives for those FP32 values; and, when q is given, q rotated into
+ * q_out, all in one launch.
+ *   q        [tokens][heads][dim] or NULL (then heads, q strides and q_out are ignored);
+ *   k, v     [tokens][kv_heads][dim]; strides in elements, channel stride 1.
+ *   slots    int64 [tokens]; a slot outside [0, pages * page) is not stored (padding
+ *            tokens carry -1).  Two tokens of one call must not share a slot.
+ *   pos      int32 [tokens], table [rows][rot / 2][2] as for mx_rope; table NULL: no
+ *            rotation (q must be NULL, pos is ignored).
+ *   q_out    [tokens][heads][dim] contiguous.
+ * Errors: as mx_rope; MX_ERR_SHAPE for a cache shape that is not offered. */
+mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dtype, int64_t tokens, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         const mx_kv_cache_t* cache, const int64_t* slots, const int32_t* pos, const float* table,
+                         int64_t rows, int rot, mx_rope_layout_t layout, const void* q, int heads,
+                         int64_t q_token_stride, int64_t q_head_stride, void* q_out, hipStream_t stream);
+
+/* Attention of new tokens over the paged cache.  Request r has the query tokens
+ * cu[r] .. cu[r + 1] - 1 and lens[r] cached tokens, its new ones among them (the last
+ * ones), so query i of m stands at p = lens[r] - m + i and sees the cached tokens
+ * j <= p (window > 0: and j > p - window).  With c = scale and kv head h / (heads / kv_heads):
+ *   o = sum_j exp(c q.k_j - lse) v_j,   lse = ln sum_j exp(c q.k_j)
+ * A query that sees nothing gives o = 0 and lse = -inf.  m = 1 is a decoding step; one
+ * call may mix requests that decode with chunks of prompts.
+ *   q      [tokens][heads][dim] BF16 or F16, 16-byte aligned rows (strides multiples of
+ *          8 elements); heads a multiple of kv_heads.
+ *   page_table  int32 [requests][table_cols], row stride table_stride; entries past a
+ *          request's length, or before its window, are not read.  A query that sees a
+ *          token whose page number is outside [0, pages) or whose place is past
+ *          table_cols gives NaN.
+ *   cu     int32 [requests + 1], non-decreasing; tokens outside every request keep
+ *          what out and lse held.
+ *   max_q, max_kv  upper bounds of cu[r + 1] - cu[r] and lens[r] (host values: they
+ *          size the grid).  A request that exceeds one of them gives NaN.
+ *   out    [tokens][heads][dim] contiguous, type of q, 16-byte aligned; lse FP32
+ *          [tokens][heads] or NULL.
+ *   workspace  mx_paged_attention_workspace bytes (16-byte aligned; may be NULL when that is 0);
+ *          its contents need no preparation and are not kept between calls.
+ * Scores, softmax sums and outputs are accumulated in FP32; the softmax weights are
+ * rounded to the type of q before the product with the values.  The cache's elements
+ * are decoded to that type, exactly but for its range: with F16 queries, cached
+ * magnitudes that round to 2^16 are infinite and those below 2^-24 fade out.  The
+ * order of all sums is fixed by the arguments.
+ * Errors: MX_ERR_UNSUPPORTED (dtype), MX_ERR_SHAPE (also a workspace too small), MX_ERR_ARG (scale not finite > 0,
+ * window, max_q or max_kv negative), MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */
+mx_status_t mx_paged_attention(const void* q, mx_dtype_t dtype, int64_t tokens, int heads, int64_t q_token_stride,
+                               int64_t q_head_stride, const mx_kv_cache_t* cache, const int32_t* page_table,
+                               int64_t table_stride, int64_t table_cols, const int32_t* cu, const int32_t* lens,
+                               int64_t requests, int64_t max_q, int64_t max_kv, int64_t window, float scale,
+                               void* out, float* lse, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that mx_paged_attention needs for these arguments, in *bytes.
+ * Errors: those of the same arguments there; MX_ERR_LAUNCH when no device can be queried. */
+mx_status_t mx_paged_attention_workspace(int64_t tokens, int heads, int kv_heads, int dim, int64_t requests,
+                                         int64_t max_q, int64_t max_kv, int64_t window, int64_t* bytes);
+
 /* Human-readable name of a status code (static storage). */
 const char* mx_status_str(mx_status_t status);
 

@@ -18,6 +18,12 @@ The functions carry the names of the C entry points declared in
     mx_quantize_sr(x, rand, rule, amax=False)
     mm_fp8(a, b, scale, trans_a, trans_b, bias, fmt)
     mx_gemm_requant(a, sa, b, sb, fmt_a, fmt_b, alpha, fmt_c, rule_c, amax=False, scale_layout="row")
+    mx_rope_table(rows, rot, base, scaling, factor, orig_len)
+    mx_rope(x, pos, table, layout, inverse, out)
+    mx_kv_append(k, v, cache, slots, pos, table, layout, q, q_out)
+    mx_paged_attention(q, cache, page_table, cu, lens, window, scale, lse, max_q, max_kv)
+
+KVCache (from new_kv_cache) is the paged MXFP8 key/value cache of the last two.
 
 scale_layout "row" stores E8M0 scales row-major [lines][K/32]; "gemm" stores them
 in the GEMM layout [K/512][lines][16] (returned as a 3-D tensor of that shape).
@@ -25,6 +31,7 @@ in the GEMM layout [K/512][lines][16] (returned as a 3-D tensor of that shape).
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -46,6 +53,8 @@ RULE = {"floor": 0, "ceil": 1}
 ORIENT = {"row": 0, "col": 1}
 SCALE_LAYOUT = {"row": 0, "gemm": 1}
 LAYOUT = {"row": 0, "transposed": 1, "dual": 2}
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 STATUS = {0: "MX_OK", 1: "MX_ERR_NULL", 2: "MX_ERR_SHAPE", 3: "MX_ERR_ALIGN", 4: "MX_ERR_UNSUPPORTED",
           5: "MX_ERR_LAUNCH", 6: "MX_ERR_ARG"}
 DEFAULT_FP8_MAX = {"e4m3": 448.0, "e5m2": 57344.0}
@@ -67,15 +76,34 @@ lib.mm_fp8.argtypes = [_p, _p, _i32, _i64, _i64, _i64, _i64, _i32, _i32, _i32, _
 lib.fp8_quantize_delayed_static.argtypes = [_p, _i32, _i64, _i64, _i32, _i32, _p, _p, _p, _i32, _i32, _f32, _f32, _p,
                                             _p]
 lib.mx_gemm_requant.argtypes = [_p, _p, _i32, _p, _p, _i32, _i32, _i64, _i64, _i64, _f32, _i32, _i32, _p, _p, _p, _p]
+_f64 = ctypes.c_double
+
+
+class _KVCacheArgs(ctypes.Structure):
+    """mx_kv_cache_t"""
+    _fields_ = [("k", _p), ("k_scales", _p), ("v", _p), ("v_scales", _p), ("pages", _i64), ("kv_heads", _i32),
+                ("page", _i32), ("dim", _i32)]
+
+
+_cache_p = ctypes.POINTER(_KVCacheArgs)
+lib.mx_rope_table.argtypes = [_i64, _i32, _f64, _i32, _f64, _i64, _p, _p]
+lib.mx_rope.argtypes = [_p, _i32, _i64, _i32, _i32, _i64, _i64, _p, _p, _i64, _i32, _i32, _i32, _p, _i64, _i64, _p]
+lib.mx_kv_append.argtypes = [_p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _cache_p, _p, _p, _p, _i64, _i32, _i32, _p, _i32,
+                             _i64, _i64, _p, _p]
+lib.mx_paged_attention.argtypes = [_p, _i32, _i64, _i32, _i64, _i64, _cache_p, _p, _i64, _i64, _p, _p, _i64, _i64, _i64,
+                                   _i64, _f32, _p, _p, _p, _i64, _p]
+lib.mx_paged_attention_workspace.argtypes = [_i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, ctypes.POINTER(_i64)]
 for _f in (lib.mx_quantize, lib.mx_quantize_dual, lib.fp8_quantize_delayed, lib.mx_dequantize, lib.mx_gemm,
-           lib.mx_quantize_sr, lib.mm_fp8, lib.mx_gemm_requant, lib.fp8_quantize_delayed_static):
+           lib.mx_quantize_sr, lib.mm_fp8, lib.mx_gemm_requant, lib.fp8_quantize_delayed_static, lib.mx_rope_table,
+           lib.mx_rope, lib.mx_kv_append, lib.mx_paged_attention, lib.mx_paged_attention_workspace):
     _f.restype = ctypes.c_int
 lib.mx_status_str.argtypes = [ctypes.c_int]
 lib.mx_status_str.restype = ctypes.c_char_p
 lib.mx_abi_version.restype = ctypes.c_int
 
 ENTRY_POINTS = ("mx_quantize", "mx_quantize_dual", "fp8_quantize_delayed", "mx_dequantize", "mx_gemm",
-                "mx_quantize_sr", "mm_fp8", "mx_gemm_requant", "fp8_quantize_delayed_static", "mx_status_str",
+                "mx_quantize_sr", "mm_fp8", "mx_gemm_requant", "fp8_quantize_delayed_static", "mx_rope_table",
+                "mx_rope", "mx_kv_append", "mx_paged_attention", "mx_paged_attention_workspace", "mx_status_str",
                 "mx_abi_version")
 
 
@@ -359,3 +387,188 @@ def mm_fp8(a, b, scale, trans_a=False, trans_b=False, bias=None, fmt=None):
     check(lib.mm_fp8(_ptr(a), _ptr(b), FMT[f], batch, M, N, K, int(ba > 1), int(bb > 1), int(ka), int(kb),
                      _ptr(scale), _ptr(bias), _ptr(out), _stream(a)))
     return out
+
+
+# ---------------------------------------------------------------- rotary positions, paged MXFP8 key/value cache
+class KVCache(NamedTuple):
+    """Paged MXFP8 keys and values (uint8 tensors, see mx_kv_cache_t):
+    codes [pages][kv_heads][page][dim], scales [pages][kv_heads][page][dim / 32]."""
+    k: torch.Tensor
+    k_scales: torch.Tensor
+    v: torch.Tensor
+    v_scales: torch.Tensor
+
+
+def new_kv_cache(pages: int, kv_heads: int, page: int, dim: int, device="cuda") -> KVCache:
+    """A zeroed cache of ``pages`` pages of ``page`` tokens."""
+    return KVCache(*(torch.zeros((pages, kv_heads, page, n), dtype=torch.uint8, device=device)
+                     for n in (dim, dim // 32, dim, dim // 32)))
+
+
+def _cache_args(cache, device):
+    k, ks, v, vs = cache
+    if k.dim() != 4:
+        raise ValueError("cache codes must be [pages][kv_heads][page][dim]")
+    pages, heads, page, dim = k.shape
+    scales = (pages, heads, page, dim // 32)
+    if v.shape != k.shape or ks.shape != scales or vs.shape != scales:
+        raise ValueError("cache tensors must be codes [pages][kv_heads][page][dim] and scales [..][dim / 32]")
+    for t in cache:
+        if t.dtype is not torch.uint8 or not t.is_contiguous() or t.device != device:
+            raise ValueError("cache tensors must be contiguous uint8 tensors on the device of the other arguments")
+    return _KVCacheArgs(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), pages, heads, page, dim)
+
+
+def _heads_3d(x, name, device):
+    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
+        raise ValueError(f"{name} must be [tokens][heads][dim] with contiguous channels")
+    if x.device != device:
+        raise ValueError(f"{name} must be on the device of the other arguments")
+
+
+def _vector(x, name, dtype, n, device):
+    if x.dtype is not dtype or x.dim() != 1 or x.shape[0] != n or not x.is_contiguous() or x.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n} on the device of the other arguments")
+
+
+def _rope_rows(table, device):
+    """(rows, rot) of a rotary table."""
+    if table.dtype is not torch.float32 or table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous() \
+            or table.device != device:
+        raise ValueError("table must be a contiguous float32 tensor [rows][rot / 2][2] on the device of the other arguments")
+    return table.shape[0], 2 * table.shape[1]
+
+
+def _on_device(t):
+    """The library launches on the current device: make it the tensors' own."""
+    if not t.is_cuda:
+        raise ValueError("libmx works on device tensors only")
+    return torch.cuda.device(t.device)
+
+
+def mx_rope_table(rows, rot, base=1e4, scaling="none", factor=1.0, orig_len=0, device="cuda"):
+    """Rotary table [rows][rot / 2][2] of float32 (cos, sin) pairs of positions 0 .. rows - 1.
+
+    scaling stretches the frequencies by ``factor`` over a model trained on ``orig_len``
+    tokens: "none", "linear", "ntk" (larger base), "yarn" (ramp over the channels, magnitude
+    1 + ln(factor) / 10) or "bands" (ramp over the turns that a channel makes in orig_len)."""
+    kind = _lookup(ROPE_SCALING, scaling, "rotary scaling")
+    if rows < 0 or rot < 2 or rot % 2:
+        raise MXValueError(2)
+    out = torch.empty((rows, rot // 2, 2), dtype=torch.float32, device=device)
+    with _on_device(out):
+        check(lib.mx_rope_table(rows, rot, float(base), kind, float(factor), int(orig_len), _ptr(out), _stream(out)))
+    return out
+
+
+def mx_rope(x, pos, table, layout="half", inverse=False, out=None):
+    """x [tokens][heads][dim] (float32, bfloat16 or float16, any strides but the channels') with
+    its first rot channels turned by the table rows of pos (int32 [tokens]).
+
+    layout "half" pairs channel i with i + rot / 2, "interleaved" 2i with 2i + 1.  inverse=True
+    turns back, which is also the backward pass: grad_x = mx_rope(grad_y, pos, table, layout,
+    inverse=True).  out may be x itself (in place)."""
+    lay = _lookup(ROPE_LAYOUT, layout, "rotary layout")
+    dt = _lookup(DTYPE, x.dtype, "dtype")
+    _heads_3d(x, "x", x.device)
+    tokens, heads, dim = x.shape
+    rows, rot = _rope_rows(table, x.device)
+    _vector(pos, "pos", torch.int32, tokens, x.device)
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
+    else:
+        _heads_3d(out, "out", x.device)
+        if out.shape != x.shape or out.dtype != x.dtype:
+            raise ValueError("out must have the shape and dtype of x")
+    with _on_device(x):
+        check(lib.mx_rope(x.data_ptr(), dt, tokens, heads, dim, x.stride(0), x.stride(1), pos.data_ptr(),
+                          table.data_ptr(), rows, rot, lay, int(bool(inverse)), out.data_ptr(), out.stride(0),
+                          out.stride(1), _stream(x)))
+    return out
+
+
+def mx_kv_append(k, v, cache, slots, pos=None, table=None, layout="half", q=None, q_out=None):
+    """Stores tokens in the cache: k rotated (if table is given) and MXFP8-encoded, v encoded, at
+    slots (int64 [tokens]; slot s is token s % page of page s // page, a slot outside the cache is
+    skipped).  With q (table needed) returns q rotated, [tokens][heads][dim], from the same launch."""
+    lay = _lookup(ROPE_LAYOUT, layout, "rotary layout")
+    dt = _lookup(DTYPE, k.dtype, "dtype")
+    dev = k.device
+    args = _cache_args(cache, dev)
+    _heads_3d(k, "k", dev)
+    _heads_3d(v, "v", dev)
+    tokens = k.shape[0]
+    if v.shape != k.shape or v.dtype != k.dtype or k.shape[1] != args.kv_heads or k.shape[2] != args.dim:
+        raise ValueError("k and v must be [tokens][kv_heads][dim] of one dtype, matching the cache")
+    _vector(slots, "slots", torch.int64, tokens, dev)
+    rows, rot = 0, 2
+    if table is not None:
+        rows, rot = _rope_rows(table, dev)
+        if pos is None:
+            raise ValueError("a rotation needs pos")
+        _vector(pos, "pos", torch.int32, tokens, dev)
+    heads, qt, qh = 0, 0, 0
+    if q is not None:
+        _heads_3d(q, "q", dev)
+        if table is None:
+            raise ValueError("q is only rotated: it needs a table")
+        if q.shape[0] != tokens or q.shape[2] != args.dim or q.dtype != k.dtype:
+            raise ValueError("q must be [tokens][heads][dim] with the dtype of k")
+        heads, qt, qh = q.shape[1], q.stride(0), q.stride(1)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous() or q_out.device != dev:
+            raise ValueError("q_out must be contiguous with the shape, dtype and device of q")
+    with _on_device(k):
+        check(lib.mx_kv_append(k.data_ptr(), v.data_ptr(), dt, tokens, k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                               args, slots.data_ptr(), None if table is None else pos.data_ptr(), _ptr(table), rows, rot,
+                               lay, _ptr(q), heads, qt, qh, None if q is None else q_out.data_ptr(), _stream(k)))
+    return None if q is None else q_out
+
+
+def mx_paged_attention(q, cache, page_table, cu, lens, window=0, scale=None, lse=False, max_q=None, max_kv=None,
+                       out=None):
+    """Causal attention of new tokens over a paged MXFP8 cache that already holds them.
+
+    q           [tokens][heads][dim] bfloat16 or float16; the query tokens of all requests in a row
+    page_table  int32 [requests][pages a request may have]
+    cu          int32 [requests + 1]: request r has the query tokens cu[r] .. cu[r + 1] - 1
+    lens        int32 [requests]: cached tokens of a request, its new ones (the last) among them
+    window      > 0: a query sees only the last ``window`` tokens up to its own
+    scale       factor on q.k, 1 / sqrt(dim) by default
+    max_q, max_kv  upper bounds of the query and cached tokens of a request.  Left out, they are
+                read from cu and lens, which waits for the GPU: give them in serving loops.
+    Returns out [tokens][heads][dim], or (out, lse [tokens][heads] float32).  Queries that see
+    nothing give 0 and -inf."""
+    dt = _lookup(DTYPE, q.dtype, "dtype")
+    dev = q.device
+    args = _cache_args(cache, dev)
+    _heads_3d(q, "q", dev)
+    tokens, heads, dim = q.shape
+    if dim != args.dim or heads % args.kv_heads:
+        raise ValueError("q must have the cache's dim and a multiple of its heads")
+    requests = lens.shape[0] if lens.dim() == 1 else -1
+    _vector(lens, "lens", torch.int32, requests, dev)
+    _vector(cu, "cu", torch.int32, requests + 1, dev)
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != requests \
+            or (page_table.stride(1) != 1 and page_table.shape[1] > 1) or page_table.device != dev:
+        raise ValueError("page_table must be an int32 tensor [requests][pages] with contiguous rows")
+    if max_q is None:
+        max_q = int((cu[1:] - cu[:-1]).max()) if requests else 0
+    if max_kv is None:
+        max_kv = int(lens.max()) if requests else 0
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be contiguous with the shape, dtype and device of q")
+    stats = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if lse else None
+    with _on_device(q):
+        need = _i64(0)
+        check(lib.mx_paged_attention_workspace(tokens, heads, args.kv_heads, dim, requests, max_q, max_kv, window, need))
+        space = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+        check(lib.mx_paged_attention(q.data_ptr(), dt, tokens, heads, q.stride(0), q.stride(1), args,
+                                     page_table.data_ptr(), page_table.stride(0), page_table.shape[1], cu.data_ptr(),
+                                     lens.data_ptr(), requests, max_q, max_kv, window,
+                                     dim ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(stats), _ptr(space),
+                                     need.value, _stream(q)))
+    return (out, stats) if lse else out

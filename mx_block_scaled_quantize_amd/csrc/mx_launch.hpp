@@ -39,6 +39,16 @@ inline mx_status_t check_common_quant(mx_dtype_t in, int64_t rows, int64_t cols,
   return MX_OK;
 }
 
+// Shape of a paged key/value cache (its pointers are checked where they are used).
+inline mx_status_t check_kv_cache(const mx_kv_cache_t& c) {
+  if (c.dim != 64 && c.dim != 96 && c.dim != 128 && c.dim != 192 && c.dim != 256) return MX_ERR_SHAPE;
+  if (c.page < 16 || c.page > 65536 || c.page % 16) return MX_ERR_SHAPE;
+  if (c.kv_heads < 1 || c.kv_heads > 65536 || c.pages < 0) return MX_ERR_SHAPE;
+  // groups of 16 rows are counted in 32 bits
+  if (c.pages > (int64_t(1) << 34) / (int64_t(c.kv_heads) * c.page)) return MX_ERR_SHAPE;
+  return MX_OK;
+}
+
 // Row-wise MXFP6 quantization (quantize_fp6.hip), reached from mx_quantize.
 mx_status_t fp6_quantize(const void* x, mx_dtype_t in, int64_t rows, int64_t cols, int block, mx_elem_t fmt,
                          mx_scale_rule_t rule, mx_orient_t orient, int hadamard, uint8_t* q, uint8_t* scales,

@@ -21,6 +21,8 @@ The oracle is plain, slow and exact:
   dequantized operands (the fake-quant emulation the MX studies use), and the
   per-tensor FP8 GEMM (op(a) @ op(b) * scale + bias, batch-broadcast).
 * ``sr``       - stochastic-rounding MXFP4 with caller-supplied random words.
+* ``attention`` - rotary tables and rotation, the append to a paged MXFP8 key/value
+  cache and attention over it.
 
 Sources (cited by page and section, see each function):
   [UE8M0]  "EU8M0 FP8 ... domestic compute chips" article (ag-981.com, news 240):
@@ -45,4 +47,4 @@ hand-written literal bytes, and a planted high-nibble-first (FP4) or
 big-endian (FP6) packer must fail those pins.
 """
 
-from . import formats, mx, delayed, hadamard, gemm, sr  # noqa: F401
+from . import formats, mx, delayed, hadamard, gemm, sr, attention  # noqa: F401
