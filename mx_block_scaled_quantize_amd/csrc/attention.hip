@@ -34,6 +34,7 @@
 namespace mxk {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f_t __attribute__((ext_vector_type(16)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h_t __attribute__((ext_vector_type(2)));
@@ -45,6 +46,9 @@ constexpr float kSlack = 8.0f;
 // F16 weights are kept 2^7 above the usual [0, 1], so that weights down to 2^-31 of the largest
 // are not lost below F16's smallest subnormal; with the slack they stay under 2^15.
 template <int DT> constexpr float kLift = DT == IN_F16 ? 7.0f : 0.0f;
+
+// Requests of up to so many rows (tokens x group) go to attention_kernel, whose waves split the keys.
+constexpr int kFewRows = 32;
 
 struct AttnArgs {
   const void* q;
@@ -64,6 +68,7 @@ struct AttnArgs {
   int window;                   // 0: none
   int row_tiles, splits, chunk; // keys of a split, a multiple of 32
   float c;                      // scale * log2(e)
+  bool few_only;                // requests of more than kFewRows rows are left to attention_tile_kernel
 };
 
 template <int DT>
@@ -104,21 +109,67 @@ __device__ __forceinline__ uint32_t any_nan_code(uint32_t w) {   // nonzero if a
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
-// What a workgroup works on.
-struct Span {
-  int64_t token0;               // first query token of the request
-  int m, kv;                    // its new and its cached tokens
-  int lo, hi;                   // keys that some row of the workgroup's row tile sees
-  bool bad;                     // the request exceeds what the caller announced
-};
+// Row group (16 rows of one page and head) of keys key .. key + 15: -1 where no row sees them (not
+// read), -2 where the page number or its place is out of range.
+__device__ __forceinline__ int row_group(const AttnArgs& g, const int32_t* __restrict__ table, int hk, int key, int lo,
+                                         int hi) {
+  if (key >= hi || key + 16 <= lo) return -1;
+  const int col = key / g.page;
+  if (col >= g.table_cols) return -2;
+  const int32_t p = table[col];
+  if (p < 0 || p >= g.pages) return -2;
+  return int((int64_t(p) * g.kv_heads + hk) * (g.page / 16) + (key - col * g.page) / 16);
+}
 
-template <int DT, int D, int NQ, int NW, bool ROWS>
+// NaN for all rows of one kv head of a request that exceeds what the caller announced.
+template <int DT, int D>
+__device__ __forceinline__ void refuse_request(const AttnArgs& g, int64_t t0, int64_t rows, int hk, int rt, int split) {
+  if (rt != 0) return;
+  const float nan = __uint_as_float(0x7FC00000u);
+  for (int64_t i = threadIdx.x; i < rows; i += blockDim.x) {
+    const int64_t row = (t0 + i / g.group) * g.heads + hk * g.group + i % g.group;
+    if (g.splits > 1) {
+      g.part_ml[(row * g.splits + split) * 2] = split ? kLowest : 0.0f;
+      g.part_ml[(row * g.splits + split) * 2 + 1] = split ? 0.0f : nan;
+    } else {
+      for (int d = 0; d < D; ++d) static_cast<uint16_t*>(g.out)[row * D + d] = DT == IN_BF16 ? 0x7FC0u : 0x7E00u;
+      if (g.lse) g.lse[row] = nan;
+    }
+  }
+}
+
+// A split without keys adds nothing to rows [row0, row1).
+__device__ __forceinline__ void empty_split(const AttnArgs& g, int64_t t0, int64_t row0, int64_t row1, int hk, int split) {
+  for (int64_t i = row0 + threadIdx.x; i < row1; i += blockDim.x) {
+    const int64_t row = (t0 + i / g.group) * g.heads + hk * g.group + i % g.group;
+    g.part_ml[(row * g.splits + split) * 2] = kLowest;
+    g.part_ml[(row * g.splits + split) * 2 + 1] = 0.0f;
+  }
+}
+
+// Log-sum-exp of reference exponent m and sum l.
+__device__ __forceinline__ float log_sum(float m, float l) {
+  const float inf = __builtin_inff();
+  return l == 0.0f ? -inf : m == inf ? inf : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+}
+
+template <int DT>
+__device__ __forceinline__ void put_stats(const AttnArgs& g, int64_t row, int split, float m, float l) {
+  if (g.splits > 1) {
+    g.part_ml[(row * g.splits + split) * 2] = m;
+    g.part_ml[(row * g.splits + split) * 2 + 1] = l;
+  } else if (g.lse) {
+    g.lse[row] = log_sum(m, l);
+  }
+}
+
+template <int DT, int D, int NQ, int NW>
 __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
   using L = Deal<D>;
   constexpr int kFrags = D / 32;                 // K steps of S^T
   constexpr int kTiles = D / 16;                 // 16-channel tiles of O^T
   constexpr int kKS = (D + 63) / 64;             // scale bytes of a key a lane needs
-  constexpr int kRows = NQ * 16 * (ROWS ? NW : 1);
+  constexpr int kRows = NQ * 16;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r = lane & 15, quarter = lane >> 4;
 
@@ -136,20 +187,9 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
   const int m = int(t1 - t0), kv = max(g.lens[req], 0);
   const int64_t rows = int64_t(m) * G, row0 = int64_t(rt) * kRows;
   using T = uint16_t;
+  if (g.few_only && rows > kFewRows) return;     // attention_tile_kernel's
   if (m > g.max_q || kv > g.max_kv) {            // not what the grid was sized for
-    if (rt == 0 && (split == 0 || g.splits > 1)) {
-      const float nan = __uint_as_float(0x7FC00000u);
-      for (int64_t i = threadIdx.x; i < rows; i += 64 * NW) {
-        const int64_t row = (t0 + i / G) * g.heads + hk * G + i % G;
-        if (g.splits > 1) {
-          g.part_ml[(row * g.splits + split) * 2] = split ? kLowest : 0.0f;
-          g.part_ml[(row * g.splits + split) * 2 + 1] = split ? 0.0f : nan;
-        } else {
-          for (int d = 0; d < D; ++d) static_cast<T*>(g.out)[row * D + d] = T(DT == IN_BF16 ? 0x7FC0u : 0x7E00u);
-          if (g.lse) g.lse[row] = nan;
-        }
-      }
-    }
+    refuse_request<DT, D>(g, t0, rows, hk, rt, split);
     return;
   }
   if (row0 >= rows) return;
@@ -158,25 +198,20 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
   const int hi_all = max(kv - m + i1 + 1, 0);
   const int lo = g.window ? max(kv - m + i0 - g.window + 1, 0) : 0;
   const int64_t start64 = int64_t(lo & ~31) + int64_t(split) * g.chunk;
-  if (split > 0 && start64 >= hi_all) {          // a split without keys: nothing to add
-    for (int64_t i = row0 + threadIdx.x; i < min(row0 + kRows, rows); i += 64 * NW) {
-      const int64_t row = (t0 + i / G) * g.heads + hk * G + i % G;
-      g.part_ml[(row * g.splits + split) * 2] = kLowest;
-      g.part_ml[(row * g.splits + split) * 2 + 1] = 0.0f;
-    }
+  if (split > 0 && start64 >= hi_all) {
+    empty_split(g, t0, row0, min(row0 + kRows, rows), hk, split);
     return;
   }
   const int start = int(start64), hi = int(min(int64_t(hi_all), start64 + g.chunk));
 
   // this lane's rows: where q is, and the keys (first, last] a row sees
-  const int64_t wrow0 = row0 + (ROWS ? wave * NQ * 16 : 0);
   int last[NQ], first[NQ];
   int64_t orow[NQ];
   u32x4_t qf[NQ][kFrags];
   int wlast_min = 0x7FFFFFFF, wfirst_max = 0;    // what every row of the wave sees
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const int64_t row = wrow0 + n * 16 + r;
+    const int64_t row = row0 + n * 16 + r;
     const bool real = row < rows;
     const int64_t rr = real ? row : rows - 1;
     const int i = int(rr / G);
@@ -213,22 +248,9 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
     uint32_t k[2][kFrags * 2], ks[2][kKS];
     uint32_t v[8][L::kWords], vs[8][L::kScales];
   } raw;
-  // row group (16 rows of one page and head) of keys 16 i .. 16 i + 15 of the current window of
-  // 1024 keys, held by lane i; -1: not read (no row sees them), -2: a page number out of range
+  // row group of keys 16 i .. 16 i + 15 of the current window of 1024 keys, held by lane i
   int groups = -1;
   const int32_t* table = g.table + req * g.table_stride;
-  auto refill = [&](int window0) {
-    const int key = window0 + lane * 16;
-    groups = -1;
-    if (key < hi && key + 16 > lo) {
-      const int col = key / g.page;
-      groups = -2;
-      if (col < g.table_cols) {
-        const int32_t p = table[col];
-        if (p >= 0 && p < g.pages) groups = int((int64_t(p) * g.kv_heads + hk) * (g.page / 16) + (key - col * g.page) / 16);
-      }
-    }
-  };
   auto load = [&](int step) {      // step: 32-key step within the window
     const int ga = __builtin_amdgcn_readlane(groups, 2 * step), gb = __builtin_amdgcn_readlane(groups, 2 * step + 1);
     if ((ga & gb) >= 0) {          // a group that is not read borrows the other's addresses
@@ -449,11 +471,10 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
     });
   };
 
-  constexpr int kStride = ROWS ? 1 : NW;
   for (int window0 = start; window0 < hi; window0 += 1024) {
-    refill(window0);
+    groups = row_group(g, table, hk, window0 + lane * 16, lo, hi);
     const int steps = (min(hi - window0, 1024) + 31) / 32;
-    for (int step = ROWS ? 0 : wave; step < steps; step += kStride) {
+    for (int step = wave; step < steps; step += NW) {
       load(step);
       compute(window0 + 32 * step);
     }
@@ -466,7 +487,7 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
     l[n] += __shfl_xor(l[n], 32, 64);
   }
   // ---- waves that split the keys: join them
-  if constexpr (!ROWS && NW > 1) {
+  {
     __shared__ float sm[NW][NQ * 16], sl[NW][NQ * 16];
     __shared__ v4f so[NQ * kTiles][64];
     if (quarter == 0) {
@@ -535,17 +556,381 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
     };
     put(0, L::kA, 0, std::integral_constant<int, L::kA>{});
     if constexpr (L::kB) put(16 * L::kA, L::kB, L::kA, std::integral_constant<int, L::kB>{});
-    if (quarter == 0) {
-      if (!direct) {
-        g.part_ml[(orow[n] * g.splits + split) * 2] = mref[n];
-        g.part_ml[(orow[n] * g.splits + split) * 2 + 1] = l[n];
-      } else if (g.lse) {
-        const float inf = __builtin_inff();
-        g.lse[orow[n]] = l[n] == 0.0f ? -inf : mref[n] == inf ? inf
-                                                              : (mref[n] + __builtin_amdgcn_logf(l[n])) * 0.6931471805599453f;
+    if (quarter == 0) put_stats<DT>(g, orow[n], split, mref[n], l[n]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows a request: keys and values decoded once per workgroup
+// ---------------------------------------------------------------------------
+// How a value row of D channels is dealt to the 32 rows of a 32 x 32 tile.
+template <int D> struct Deal32 {
+  static constexpr int kA = D >= 256 ? 8 : D >= 128 ? 4 : 2;
+  static constexpr int kB = D / 32 - kA;         // 0, 1 or 2
+};
+
+template <int DT>
+__device__ __forceinline__ v16f_t mfma32(u32x4_t a, u32x4_t b, v16f_t acc) {
+  if constexpr (DT == IN_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), acc, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), acc, 0, 0, 0);
+}
+
+// A workgroup of NW waves takes 32 NW rows; a wave takes 32 of them and all keys.
+// Of every tile of 64 keys, the waves decode the four groups of 16 (of eight waves,
+// four the keys and four the values) and write them to LDS as whole operand
+// fragments (64 lanes x 16 bytes), so that every product afterwards is one
+// contiguous 16-byte LDS read per lane and a matrix instruction.  Two tiles are kept:
+// the next one's codes are in flight or being decoded while this one is computed, one
+// barrier a tile.
+//   - S^T = K Q^T and O^T = V^T P^T in 32 x 32 x 16 steps.  S^T leaves lane (q =
+//     lane % 32, h = lane / 32) with rows 8 i + 4 h + (0 .. 3); a key whose place in its 16
+//     has bits b3 b2 b1 b0 is put into row b2 b3 b1 b0, so that the lane's 8 rows of a
+//     16-key step are keys 8 h .. 8 h + 7, the ones it feeds as P^T.
+//   - fragments are 1040 bytes apart: lanes that write 8 fragments of one key then
+//     meet 8 different groups of banks.
+template <int DT, int D, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_tile_kernel(const AttnArgs g) {
+  using L = Deal32<D>;
+  using T = uint16_t;
+  constexpr int kSteps = D / 16;                 // K steps of S^T
+  constexpr int kTiles = D / 32;                 // 32-channel tiles of O^T
+  constexpr int kFrag = 1040;
+  constexpr int kFragsK = 2 * kSteps, kFrags = kFragsK + 4 * kTiles;
+  constexpr int kRows = 32 * NW;
+  constexpr int kKLoads = (D + 63) / 64;         // 16-byte loads of a lane for 16 keys
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kFrags * kFrag];
+  __shared__ int nan_tile[2][4];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave & 3;                     // row group of a tile that this wave decodes
+  const bool decodes_k = NW == 4 || wave < 4, decodes_v = NW == 4 || wave >= 4;
+  const int r = lane & 31, h = lane >> 5;
+
+  int64_t b = blockIdx.x;
+  const int hk = int(b % g.kv_heads); b /= g.kv_heads;
+  const int split = int(b % g.splits); b /= g.splits;
+  const int rt = int(b % g.row_tiles);
+  const int64_t req = b / g.row_tiles;
+  const int G = g.group;
+  const int64_t t0 = min(max(int64_t(g.cu[req]), int64_t(0)), g.tokens);
+  const int64_t t1 = min(max(int64_t(g.cu[req + 1]), t0), g.tokens);
+  const int m = int(t1 - t0), kv = max(g.lens[req], 0);
+  const int64_t rows = int64_t(m) * G, row0 = int64_t(rt) * kRows;
+  if (rows <= kFewRows || row0 >= rows) return;  // requests of few rows are attention_kernel's
+  if (m > g.max_q || kv > g.max_kv) {            // not what the grid was sized for
+    refuse_request<DT, D>(g, t0, rows, hk, rt, split);
+    return;
+  }
+  const int i0 = int(row0 / G), i1 = int((min(row0 + kRows, rows) - 1) / G);
+  const int hi_all = max(kv - m + i1 + 1, 0);
+  const int lo = g.window ? max(kv - m + i0 - g.window + 1, 0) : 0;
+  const int64_t start64 = int64_t(lo & ~31) + int64_t(split) * g.chunk;
+  if (split > 0 && start64 >= hi_all) {
+    empty_split(g, t0, row0, min(row0 + kRows, rows), hk, split);
+    return;
+  }
+  const int start = int(start64), hi = int(min(int64_t(hi_all), start64 + g.chunk));
+  // keys in [all_from, all_to) are seen by every row of the workgroup
+  const int all_from = g.window ? max(kv - m + i1 - g.window + 1, 0) : 0, all_to = min(hi, kv - m + i0 + 1);
+
+  int last, first;
+  int64_t orow;
+  u32x4_t qf[kSteps];
+  int wlast_min, wfirst_max;
+  {
+    const int64_t row = row0 + wave * 32 + r;
+    const bool real = row < rows;
+    const int64_t rr = real ? row : rows - 1;
+    const int i = int(rr / G);
+    const int64_t head = int64_t(hk) * G + (rr - int64_t(i) * G);
+    orow = real ? (t0 + i) * g.heads + head : -1;
+    last = real ? kv - m + i : -1;
+    first = g.window ? max(kv - m + i - g.window + 1, 0) : 0;
+    wlast_min = real ? last : 0x7FFFFFFF;
+    wfirst_max = real ? first : 0;
+    const T* q = static_cast<const T*>(g.q) + (t0 + i) * g.q_ts + head * g.q_hs + 8 * h;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) qf[s] = *reinterpret_cast<const u32x4_t*>(q + 16 * s);
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    wlast_min = min(wlast_min, __shfl_xor(wlast_min, off, 64));
+    wfirst_max = max(wfirst_max, __shfl_xor(wfirst_max, off, 64));
+  }
+  wlast_min = __builtin_amdgcn_readfirstlane(wlast_min);
+  wfirst_max = __builtin_amdgcn_readfirstlane(wfirst_max);
+
+  v16f_t o[kTiles];
+  float mref = kLowest, l = 0.0f;
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) o[t][v] = 0.0f;
+
+  // ---- this wave's 16 keys or values of a tile
+  uint4 rk[kKLoads];
+  uint32_t rks[kKLoads];
+  uint32_t rv[8][L::kA == 8 ? 2 : 1], rvb[8], rvs[8], rvsb[8];
+  int groups = -1;
+  const int32_t* table = g.table + req * g.table_stride;
+  auto load = [&](int tile0) {
+    if (((tile0 - start) & 1023) == 0) groups = row_group(g, table, hk, tile0 + lane * 16, lo, hi);
+    const int grp = __builtin_amdgcn_readlane(groups, ((tile0 - start) & 1023) / 16 + part);
+    if (grp >= 0) {
+      const uint8_t* k = g.kc + int64_t(grp) * 16 * D;
+      const uint8_t* ks = g.ks + int64_t(grp) * 16 * (D / 32);
+      if (decodes_k) {
+#pragma unroll
+        for (int u = 0; u < kKLoads; ++u) {
+          const int c = lane + 64 * u;           // 16-byte chunk of the 16 rows
+          if (D % 64 == 0 || c < D) {
+            rk[u] = *reinterpret_cast<const uint4*>(k + 16 * c);
+            rks[u] = ks[c / 2];                  // two chunks to a block of 32
+          }
+        }
+      }
+      if (!decodes_v) return;
+      const uint8_t* v = g.vc + int64_t(grp) * 16 * D + 8 * h * D;
+      const uint8_t* vs = g.vs + int64_t(grp) * 16 * (D / 32) + 8 * h * (D / 32);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint8_t* a = v + j * D + L::kA * r;
+        if constexpr (L::kA == 8) {
+          const uint2 w = *reinterpret_cast<const uint2*>(a);
+          rv[j][0] = w.x; rv[j][1] = w.y;
+        } else if constexpr (L::kA == 4) {
+          rv[j][0] = *reinterpret_cast<const uint32_t*>(a);
+        } else {
+          rv[j][0] = *reinterpret_cast<const uint16_t*>(a);
+        }
+        rvs[j] = vs[j * (D / 32) + (L::kA * r) / 32];
+        if constexpr (L::kB) {
+          const uint8_t* e = v + j * D + 32 * L::kA + L::kB * r;
+          if constexpr (L::kB == 2) rvb[j] = *reinterpret_cast<const uint16_t*>(e);
+          else rvb[j] = *e;
+          rvsb[j] = vs[j * (D / 32) + (32 * L::kA + L::kB * r) / 32];
+        }
+      }
+    } else {                                     // keys of a bad page are NaN, and so is what sees them
+#pragma unroll
+      for (int u = 0; u < kKLoads; ++u) {
+        rk[u] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        rks[u] = 127;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        rv[j][0] = rvb[j] = 0;
+        if constexpr (L::kA == 8) rv[j][1] = 0;
+        rvs[j] = rvsb[j] = 127;
       }
     }
+  };
+  auto decode = [&](int tile0, int buf) {
+    uint8_t* base = lds[buf];
+    if (decodes_k)
+#pragma unroll
+    for (int u = 0; u < kKLoads; ++u) {
+      const int c = lane + 64 * u;
+      const int key = c / kSteps, s = c % kSteps;
+      const int row = ((key >> 2) & 1) * 8 + (key >> 3) * 4 + (key & 3) + 16 * (part & 1);
+      const uint32_t sc = rks[u] << 23;
+      uint8_t* dst = base + ((part >> 1) * kSteps + s) * kFrag + row * 16;
+      if (D % 64 == 0 || c < D) {
+        *reinterpret_cast<u32x4_t*>(dst) = u32x4_t{decode2<DT, false>(rk[u].x, sc), decode2<DT, true>(rk[u].x, sc),
+                                                   decode2<DT, false>(rk[u].y, sc), decode2<DT, true>(rk[u].y, sc)};
+        *reinterpret_cast<u32x4_t*>(dst + 512) = u32x4_t{decode2<DT, false>(rk[u].z, sc), decode2<DT, true>(rk[u].z, sc),
+                                                         decode2<DT, false>(rk[u].w, sc), decode2<DT, true>(rk[u].w, sc)};
+      }
+    }
+    if (!decodes_v) return;
+    // values that no row sees may be anything; the weight 0 must not meet a NaN there
+    const int key0 = tile0 + 16 * part;
+    uint32_t nan = 0;
+    if (tile0 < all_from || tile0 + 64 > all_to) {
+      const uint32_t from = uint32_t(lo - key0 - 8 * h), many = uint32_t(max(hi - lo, 0));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool keep = uint32_t(j) - from < many;
+        rv[j][0] = keep ? rv[j][0] : 0u;
+        if constexpr (L::kA == 8) rv[j][1] = keep ? rv[j][1] : 0u;
+        rvs[j] = keep ? rvs[j] : 127u;
+        nan |= any_nan_code(rv[j][0]) | (rvs[j] == 255u ? 1u : 0u);
+        if constexpr (L::kA == 8) nan |= any_nan_code(rv[j][1]);
+        if constexpr (L::kB) {
+          rvb[j] = keep ? rvb[j] : 0u;
+          rvsb[j] = keep ? rvsb[j] : 127u;
+          nan |= any_nan_code(rvb[j]) | (rvsb[j] == 255u ? 1u : 0u);
+        }
+      }
+    }
+    const bool any = __ballot(nan != 0) != 0;
+    if (lane == 0) nan_tile[buf][part] = any;
+    uint8_t* vb = base + (kFragsK + part) * kFrag + lane * 16;   // fragment (tile, step) at kFragsK + 4 tile + step
+    auto pair = [&](const uint32_t (&w)[8], const uint32_t (&sc)[8], auto hi_half, int tile, bool both) {
+      constexpr bool HI = decltype(hi_half)::value;
+      u32x4_t a, c;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = decode2<DT, HI>(w[2 * j], sc[2 * j] << 23);
+        const uint32_t y = decode2<DT, HI>(w[2 * j + 1], sc[2 * j + 1] << 23);
+        a[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+        c[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+      }
+      *reinterpret_cast<u32x4_t*>(vb + 4 * tile * kFrag) = a;
+      if (both) *reinterpret_cast<u32x4_t*>(vb + 4 * (tile + 1) * kFrag) = c;
+    };
+#pragma unroll
+    for (int w = 0; w < (L::kA == 8 ? 2 : 1); ++w) {
+      uint32_t x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = rv[j][w];
+      pair(x, rvs, std::false_type{}, 4 * w, true);
+      if constexpr (L::kA >= 4) pair(x, rvs, std::true_type{}, 4 * w + 2, true);
+    }
+    if constexpr (L::kB) pair(rvb, rvsb, std::false_type{}, L::kA, L::kB == 2);
+  };
+
+  // A tile with NaN values that some rows of the workgroup see and others do not: 0 * NaN would reach
+  // those.  The NaNs are put into the outputs of the rows that see them, where a product of marks and
+  // visibility finds any, and then taken out of the tile.
+  auto take_nans = [&](int tile0, int buf) {
+    constexpr uint32_t kInfBits = DT == IN_BF16 ? 0x7F80u : 0x7C00u, kOne = DT == IN_BF16 ? 0x3F80u : 0x3C00u;
+    auto nans = [](u32x4_t x) {                  // all bits of the NaN halves
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[j] = ((x[j] & 0x7FFFu) > kInfBits ? 0xFFFFu : 0u) | (((x[j] >> 16) & 0x7FFFu) > kInfBits ? 0xFFFF0000u : 0u);
+      return x;
+    };
+    const uint32_t from = uint32_t(first - tile0 - 8 * h), many = uint32_t(max(min(last, hi - 1) - first + 1, 0));
+#pragma nounroll
+    for (int u = 0; u < 4; ++u) {
+      u32x4_t see;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        see[j] = (uint32_t(16 * u + 2 * j) - from < many ? kOne : 0u) |
+                 (uint32_t(16 * u + 2 * j + 1) - from < many ? kOne << 16 : 0u);
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        u32x4_t mark = nans(*reinterpret_cast<const u32x4_t*>(lds[buf] + (kFragsK + 4 * t + u) * kFrag + lane * 16));
+        mark &= kOne | kOne << 16;
+        v16f_t hits;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) hits[v] = 0.0f;
+        hits = mfma32<DT>(mark, see, hits);
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int any = -__float_as_int(hits[v]) >> 31;
+          o[t][v] = __uint_as_float(__float_as_uint(o[t][v]) | (uint32_t(any) & 0x7FC00000u));
+        }
+        __builtin_amdgcn_sched_barrier(0);       // one fragment at a time: this path shall cost no registers
+      }
+    }
+    __syncthreads();
+    for (int f = kFragsK + wave; f < kFrags; f += NW) {
+      u32x4_t* at = reinterpret_cast<u32x4_t*>(lds[buf] + f * kFrag + lane * 16);
+      *at &= ~nans(*at);
+    }
+    __syncthreads();
+  };
+
+  auto compute = [&](int tile0, int buf) {
+    const uint8_t* base = lds[buf] + lane * 16;
+    // ---- S^T
+    v16f_t s[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+      for (int v = 0; v < 16; ++v) s[kt][v] = 0.0f;
+#pragma unroll
+      for (int f = 0; f < kSteps; ++f)
+        s[kt] = mfma32<DT>(*reinterpret_cast<const u32x4_t*>(base + (kt * kSteps + f) * kFrag), qf[f], s[kt]);
+    }
+    // ---- masks: value 8 i + j of s[kt] is key 32 kt + 16 i + 8 h + j of the tile
+    const uint32_t from = uint32_t(first - tile0 - 8 * h), many = uint32_t(max(min(last, hi - 1) - first + 1, 0));
+    const bool edge = tile0 + 63 > wlast_min || tile0 < wfirst_max || tile0 + 64 > hi;
+    if (edge) {
+#pragma unroll
+      for (int v = 0; v < 32; ++v)
+        s[v >> 4][v & 15] = uint32_t(16 * (v >> 3) + (v & 7)) - from < many ? s[v >> 4][v & 15] : -__builtin_inff();
+    }
+    // ---- reference exponent
+    float top = s[0][0];
+#pragma unroll
+    for (int v = 1; v < 32; ++v) top = fmaxf(top, s[v >> 4][v & 15]);
+    top *= g.c;
+    if (__ballot(top > mref + (kLift<DT> + kSlack))) {
+      const float next = fmaxf(mref, fmaxf(top, __shfl_xor(top, 32, 64)) - kLift<DT>);
+      const float a = mref == next ? 1.0f : __builtin_amdgcn_exp2f(mref - next);
+      mref = next;
+      l *= a;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) o[t] *= a;
+    }
+    // ---- weights
+    u32x4_t p[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u >> 1][8 * (u & 1) + j], g.c, -mref));
+      l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      p[u] = u32x4_t{pack2<DT>(e[0], e[1]), pack2<DT>(e[2], e[3]), pack2<DT>(e[4], e[5]), pack2<DT>(e[6], e[7])};
+    }
+    // ---- O^T
+    const uint8_t* vbase = base + kFragsK * kFrag;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+        o[t] = mfma32<DT>(*reinterpret_cast<const u32x4_t*>(vbase + (4 * t + u) * kFrag), p[u], o[t]);
+  };
+
+  if (start < hi) {
+    load(start);
+    decode(start, 0);
+    if (start + 64 < hi) load(start + 64);
+    __syncthreads();
+    int buf = 0;
+    for (int tile0 = start; tile0 < hi; tile0 += 64) {
+      if (tile0 + 64 < hi) {
+        decode(tile0 + 64, buf ^ 1);
+        if (tile0 + 128 < hi) load(tile0 + 128);
+      }
+      if (nan_tile[buf][0] | nan_tile[buf][1] | nan_tile[buf][2] | nan_tile[buf][3]) take_nans(tile0, buf);
+      compute(tile0, buf);
+      __syncthreads();
+      buf ^= 1;
+    }
   }
+
+  // ---- outputs: the lane holds channels kA c + t of the first run (c = 8 (v / 4) + 4 h + v % 4), likewise of the second
+  l += __shfl_xor(l, 32, 64);
+  if (orow < 0) return;
+  const bool direct = g.splits == 1;
+  const float inv = direct ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+  auto put = [&](int base, int tile0, auto kWidth) {
+    constexpr int W = decltype(kWidth)::value;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int64_t d = base + W * (8 * (v >> 2) + 4 * h + (v & 3));
+      if (direct) {
+        T* dst = static_cast<T*>(g.out) + orow * D + d;
+        if constexpr (W == 1) *dst = T(pack2<DT>(o[tile0][v] * inv, 0.0f));
+        else
+#pragma unroll
+          for (int t = 0; t < W; t += 2)
+            *reinterpret_cast<uint32_t*>(dst + t) = pack2<DT>(o[tile0 + t][v] * inv, o[tile0 + t + (W > 1)][v] * inv);
+      } else {
+        float* dst = g.part + (orow * g.splits + split) * D + d;
+#pragma unroll
+        for (int t = 0; t < W; ++t) dst[t] = o[tile0 + t][v];
+      }
+    }
+  };
+  put(0, 0, std::integral_constant<int, L::kA>{});
+  if constexpr (L::kB) put(32 * L::kA, L::kA, std::integral_constant<int, L::kB>{});
+  if (h == 0) put_stats<DT>(g, orow, split, mref, l);
 }
 
 // Joins the splits of one row: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
@@ -591,19 +976,18 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs g, i
     if (d < D)
       *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(g.out) + row * D + d) = pack2<DT>(acc[u][0] * inv, acc[u][1] * inv);
   }
-  if (g.lse && lane == 0) {
-    const float inf = __builtin_inff();
-    g.lse[row] = sum == 0.0f ? -inf : top == inf ? inf : (top + __builtin_amdgcn_logf(sum)) * 0.6931471805599453f;
-  }
+  if (g.lse && lane == 0) g.lse[row] = log_sum(top, sum);
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
 struct Plan {
-  bool rows;                    // the waves of a workgroup split the rows, not the keys
-  int nq;                       // 16-row tiles of a wave
-  int64_t row_tiles, splits, chunk;
+  int nq;                       // 16-row tiles of attention_kernel
+  bool tiles;                   // some request may have more than kFewRows rows
+  bool few;                     // some request may have no more
+  int64_t row_tiles, tile_rows; // of attention_tile_kernel
+  int64_t splits, chunk;
   int64_t bytes;                // workspace
 };
 
@@ -616,37 +1000,46 @@ mx_status_t plan_attention(int64_t tokens, int heads, int kv_heads, int dim, int
   if (dim != 64 && dim != 96 && dim != 128 && dim != 192 && dim != 256) return MX_ERR_SHAPE;
   if (max_q < 0 || max_kv < 0 || window < 0) return MX_ERR_ARG;
   if (tokens > lim || requests > lim || max_kv > lim || max_q > lim) return MX_ERR_SHAPE;
-  max_q = std::min(max_q, tokens);
   const int64_t cus = device_cus();
   if (cus <= 0) return MX_ERR_LAUNCH;
-  const int group = heads / kv_heads;
-  const int64_t rows = std::max<int64_t>(max_q * group, 1);
-  p.nq = rows <= 16 ? 1 : 2;
-  p.rows = rows > 32;
-  const int tile = p.nq * 16 * (p.rows ? kWaves : 1);
-  p.row_tiles = (rows + tile - 1) / tile;
+  const int64_t group = heads / kv_heads, reqs = std::max<int64_t>(requests, 1);
+  const int64_t rows = std::max<int64_t>(std::min(max_q, tokens) * group, 1);
+  p.tiles = rows > kFewRows;
+  p.few = !p.tiles || requests > 1;
+  p.nq = std::min<int64_t>(rows, p.tiles ? kFewRows : rows) <= 16 ? 1 : 2;
+  p.tile_rows = dim > 128 ? 128 : 256;
+  p.row_tiles = p.tiles ? (rows + p.tile_rows - 1) / p.tile_rows : 1;
   // keys that one row tile can see
   int64_t keys = max_kv;
-  if (window > 0) keys = std::min(keys, window + tile / group + 33);
+  if (window > 0) keys = std::min(keys, window + (p.tiles ? p.tile_rows : kFewRows) / group + 33);
   keys = std::max<int64_t>((keys + 31) / 32 * 32, 32);
-  // enough workgroups for three on every CU, but no split under two steps a wave
-  const int64_t base = std::max<int64_t>(requests, 1) * kv_heads * p.row_tiles;
-  const int64_t want = std::max<int64_t>(1, 3 * cus / base);
-  const int64_t least = 32 * 2 * (p.rows ? 4 : kWaves);
-  p.chunk = std::max((keys + want - 1) / want, least);
+  // Splits: enough workgroups for three of attention_kernel on every CU, or one and a half of
+  // attention_tile_kernel (one fits a CU), but none with less than two steps a wave or four tiles.
+  const int64_t base = p.tiles ? std::min(reqs * p.row_tiles, tokens * group / p.tile_rows + reqs) * kv_heads
+                               : reqs * kv_heads;
+  const int64_t want = std::max<int64_t>(1, (p.tiles ? cus + cus / 2 : 3 * cus) / base);
+  p.chunk = std::max<int64_t>((keys + want - 1) / want, 256);
   p.chunk = (p.chunk + 127) / 128 * 128;
   p.splits = (keys + p.chunk - 1) / p.chunk;
   p.bytes = p.splits > 1 ? tokens * heads * p.splits * (dim + 2) * 4 : 0;
-  if (base * p.splits > 0x7FFFFFFF) return MX_ERR_SHAPE;
+  if (reqs * kv_heads * p.row_tiles > 0x7FFFFFFF / p.splits) return MX_ERR_SHAPE;
   return MX_OK;
 }
 
 template <int DT, int D>
-void launch_attention(const Plan& p, const AttnArgs& g, int64_t requests, hipStream_t stream) {
-  const unsigned grid = unsigned(requests * g.kv_heads * p.row_tiles * p.splits);
-  if (p.rows) attention_kernel<DT, D, 2, kWaves, true><<<grid, 64 * kWaves, 0, stream>>>(g);
-  else if (p.nq == 1) attention_kernel<DT, D, 1, kWaves, false><<<grid, 64 * kWaves, 0, stream>>>(g);
-  else attention_kernel<DT, D, 2, kWaves, false><<<grid, 64 * kWaves, 0, stream>>>(g);
+void launch_attention(const Plan& p, AttnArgs g, int64_t requests, hipStream_t stream) {
+  if (p.tiles) {
+    constexpr int NW = D > 128 ? 4 : 8;
+    const unsigned grid = unsigned(requests * g.kv_heads * p.row_tiles * p.splits);
+    attention_tile_kernel<DT, D, NW><<<grid, 64 * NW, 0, stream>>>(g);
+  }
+  if (p.few) {
+    g.few_only = p.tiles;
+    g.row_tiles = 1;
+    const unsigned grid = unsigned(requests * g.kv_heads * p.splits);
+    if (p.nq == 1) attention_kernel<DT, D, 1, kWaves><<<grid, 64 * kWaves, 0, stream>>>(g);
+    else attention_kernel<DT, D, 2, kWaves><<<grid, 64 * kWaves, 0, stream>>>(g);
+  }
   if (p.splits > 1)
     attention_join_kernel<DT, D><<<unsigned((g.tokens * g.heads + 3) / 4), 256, 0, stream>>>(g, requests);
 }
