@@ -1,10 +1,11 @@
 """Python binding of libmx: OCP MX block quantization and block-scaled GEMM on
 AMD Instinct MI355X (gfx950).
 
-Argument marshalling only.  Every step of the computation runs in the HIP
+Argument marshalling only (of the rotary and cache operators by ``_bind.so``, from
+``csrc/bind.cpp``, which costs a call less time than ctypes).  Every step of the computation runs in the HIP
 kernels of ``libmx.so`` (built from ``csrc/`` by ``_build.py``); PyTorch only
 provides device memory and the current HIP stream.  There is no CPU fallback:
-importing this module without the built library, or passing host tensors,
+importing this module without the built libraries, or passing host tensors,
 raises.
 
 The functions carry the names of the C entry points declared in
@@ -45,6 +46,12 @@ if not os.path.exists(LIB_PATH):
 
 # torch is imported first so that its HIP runtime is the one libmx binds to
 lib = ctypes.CDLL(LIB_PATH)
+
+try:
+    from . import _bind
+except ImportError as e:
+    raise ImportError(f"the binding {os.path.join(_HERE, '_bind.so')} is missing or does not load: build it first "
+                      "(python -c 'import __graft_entry__ as g; g.build()')") from e
 
 # ---------------------------------------------------------------- enums (include/mx.h)
 FMT = {"e4m3": 0, "e5m2": 1, "e2m1": 2, "e2m3": 3, "e3m2": 4}
@@ -124,6 +131,9 @@ def check(status: int):
     if status in (2, 4, 6):
         raise MXValueError(status)
     raise MXError(status)
+
+
+_bind.set_check(check)
 
 
 def _ptr(t):
@@ -405,47 +415,6 @@ def new_kv_cache(pages: int, kv_heads: int, page: int, dim: int, device="cuda") 
                      for n in (dim, dim // 32, dim, dim // 32)))
 
 
-def _cache_args(cache, device):
-    k, ks, v, vs = cache
-    if k.dim() != 4:
-        raise ValueError("cache codes must be [pages][kv_heads][page][dim]")
-    pages, heads, page, dim = k.shape
-    scales = (pages, heads, page, dim // 32)
-    if v.shape != k.shape or ks.shape != scales or vs.shape != scales:
-        raise ValueError("cache tensors must be codes [pages][kv_heads][page][dim] and scales [..][dim / 32]")
-    for t in cache:
-        if t.dtype is not torch.uint8 or not t.is_contiguous() or t.device != device:
-            raise ValueError("cache tensors must be contiguous uint8 tensors on the device of the other arguments")
-    return _KVCacheArgs(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), pages, heads, page, dim)
-
-
-def _heads_3d(x, name, device):
-    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
-        raise ValueError(f"{name} must be [tokens][heads][dim] with contiguous channels")
-    if x.device != device:
-        raise ValueError(f"{name} must be on the device of the other arguments")
-
-
-def _vector(x, name, dtype, n, device):
-    if x.dtype is not dtype or x.dim() != 1 or x.shape[0] != n or not x.is_contiguous() or x.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} vector of length {n} on the device of the other arguments")
-
-
-def _rope_rows(table, device):
-    """(rows, rot) of a rotary table."""
-    if table.dtype is not torch.float32 or table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous() \
-            or table.device != device:
-        raise ValueError("table must be a contiguous float32 tensor [rows][rot / 2][2] on the device of the other arguments")
-    return table.shape[0], 2 * table.shape[1]
-
-
-def _on_device(t):
-    """The library launches on the current device: make it the tensors' own."""
-    if not t.is_cuda:
-        raise ValueError("libmx works on device tensors only")
-    return torch.cuda.device(t.device)
-
-
 def mx_rope_table(rows, rot, base=1e4, scaling="none", factor=1.0, orig_len=0, device="cuda"):
     """Rotary table [rows][rot / 2][2] of float32 (cos, sin) pairs of positions 0 .. rows - 1.
 
@@ -456,8 +425,7 @@ def mx_rope_table(rows, rot, base=1e4, scaling="none", factor=1.0, orig_len=0, d
     if rows < 0 or rot < 2 or rot % 2:
         raise MXValueError(2)
     out = torch.empty((rows, rot // 2, 2), dtype=torch.float32, device=device)
-    with _on_device(out):
-        check(lib.mx_rope_table(rows, rot, float(base), kind, float(factor), int(orig_len), _ptr(out), _stream(out)))
+    _bind.rope_table(rows, rot, base, kind, factor, orig_len, out)
     return out
 
 
@@ -468,62 +436,14 @@ def mx_rope(x, pos, table, layout="half", inverse=False, out=None):
     layout "half" pairs channel i with i + rot / 2, "interleaved" 2i with 2i + 1.  inverse=True
     turns back, which is also the backward pass: grad_x = mx_rope(grad_y, pos, table, layout,
     inverse=True).  out may be x itself (in place)."""
-    lay = _lookup(ROPE_LAYOUT, layout, "rotary layout")
-    dt = _lookup(DTYPE, x.dtype, "dtype")
-    _heads_3d(x, "x", x.device)
-    tokens, heads, dim = x.shape
-    rows, rot = _rope_rows(table, x.device)
-    _vector(pos, "pos", torch.int32, tokens, x.device)
-    if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
-    else:
-        _heads_3d(out, "out", x.device)
-        if out.shape != x.shape or out.dtype != x.dtype:
-            raise ValueError("out must have the shape and dtype of x")
-    with _on_device(x):
-        check(lib.mx_rope(x.data_ptr(), dt, tokens, heads, dim, x.stride(0), x.stride(1), pos.data_ptr(),
-                          table.data_ptr(), rows, rot, lay, int(bool(inverse)), out.data_ptr(), out.stride(0),
-                          out.stride(1), _stream(x)))
-    return out
+    return _bind.rope(x, pos, table, _lookup(ROPE_LAYOUT, layout, "rotary layout"), inverse, out)
 
 
 def mx_kv_append(k, v, cache, slots, pos=None, table=None, layout="half", q=None, q_out=None):
     """Stores tokens in the cache: k rotated (if table is given) and MXFP8-encoded, v encoded, at
     slots (int64 [tokens]; slot s is token s % page of page s // page, a slot outside the cache is
     skipped).  With q (table needed) returns q rotated, [tokens][heads][dim], from the same launch."""
-    lay = _lookup(ROPE_LAYOUT, layout, "rotary layout")
-    dt = _lookup(DTYPE, k.dtype, "dtype")
-    dev = k.device
-    args = _cache_args(cache, dev)
-    _heads_3d(k, "k", dev)
-    _heads_3d(v, "v", dev)
-    tokens = k.shape[0]
-    if v.shape != k.shape or v.dtype != k.dtype or k.shape[1] != args.kv_heads or k.shape[2] != args.dim:
-        raise ValueError("k and v must be [tokens][kv_heads][dim] of one dtype, matching the cache")
-    _vector(slots, "slots", torch.int64, tokens, dev)
-    rows, rot = 0, 2
-    if table is not None:
-        rows, rot = _rope_rows(table, dev)
-        if pos is None:
-            raise ValueError("a rotation needs pos")
-        _vector(pos, "pos", torch.int32, tokens, dev)
-    heads, qt, qh = 0, 0, 0
-    if q is not None:
-        _heads_3d(q, "q", dev)
-        if table is None:
-            raise ValueError("q is only rotated: it needs a table")
-        if q.shape[0] != tokens or q.shape[2] != args.dim or q.dtype != k.dtype:
-            raise ValueError("q must be [tokens][heads][dim] with the dtype of k")
-        heads, qt, qh = q.shape[1], q.stride(0), q.stride(1)
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous() or q_out.device != dev:
-            raise ValueError("q_out must be contiguous with the shape, dtype and device of q")
-    with _on_device(k):
-        check(lib.mx_kv_append(k.data_ptr(), v.data_ptr(), dt, tokens, k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                               args, slots.data_ptr(), None if table is None else pos.data_ptr(), _ptr(table), rows, rot,
-                               lay, _ptr(q), heads, qt, qh, None if q is None else q_out.data_ptr(), _stream(k)))
-    return None if q is None else q_out
+    return _bind.kv_append(k, v, *cache, slots, pos, table, _lookup(ROPE_LAYOUT, layout, "rotary layout"), q, q_out)
 
 
 def mx_paged_attention(q, cache, page_table, cu, lens, window=0, scale=None, lse=False, max_q=None, max_kv=None,
@@ -540,35 +460,8 @@ def mx_paged_attention(q, cache, page_table, cu, lens, window=0, scale=None, lse
                 read from cu and lens, which waits for the GPU: give them in serving loops.
     Returns out [tokens][heads][dim], or (out, lse [tokens][heads] float32).  Queries that see
     nothing give 0 and -inf."""
-    dt = _lookup(DTYPE, q.dtype, "dtype")
-    dev = q.device
-    args = _cache_args(cache, dev)
-    _heads_3d(q, "q", dev)
-    tokens, heads, dim = q.shape
-    if dim != args.dim or heads % args.kv_heads:
-        raise ValueError("q must have the cache's dim and a multiple of its heads")
-    requests = lens.shape[0] if lens.dim() == 1 else -1
-    _vector(lens, "lens", torch.int32, requests, dev)
-    _vector(cu, "cu", torch.int32, requests + 1, dev)
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != requests \
-            or (page_table.stride(1) != 1 and page_table.shape[1] > 1) or page_table.device != dev:
-        raise ValueError("page_table must be an int32 tensor [requests][pages] with contiguous rows")
     if max_q is None:
-        max_q = int((cu[1:] - cu[:-1]).max()) if requests else 0
+        max_q = int((cu[1:] - cu[:-1]).max()) if lens.numel() else 0
     if max_kv is None:
-        max_kv = int(lens.max()) if requests else 0
-    if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
-        raise ValueError("out must be contiguous with the shape, dtype and device of q")
-    stats = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if lse else None
-    with _on_device(q):
-        need = _i64(0)
-        check(lib.mx_paged_attention_workspace(tokens, heads, args.kv_heads, dim, requests, max_q, max_kv, window, need))
-        space = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-        check(lib.mx_paged_attention(q.data_ptr(), dt, tokens, heads, q.stride(0), q.stride(1), args,
-                                     page_table.data_ptr(), page_table.stride(0), page_table.shape[1], cu.data_ptr(),
-                                     lens.data_ptr(), requests, max_q, max_kv, window,
-                                     dim ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(stats), _ptr(space),
-                                     need.value, _stream(q)))
-    return (out, stats) if lse else out
+        max_kv = int(lens.max()) if lens.numel() else 0
+    return _bind.paged_attention(q, *cache, page_table, cu, lens, window, scale, lse, max_q, max_kv, out)

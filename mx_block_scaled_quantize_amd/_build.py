@@ -1,19 +1,22 @@
-"""Build libmx.so (HIP, gfx950) in-tree with hipcc.
+"""Build libmx.so (HIP, gfx950) and the binding _bind.so in-tree.
 
-Every .hip source under csrc/ is compiled to its own object (in parallel) and
-linked into ``mx_block_scaled_quantize_amd/libmx.so``.  hipcc cross-compiles for
-gfx950 without a GPU present.
+Every .hip source under csrc/ is compiled with hipcc to its own object (in
+parallel) and linked into ``mx_block_scaled_quantize_amd/libmx.so``.  hipcc
+cross-compiles for gfx950 without a GPU present.  csrc/bind.cpp is host code
+against Python's and torch's headers, compiled with g++ into ``_bind.so``.
 """
 
 import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmx.so")
+BIND = os.path.join(PKG, "_bind.so")
 ARCH = "gfx950"
 
 # Device code keeps FP32 denormals (the default) and never contracts a*b+c into
@@ -46,19 +49,43 @@ def _compile(src):
     return obj
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_bind():
+    import torch
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "bind.o")
+    _run(["g++", "-std=c++17", "-O2", "-fPIC", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include", "-I/opt/rocm/include",
+          f"-I{sysconfig.get_paths()['include']}", "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj], "g++ bind.cpp")
+    return obj, os.path.join(root, "lib")
+
+
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(_compile, srcs))
+        bind_obj, torch_lib = bind.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # torch's libraries are loaded before the binding is; libmx lies beside it
+    tmp = BIND + ".tmp"
+    _run(["g++", "-shared", "-o", tmp, bind_obj, f"-L{PKG}", "-lmx", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu",
+          "-lc10", "-lc10_hip", "-lamdhip64", "-Wl,-rpath,$ORIGIN"], "link of _bind.so")
+    os.replace(tmp, BIND)
     if verbose:
-        print(f"built {LIB}", file=sys.stderr)
+        print(f"built {LIB} and {BIND}", file=sys.stderr)
     return LIB
 
 
