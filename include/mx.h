@@ -348,8 +348,8 @@ mx_status_t mm_fp8(const uint8_t* a, const uint8_t* b, mx_elem_t fmt, int64_t ba
  * The cache keeps every token's key and value as MXFP8 (E4M3 elements, blocks of
  * 32 along the head dimension, round-up scale rule; [UE8M0] MX definition
  * paragraph), in pages of `page` tokens:
- *   codes  [pages][kv_heads][page][dim], 16-byte aligned;
- *   scales [pages][kv_heads][page][dim / 32].
+ *   codes  [pages][kv_heads][page][dim],
+ *   scales [pages][kv_heads][page][dim / 32], all four arrays 16-byte aligned.
  * Slot s of the cache is token s % page of page s / page.  A request's tokens lie
  * in the pages that its row of the page table lists, in order.
  * dim is 64, 96, 128, 192 or 256; page a multiple of 16 in 16 .. 65536;

@@ -47,8 +47,9 @@ constexpr float kSlack = 8.0f;
 // are not lost below F16's smallest subnormal; with the slack they stay under 2^15.
 template <int DT> constexpr float kLift = DT == IN_F16 ? 7.0f : 0.0f;
 
-// Requests of up to so many rows (tokens x group) go to attention_kernel, whose waves split the keys.
+// Requests of up to so many rows (tokens x group) are taken by workgroups whose waves split the keys.
 constexpr int kFewRows = 32;
+constexpr int64_t kFewPerCu = 8;
 
 struct AttnArgs {
   const void* q;
@@ -68,7 +69,8 @@ struct AttnArgs {
   int window;                   // 0: none
   int row_tiles, splits, chunk; // keys of a split, a multiple of 32
   float c;                      // scale * log2(e)
-  bool few_only;                // requests of more than kFewRows rows are left to attention_tile_kernel
+  int64_t tile_blocks;          // workgroups of attention_tile_kernel that take requests of many rows
+  bool few_only;                // few_rows leaves requests of more than kFewRows rows to them
 };
 
 template <int DT>
@@ -123,8 +125,7 @@ __device__ __forceinline__ int row_group(const AttnArgs& g, const int32_t* __res
 
 // NaN for all rows of one kv head of a request that exceeds what the caller announced.
 template <int DT, int D>
-__device__ __forceinline__ void refuse_request(const AttnArgs& g, int64_t t0, int64_t rows, int hk, int rt, int split) {
-  if (rt != 0) return;
+__device__ __forceinline__ void refuse_request(const AttnArgs& g, int64_t t0, int64_t rows, int hk, int split) {
   const float nan = __uint_as_float(0x7FC00000u);
   for (int64_t i = threadIdx.x; i < rows; i += blockDim.x) {
     const int64_t row = (t0 + i / g.group) * g.heads + hk * g.group + i % g.group;
@@ -163,63 +164,76 @@ __device__ __forceinline__ void put_stats(const AttnArgs& g, int64_t row, int sp
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows a request: the waves of a workgroup split the keys
+// ---------------------------------------------------------------------------
+// How the scale bytes of a step come: with 2 or 4 blocks to a row, whole words are
+// loaded and a rotation brings the byte a lane needs under the exponent field;
+// otherwise byte by byte.
+template <int D> struct ScaleLoad {
+  static constexpr bool kWordsK = D == 64 || D == 128 || D == 256, kWordsV = D == 64 || D == 128;
+  static constexpr int kK = D == 256 ? 2 : kWordsK ? 1 : (D + 63) / 64;   // registers for a key
+  static constexpr int kV = kWordsV ? D / 16 : 8 * Deal<D>::kScales;      // for a lane's 8 keys' values
+};
+
+// LDS of join_waves: the waves' outputs, rows 4 floats apart beyond D so that the 16
+// rows of a tile meet different banks, and their statistics.
+template <int D, int NQ, int NW> struct FewLds {
+  float o[NW][NQ * 16][D + 4];
+  float m[NW][NQ * 16], l[NW][NQ * 16];
+};
+
+// One request, kv head and split of up to 16 NQ rows.  Wave w takes the 32-key steps
+// w, w + NW, ... of the split: no wave waits for another before the end.  The next
+// step's bytes are loaded while this one is computed.
 template <int DT, int D, int NQ, int NW>
-__global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
+__device__ __forceinline__ void few_rows(const AttnArgs& g, int64_t block, FewLds<D, NQ, NW>& lds) {
   using L = Deal<D>;
+  using SL = ScaleLoad<D>;
+  using T = uint16_t;
   constexpr int kFrags = D / 32;                 // K steps of S^T
   constexpr int kTiles = D / 16;                 // 16-channel tiles of O^T
-  constexpr int kKS = (D + 63) / 64;             // scale bytes of a key a lane needs
   constexpr int kRows = NQ * 16;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, quarter = lane >> 4;
 
   // the kv head runs fastest over the grid: neighbouring workgroups go to different
   // XCDs, so with 8 kv heads each XCD's L2 serves one head's pages
-  int64_t b = blockIdx.x;
-  const int hk = int(b % g.kv_heads); b /= g.kv_heads;
-  const int split = int(b % g.splits); b /= g.splits;
-  const int rt = int(b % g.row_tiles);
-  const int64_t req = b / g.row_tiles;
+  const int hk = int(block % g.kv_heads); block /= g.kv_heads;
+  const int split = int(block % g.splits);
+  const int64_t req = block / g.splits;
   const int G = g.group;
 
   const int64_t t0 = min(max(int64_t(g.cu[req]), int64_t(0)), g.tokens);
   const int64_t t1 = min(max(int64_t(g.cu[req + 1]), t0), g.tokens);
   const int m = int(t1 - t0), kv = max(g.lens[req], 0);
-  const int64_t rows = int64_t(m) * G, row0 = int64_t(rt) * kRows;
-  using T = uint16_t;
-  if (g.few_only && rows > kFewRows) return;     // attention_tile_kernel's
+  if (g.few_only && int64_t(m) * G > kFewRows) return;     // attention_tile_kernel's own
   if (m > g.max_q || kv > g.max_kv) {            // not what the grid was sized for
-    refuse_request<DT, D>(g, t0, rows, hk, rt, split);
+    refuse_request<DT, D>(g, t0, int64_t(m) * G, hk, split);
     return;
   }
-  if (row0 >= rows) return;
-  // keys that some row of this tile sees
-  const int i0 = int(row0 / G), i1 = int((min(row0 + kRows, rows) - 1) / G);
-  const int hi_all = max(kv - m + i1 + 1, 0);
-  const int lo = g.window ? max(kv - m + i0 - g.window + 1, 0) : 0;
+  const int rows = m * G;
+  if (rows == 0) return;
+  // keys that some row sees
+  const int hi_all = kv;
+  const int lo = g.window ? max(kv - m - g.window + 1, 0) : 0;
   const int64_t start64 = int64_t(lo & ~31) + int64_t(split) * g.chunk;
   if (split > 0 && start64 >= hi_all) {
-    empty_split(g, t0, row0, min(row0 + kRows, rows), hk, split);
+    empty_split(g, t0, 0, rows, hk, split);
     return;
   }
   const int start = int(start64), hi = int(min(int64_t(hi_all), start64 + g.chunk));
 
   // this lane's rows: where q is, and the keys (first, last] a row sees
   int last[NQ], first[NQ];
-  int64_t orow[NQ];
   u32x4_t qf[NQ][kFrags];
-  int wlast_min = 0x7FFFFFFF, wfirst_max = 0;    // what every row of the wave sees
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const int64_t row = row0 + n * 16 + r;
-    const bool real = row < rows;
-    const int64_t rr = real ? row : rows - 1;
-    const int i = int(rr / G);
-    const int64_t head = int64_t(hk) * G + (rr - int64_t(i) * G);
-    orow[n] = real ? (t0 + i) * g.heads + head : -1;
-    last[n] = real ? kv - m + i : -1;
+    const int row = n * 16 + r;
+    const int rr = min(row, rows - 1);
+    const int i = rr / G, head = hk * G + (rr - i * G);
+    last[n] = row < rows ? kv - m + i : -1;
     first[n] = g.window ? max(kv - m + i - g.window + 1, 0) : 0;
-    if (real) { wlast_min = min(wlast_min, last[n]); wfirst_max = max(wfirst_max, first[n]); }
     const T* q = static_cast<const T*>(g.q) + (t0 + i) * g.q_ts + head * g.q_hs;
 #pragma unroll
     for (int s = 0; s < kFrags; ++s) {
@@ -227,11 +241,8 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
       qf[n][s] = *reinterpret_cast<const u32x4_t*>(q + d);
     }
   }
-#pragma unroll
-  for (int off = 8; off >= 1; off >>= 1) {
-    wlast_min = min(wlast_min, __shfl_xor(wlast_min, off, 64));
-    wfirst_max = max(wfirst_max, __shfl_xor(wfirst_max, off, 64));
-  }
+  // keys in [all_from, all_to) are seen by every row
+  const int all_from = g.window ? max(kv - g.window, 0) : 0, all_to = min(hi, kv - m + 1);
 
   v4f o[NQ][kTiles];
   float mref[NQ], l[NQ];
@@ -245,14 +256,19 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
 
   // ---- one 32-key step as it lies in memory
   struct Raw {
-    uint32_t k[2][kFrags * 2], ks[2][kKS];
-    uint32_t v[8][L::kWords], vs[8][L::kScales];
-  } raw;
+    uint32_t k[2][kFrags * 2], ks[2][SL::kK];
+    uint32_t v[8][L::kWords], vs[SL::kV];
+  };
   // row group of keys 16 i .. 16 i + 15 of the current window of 1024 keys, held by lane i
-  int groups = -1;
+  int groups = -1, window = -1;
   const int32_t* table = g.table + req * g.table_stride;
-  auto load = [&](int step) {      // step: 32-key step within the window
-    const int ga = __builtin_amdgcn_readlane(groups, 2 * step), gb = __builtin_amdgcn_readlane(groups, 2 * step + 1);
+  const int blk_a = (L::kA * r) / 32, blk_b = (16 * L::kA + L::kB * r) / 32;   // blocks of the lane's runs
+  auto load = [&](Raw& raw, int step) {
+    if (step >> 5 != window) {
+      window = step >> 5;
+      groups = row_group(g, table, hk, start + 1024 * window + lane * 16, lo, hi);
+    }
+    const int ga = __builtin_amdgcn_readlane(groups, 2 * (step & 31)), gb = __builtin_amdgcn_readlane(groups, 2 * (step & 31) + 1);
     if ((ga & gb) >= 0) {          // a group that is not read borrows the other's addresses
       const int64_t a16 = int64_t(ga < 0 ? gb : ga) * 16, b16 = int64_t(gb < 0 ? ga : gb) * 16;
       const int64_t krow = ((r & 8) ? b16 : a16) + 8 * ((r >> 2) & 1) + (r & 3);
@@ -265,57 +281,86 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
         for (int u = 0; u < D / 64; ++u) {
           const uint4 w = *reinterpret_cast<const uint4*>(k + 64 * u + 16 * quarter);
           raw.k[t][4 * u] = w.x; raw.k[t][4 * u + 1] = w.y; raw.k[t][4 * u + 2] = w.z; raw.k[t][4 * u + 3] = w.w;
-          raw.ks[t][u] = s[2 * u + (quarter >> 1)];
+          if constexpr (!SL::kWordsK) raw.ks[t][u] = s[2 * u + (quarter >> 1)];
+        }
+        if constexpr (D == 64) raw.ks[t][0] = *reinterpret_cast<const uint16_t*>(s);
+        if constexpr (D == 128) raw.ks[t][0] = *reinterpret_cast<const uint32_t*>(s);
+        if constexpr (D == 256) {
+          const uint2 w = *reinterpret_cast<const uint2*>(s);
+          raw.ks[t][0] = w.x; raw.ks[t][1] = w.y;
         }
         if constexpr (D % 64) {
           const uint2 w = *reinterpret_cast<const uint2*>(k + D / 64 * 64 + 8 * quarter);
           raw.k[t][kFrags * 2 - 2] = w.x; raw.k[t][kFrags * 2 - 1] = w.y;
-          raw.ks[t][kKS - 1] = s[D / 32 - 1];
+          raw.ks[t][SL::kK - 1] = s[D / 32 - 1];
         }
       }
-      const uint8_t* v = g.vc + vrow * D + L::kA * r;
-      const uint8_t* s = g.vs + vrow * (D / 32) + (L::kA * r) / 32;
+      const uint8_t* v = g.vc + vrow * D;
+      const uint8_t* s = g.vs + vrow * (D / 32);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        const uint8_t* a = v + j * D + L::kA * r;
         if constexpr (L::kA == 4) {
-          raw.v[j][0] = *reinterpret_cast<const uint32_t*>(v + j * D);
+          raw.v[j][0] = *reinterpret_cast<const uint32_t*>(a);
         } else if constexpr (L::kA == 8) {
-          const uint2 w = *reinterpret_cast<const uint2*>(v + j * D);
+          const uint2 w = *reinterpret_cast<const uint2*>(a);
           raw.v[j][0] = w.x; raw.v[j][1] = w.y;
         } else {
-          const uint4 w = *reinterpret_cast<const uint4*>(v + j * D);
+          const uint4 w = *reinterpret_cast<const uint4*>(a);
           raw.v[j][0] = w.x; raw.v[j][1] = w.y; raw.v[j][2] = w.z; raw.v[j][3] = w.w;
         }
-        raw.vs[j][0] = s[j * (D / 32)];
         if constexpr (L::kB) {
-          const uint8_t* e = g.vc + (vrow + j) * D + 16 * L::kA + L::kB * r;
+          const uint8_t* e = v + j * D + 16 * L::kA + L::kB * r;
           if constexpr (L::kB == 4) raw.v[j][L::kWordsA] = *reinterpret_cast<const uint32_t*>(e);
           else raw.v[j][L::kWordsA] = *reinterpret_cast<const uint16_t*>(e);
-          raw.vs[j][1] = g.vs[(vrow + j) * (D / 32) + (16 * L::kA + L::kB * r) / 32];
+        }
+        if constexpr (!SL::kWordsV) {
+          raw.vs[j] = s[j * (D / 32) + blk_a];
+          if constexpr (L::kB) raw.vs[8 + j] = s[j * (D / 32) + blk_b];
+        }
+      }
+      if constexpr (SL::kWordsV) {
+#pragma unroll
+        for (int w = 0; w < SL::kV / 4; ++w) {
+          const uint4 x = reinterpret_cast<const uint4*>(s)[w];
+          raw.vs[4 * w] = x.x; raw.vs[4 * w + 1] = x.y; raw.vs[4 * w + 2] = x.z; raw.vs[4 * w + 3] = x.w;
         }
       }
     }
-    if ((ga | gb) < 0) {           // keys of a bad page are NaN, and so is what sees them; values are masked below
+    if ((ga | gb) < 0) {           // keys of a bad page are NaN, and so is what sees them; its values count as 0
       const int grp = (r & 8) ? gb : ga;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
 #pragma unroll
         for (int u = 0; u < kFrags * 2; ++u) raw.k[t][u] = grp >= 0 ? raw.k[t][u] : 0x7F7F7F7Fu;
 #pragma unroll
-        for (int u = 0; u < kKS; ++u) raw.ks[t][u] = grp >= 0 ? raw.ks[t][u] : 127u;
+        for (int u = 0; u < SL::kK; ++u) raw.ks[t][u] = grp >= 0 ? raw.ks[t][u] : 0x7F7F7F7Fu;
       }
       const bool none = ((quarter & 2) ? gb : ga) < 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int w = 0; w < L::kWords; ++w) raw.v[j][w] = none ? 0u : raw.v[j][w];
 #pragma unroll
-        for (int w = 0; w < L::kScales; ++w) raw.vs[j][w] = none ? 127u : raw.vs[j][w];
-      }
+      for (int w = 0; w < SL::kV; ++w) raw.vs[w] = none ? 0x7F7F7F7Fu : raw.vs[w];
     }
   };
+  // scale operand of fragments 2 u, 2 u + 1 of tile t's keys; of key j's values, first or second run
+  auto k_scale = [&](const Raw& raw, int t, int u) -> uint32_t {
+    if constexpr (SL::kWordsK) {
+      const uint32_t w = raw.ks[t][u / 2];
+      return __builtin_amdgcn_alignbit(w, w, 16 * (u & 1) + 8 * (quarter >> 1) + 9);
+    } else {
+      return raw.ks[t][u] << 23;
+    }
+  };
+  auto v_scale = [&](const Raw& raw, int j, int run) -> uint32_t {
+    if constexpr (D == 64) return __builtin_amdgcn_alignbit(raw.vs[j / 2], raw.vs[j / 2], 16 * (j & 1) + 8 * blk_a + 9);
+    else if constexpr (D == 128) return __builtin_amdgcn_alignbit(raw.vs[j], raw.vs[j], 8 * blk_a + 9);
+    else return raw.vs[8 * run + j] << 23;
+  };
 
-  auto compute = [&](int key0) {
+  auto compute = [&](Raw& raw, int key0) {
     // ---- S^T
     v4f s[NQ][2];
 #pragma unroll
@@ -323,7 +368,7 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
       u32x4_t kf[kFrags];
 #pragma unroll
       for (int f = 0; f < kFrags; ++f) {
-        const uint32_t sc = raw.ks[t][f / 2] << 23;
+        const uint32_t sc = k_scale(raw, t, f / 2);
         kf[f] = u32x4_t{decode2<DT, false>(raw.k[t][2 * f], sc), decode2<DT, true>(raw.k[t][2 * f], sc),
                         decode2<DT, false>(raw.k[t][2 * f + 1], sc), decode2<DT, true>(raw.k[t][2 * f + 1], sc)};
       }
@@ -334,9 +379,37 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
         for (int f = 0; f < kFrags; ++f) s[n][t] = mfma16<DT>(kf[f], qf[n][f], s[n][t]);
       }
     }
+    uint32_t vsc[8][L::kScales];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int w = 0; w < L::kScales; ++w) vsc[j][w] = v_scale(raw, j, w);
+    // decodes channels of word w of the lane's run, all 8 keys, into two fragments
+    auto fragments = [&](int w, auto hi_half, u32x4_t& a, u32x4_t& c) {
+      constexpr bool HI = decltype(hi_half)::value;
+      const int run = L::kScales > 1 && w >= L::kWordsA ? 1 : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = decode2<DT, HI>(raw.v[2 * j][w], vsc[2 * j][run]);
+        const uint32_t y = decode2<DT, HI>(raw.v[2 * j + 1][w], vsc[2 * j + 1][run]);
+        a[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+        c[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+      }
+    };
+    auto for_tiles = [&](auto f) {   // f(tile, fragment)
+#pragma unroll
+      for (int w = 0; w < L::kWords; ++w) {
+        u32x4_t a, c;
+        fragments(w, std::false_type{}, a, c);
+        f(4 * w, a); f(4 * w + 1, c);
+        if (4 * w + 2 < kTiles) {
+          fragments(w, std::true_type{}, a, c);
+          f(4 * w + 2, a); f(4 * w + 3, c);
+        }
+      }
+    };
     // ---- masks: only a step that some row does not see whole needs them
-    const bool edge = key0 + 31 > wlast_min || key0 < wfirst_max || key0 + 32 > hi;
-    if (edge) {
+    if (key0 + 32 > all_to || key0 < all_from) {
       // key 8 quarter + j of the step is seen by row n iff unsigned(j - from) < many
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -347,13 +420,66 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
       }
       // values that no row sees may be anything; the weight 0 must not meet a NaN there
       const uint32_t from = uint32_t(lo - key0 - 8 * quarter), many = uint32_t(max(hi - lo, 0));
+      uint32_t nan = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const bool keep = uint32_t(j) - from < many;
 #pragma unroll
-        for (int w = 0; w < L::kWords; ++w) raw.v[j][w] = keep ? raw.v[j][w] : 0u;
+        for (int w = 0; w < L::kWords; ++w) {
+          raw.v[j][w] = keep ? raw.v[j][w] : 0u;
+          nan |= any_nan_code(raw.v[j][w]);
+        }
 #pragma unroll
-        for (int w = 0; w < L::kScales; ++w) raw.vs[j][w] = keep ? raw.vs[j][w] : 127u;
+        for (int w = 0; w < L::kScales; ++w) {
+          vsc[j][w] = keep ? vsc[j][w] : 127u << 23;
+          nan |= (vsc[j][w] & 0x7F800000u) == 0x7F800000u ? 1u : 0u;
+        }
+      }
+      // A NaN value that some rows see and others do not: 0 * NaN would reach them all.  Such values
+      // are taken out, and put into the outputs of the rows that see them where a product of marks
+      // (E4M3 1.0 at scale 1) and visibility finds any.
+      if (__ballot(nan != 0)) {
+        uint32_t clean[8][L::kWords], clean_sc[8][L::kScales];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+          for (int w = 0; w < L::kWords; ++w) {
+            const bool all = (vsc[j][L::kScales > 1 && w >= L::kWordsA ? 1 : 0] & 0x7F800000u) == 0x7F800000u;
+            const uint32_t mark = all ? 0x01010101u : any_nan_code(raw.v[j][w]) >> 7;    // 1 in every NaN byte
+            clean[j][w] = raw.v[j][w] & ~(mark * 255u);
+            raw.v[j][w] = mark * 0x38u;
+          }
+#pragma unroll
+          for (int w = 0; w < L::kScales; ++w) {
+            clean_sc[j][w] = (vsc[j][w] & 0x7F800000u) == 0x7F800000u ? 127u << 23 : vsc[j][w];
+            vsc[j][w] = 127u << 23;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          float e[8];
+          const uint32_t mine = uint32_t(first[n] - key0 - 8 * quarter);
+          const uint32_t seen = uint32_t(max(min(last[n], hi - 1) - first[n] + 1, 0));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = uint32_t(j) - mine < seen ? 1.0f : 0.0f;
+          const u32x4_t see = {pack2<DT>(e[0], e[1]), pack2<DT>(e[2], e[3]), pack2<DT>(e[4], e[5]), pack2<DT>(e[6], e[7])};
+          for_tiles([&](int t, u32x4_t a) {
+            const v4f hits = mfma16<DT>(a, see, v4f{0, 0, 0, 0});
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {        // a count: all bits of `any` set where it is not zero
+              const int any = -__float_as_int(hits[v]) >> 31;
+              o[n][t][v] = __uint_as_float(__float_as_uint(o[n][t][v]) | (uint32_t(any) & 0x7FC00000u));
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one tile at a time: this path shall cost no registers
+          });
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+          for (int w = 0; w < L::kWords; ++w) raw.v[j][w] = clean[j][w];
+#pragma unroll
+          for (int w = 0; w < L::kScales; ++w) vsc[j][w] = clean_sc[j][w];
+        }
       }
     }
     // ---- reference exponents
@@ -389,81 +515,6 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
       l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
       p[n] = u32x4_t{pack2<DT>(e[0], e[1]), pack2<DT>(e[2], e[3]), pack2<DT>(e[4], e[5]), pack2<DT>(e[6], e[7])};
     }
-    // channels 2 c, 2 c + 1 of the lane's run, all 8 keys
-    auto fragments = [&](int w, auto hi_half, u32x4_t& a, u32x4_t& c) {
-      constexpr bool HI = decltype(hi_half)::value;
-      const int sc = w >= L::kWordsA ? 1 : 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t x = decode2<DT, HI>(raw.v[2 * j][w], raw.vs[2 * j][L::kScales > 1 ? sc : 0] << 23);
-        const uint32_t y = decode2<DT, HI>(raw.v[2 * j + 1][w], raw.vs[2 * j + 1][L::kScales > 1 ? sc : 0] << 23);
-        a[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
-        c[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
-      }
-    };
-    auto for_tiles = [&](auto f) {   // f(tile, fragments) over pairs of tiles
-#pragma unroll
-      for (int w = 0; w < L::kWords; ++w) {
-        u32x4_t a, c;
-        fragments(w, std::false_type{}, a, c);
-        f(4 * w, a); f(4 * w + 1, c);
-        if (4 * w + 2 < kTiles) {
-          fragments(w, std::true_type{}, a, c);
-          f(4 * w + 2, a); f(4 * w + 3, c);
-        }
-      }
-    };
-    // A NaN value that some rows of the wave see and others do not: 0 * NaN would reach
-    // them all.  Such values are taken out, and put into the outputs of the rows that
-    // see them where a product of marks and visibility finds any.
-    if (edge) {
-      uint32_t nan = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-#pragma unroll
-        for (int w = 0; w < L::kWords; ++w)
-          nan |= any_nan_code(w >= L::kWordsA && L::kB == 2 ? raw.v[j][w] & 0xFFFFu : raw.v[j][w]);
-#pragma unroll
-        for (int w = 0; w < L::kScales; ++w) nan |= raw.vs[j][w] == 255u ? 1u : 0u;
-      }
-      if (__ballot(nan != 0)) {
-        Raw keep = raw;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-#pragma unroll
-          for (int w = 0; w < L::kWords; ++w) {
-            const uint32_t bytes = any_nan_code(raw.v[j][w]) >> 7;      // 1 in every NaN byte
-            const bool all = raw.vs[j][L::kScales > 1 && w >= L::kWordsA ? 1 : 0] == 255u;
-            const uint32_t mark = all ? 0x01010101u : bytes;
-            keep.v[j][w] = raw.v[j][w] & ~(mark * 255u);
-            raw.v[j][w] = mark * 0x38u;                                 // E4M3 1.0
-          }
-#pragma unroll
-          for (int w = 0; w < L::kScales; ++w) {
-            keep.vs[j][w] = raw.vs[j][w] == 255u ? 127u : raw.vs[j][w];
-            raw.vs[j][w] = 127u;
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          float e[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            e[j] = uint32_t(j) - uint32_t(first[n] - key0 - 8 * quarter) < uint32_t(max(min(last[n], hi - 1) - first[n] + 1, 0))
-                       ? 1.0f : 0.0f;
-          const u32x4_t see = {pack2<DT>(e[0], e[1]), pack2<DT>(e[2], e[3]), pack2<DT>(e[4], e[5]), pack2<DT>(e[6], e[7])};
-          for_tiles([&](int t, u32x4_t a) {
-            const v4f hits = mfma16<DT>(a, see, v4f{0, 0, 0, 0});
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {      // a count: all bits of `any` set where it is not zero
-              const int any = -__float_as_int(hits[v]) >> 31;
-              o[n][t][v] = __uint_as_float(__float_as_uint(o[n][t][v]) | (uint32_t(any) & 0x7FC00000u));
-            }
-          });
-        }
-        raw = keep;
-      }
-    }
     // ---- O^T
     for_tiles([&](int t, u32x4_t a) {
 #pragma unroll
@@ -471,93 +522,82 @@ __global__ __launch_bounds__(64 * NW) void attention_kernel(const AttnArgs g) {
     });
   };
 
-  for (int window0 = start; window0 < hi; window0 += 1024) {
-    groups = row_group(g, table, hk, window0 + lane * 16, lo, hi);
-    const int steps = (min(hi - window0, 1024) + 31) / 32;
+  const int steps = (hi - start + 31) / 32;
+  if (wave < steps) {
+    constexpr bool kAhead = D * NQ <= 256;       // two steps' bytes fit the registers
+    Raw raw;
+    if constexpr (kAhead) load(raw, wave);
     for (int step = wave; step < steps; step += NW) {
-      load(step);
-      compute(window0 + 32 * step);
+      if constexpr (kAhead) {
+        Raw next = raw;
+        if (step + NW < steps) load(next, step + NW);
+        compute(raw, start + 32 * step);
+        raw = next;
+      } else {
+        load(raw, step);
+        compute(raw, start + 32 * step);
+      }
     }
   }
 
-  // ---- sums over the quarters of a row's keys
+  // ---- join the waves: every wave brings its outputs to the common reference exponent
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     l[n] += __shfl_xor(l[n], 16, 64);
     l[n] += __shfl_xor(l[n], 32, 64);
+    if (quarter == 0) { lds.m[wave][n * 16 + r] = mref[n]; lds.l[wave][n * 16 + r] = l[n]; }
   }
-  // ---- waves that split the keys: join them
-  {
-    __shared__ float sm[NW][NQ * 16], sl[NW][NQ * 16];
-    __shared__ v4f so[NQ * kTiles][64];
-    if (quarter == 0) {
-#pragma unroll
-      for (int n = 0; n < NQ; ++n) { sm[wave][n * 16 + r] = mref[n]; sl[wave][n * 16 + r] = l[n]; }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      float top = kLowest, sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) top = fmaxf(top, sm[w][n * 16 + r]);
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float lw = sl[w][n * 16 + r];
-        if (lw != 0.0f) sum += lw * (sm[w][n * 16 + r] == top ? 1.0f : __builtin_amdgcn_exp2f(sm[w][n * 16 + r] - top));
-      }
-      const float a = mref[n] == top ? 1.0f : __builtin_amdgcn_exp2f(mref[n] - top);
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) o[n][t] *= a;
-      mref[n] = top;
-      l[n] = sum;
-    }
-    for (int w = 1; w < NW; ++w) {               // wave 0 adds the others in order
-      if (wave == w) {
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) so[n * kTiles + t][lane] = o[n][t];
-      }
-      __syncthreads();
-      if (wave == 0) {
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int t = 0; t < kTiles; ++t) o[n][t] += so[n * kTiles + t][lane];
-      }
-      __syncthreads();
-    }
-    if (wave != 0) return;
-  }
-
-  // ---- outputs: the lane holds channels kA (4 quarter + v) + t of the first run, likewise of the second
+  __syncthreads();
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    if (orow[n] < 0) continue;
-    const bool direct = g.splits == 1;
-    const float inv = direct ? (l[n] == 0.0f ? 0.0f : 1.0f / l[n]) : 1.0f;
-    auto put = [&](int base, int width, int tile0, auto kWidth) {
-      constexpr int W = decltype(kWidth)::value;
+    float top = kLowest;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int64_t d = base + W * (4 * quarter + v);
-        if (direct) {
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, lds.m[w][n * 16 + r]);
+    const float a = mref[n] == top ? 1.0f : __builtin_amdgcn_exp2f(mref[n] - top);
+    // the lane holds channels kA (4 quarter + v) + t of the first run, likewise of the second
+    float* dst = lds.o[wave][n * 16 + r];
 #pragma unroll
-          for (int t = 0; t < W; t += 2)
-            *reinterpret_cast<uint32_t*>(static_cast<T*>(g.out) + orow[n] * D + d + t) =
-                pack2<DT>(o[n][tile0 + t][v] * inv, o[n][tile0 + t + 1][v] * inv);
-        } else {
-          float* dst = g.part + (orow[n] * g.splits + split) * D + d;
+    for (int v = 0; v < 4; ++v) {
 #pragma unroll
-          for (int t = 0; t < W; t += 2)
-            *reinterpret_cast<float2*>(dst + t) = make_float2(o[n][tile0 + t][v], o[n][tile0 + t + 1][v]);
-        }
-      }
-    };
-    put(0, L::kA, 0, std::integral_constant<int, L::kA>{});
-    if constexpr (L::kB) put(16 * L::kA, L::kB, L::kA, std::integral_constant<int, L::kB>{});
-    if (quarter == 0) put_stats<DT>(g, orow[n], split, mref[n], l[n]);
+      for (int t = 0; t < L::kA; t += 4)
+        *reinterpret_cast<v4f*>(dst + L::kA * (4 * quarter + v) + t) =
+            v4f{o[n][t][v], o[n][t + 1][v], o[n][t + 2][v], o[n][t + 3][v]} * a;
+      if constexpr (L::kB == 4)
+        *reinterpret_cast<v4f*>(dst + 16 * L::kA + 4 * (4 * quarter + v)) =
+            v4f{o[n][L::kA][v], o[n][L::kA + 1][v], o[n][L::kA + 2][v], o[n][L::kA + 3][v]} * a;
+      if constexpr (L::kB == 2)
+        *reinterpret_cast<v2f*>(dst + 16 * L::kA + 2 * (4 * quarter + v)) = v2f{o[n][L::kA][v], o[n][L::kA + 1][v]} * a;
+    }
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * NW) {
+    const int row = i / (D / 4), d = i % (D / 4) * 4;
+    float top = kLowest, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, lds.m[w][row]);
+    v4f x = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float lw = lds.l[w][row];
+      if (lw != 0.0f) sum += lw * (lds.m[w][row] == top ? 1.0f : __builtin_amdgcn_exp2f(lds.m[w][row] - top));
+      x += *reinterpret_cast<const v4f*>(&lds.o[w][row][d]);
+    }
+    const int64_t to = (t0 + row / G) * g.heads + hk * G + row % G;
+    if (g.splits == 1) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      *reinterpret_cast<u32x2_t*>(static_cast<T*>(g.out) + to * D + d) =
+          u32x2_t{pack2<DT>(x[0] * inv, x[1] * inv), pack2<DT>(x[2] * inv, x[3] * inv)};
+    } else {
+      *reinterpret_cast<v4f*>(g.part + (to * g.splits + split) * D + d) = x;
+    }
+    if (d == 0) put_stats<DT>(g, to, split, top, sum);
+  }
+}
+
+template <int DT, int D, int NQ, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void attention_few_kernel(const AttnArgs g) {
+  __shared__ FewLds<D, NQ, NW> lds;
+  few_rows<DT, D, NQ, NW>(g, blockIdx.x, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -590,24 +630,29 @@ __device__ __forceinline__ v16f_t mfma32(u32x4_t a, u32x4_t b, v16f_t acc) {
 //     16-key step are keys 8 h .. 8 h + 7, the ones it feeds as P^T.
 //   - fragments are 1040 bytes apart: lanes that write 8 fragments of one key then
 //     meet 8 different groups of banks.
+template <int D> struct TileLds {
+  static constexpr int kFrag = 1040;
+  alignas(16) uint8_t codes[2][D / 4 * kFrag];
+  int nan_tile[2][4];
+};
+
 template <int DT, int D, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_tile_kernel(const AttnArgs g) {
+__device__ __forceinline__ void tile_rows(const AttnArgs& g, int64_t b, TileLds<D>& shared) {
   using L = Deal32<D>;
   using T = uint16_t;
   constexpr int kSteps = D / 16;                 // K steps of S^T
   constexpr int kTiles = D / 32;                 // 32-channel tiles of O^T
-  constexpr int kFrag = 1040;
+  constexpr int kFrag = TileLds<D>::kFrag;
   constexpr int kFragsK = 2 * kSteps, kFrags = kFragsK + 4 * kTiles;
   constexpr int kRows = 32 * NW;
   constexpr int kKLoads = (D + 63) / 64;         // 16-byte loads of a lane for 16 keys
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kFrags * kFrag];
-  __shared__ int nan_tile[2][4];
+  auto& lds = shared.codes;
+  auto& nan_tile = shared.nan_tile;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = wave & 3;                     // row group of a tile that this wave decodes
   const bool decodes_k = NW == 4 || wave < 4, decodes_v = NW == 4 || wave >= 4;
   const int r = lane & 31, h = lane >> 5;
 
-  int64_t b = blockIdx.x;
   const int hk = int(b % g.kv_heads); b /= g.kv_heads;
   const int split = int(b % g.splits); b /= g.splits;
   const int rt = int(b % g.row_tiles);
@@ -617,9 +662,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
   const int64_t t1 = min(max(int64_t(g.cu[req + 1]), t0), g.tokens);
   const int m = int(t1 - t0), kv = max(g.lens[req], 0);
   const int64_t rows = int64_t(m) * G, row0 = int64_t(rt) * kRows;
-  if (rows <= kFewRows || row0 >= rows) return;  // requests of few rows are attention_kernel's
+  if (rows <= kFewRows || row0 >= rows) return;  // requests of few rows are few_rows' own
   if (m > g.max_q || kv > g.max_kv) {            // not what the grid was sized for
-    refuse_request<DT, D>(g, t0, rows, hk, rt, split);
+    if (rt == 0) refuse_request<DT, D>(g, t0, rows, hk, split);
     return;
   }
   const int i0 = int(row0 / G), i1 = int((min(row0 + kRows, rows) - 1) / G);
@@ -933,41 +978,75 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4,
   if (h == 0) put_stats<DT>(g, orow, split, mref, l);
 }
 
+// Requests of many rows, and in the same launch, behind them, the others of the call.
+template <int DT, int D, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_tile_kernel(const AttnArgs g) {
+  __shared__ union { TileLds<D> tile; FewLds<D, 2, NW> few; } lds;
+  if (int64_t(blockIdx.x) < g.tile_blocks) tile_rows<DT, D, NW>(g, blockIdx.x, lds.tile);
+  else few_rows<DT, D, 2, NW>(g, blockIdx.x - g.tile_blocks, lds.few);
+}
+
 // Joins the splits of one row: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
-// One wave per row; a lane takes channels 2 lane, 2 lane + 1 of each 128.
-template <int DT, int D>
+// WPR waves per row take every WPR-th split; a lane takes channels 2 lane, 2 lane + 1 of
+// each 128.  Outputs of splits without keys were never written: they are loaded with the
+// others (the loads need no waiting between them) and dropped.
+template <int DT, int D, int WPR>
 __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs g, int64_t requests) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (row >= g.tokens * g.heads) return;
-  const int64_t token = row / g.heads;
-  if (token < g.cu[0] || token >= g.cu[requests]) return;
-  const float* ml = g.part_ml + row * g.splits * 2;
-  float top = kLowest;
-  for (int i = lane; i < g.splits; i += 64)
-    if (ml[2 * i + 1] != 0.0f) top = fmaxf(top, ml[2 * i]);
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-  float sum = 0.0f;
   constexpr int kPer = (D + 127) / 128;
+  __shared__ v2f part[4][kPer][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave % WPR;
+  const int64_t row = int64_t(blockIdx.x) * (4 / WPR) + wave / WPR;
+  const int64_t token = row / g.heads;
+  const bool mine = row < g.tokens * g.heads && token >= g.cu[0] && token < g.cu[requests];
+  if (WPR == 1 && !mine) return;
   v2f acc[kPer];
 #pragma unroll
   for (int u = 0; u < kPer; ++u) acc[u] = v2f{0, 0};
-  for (int i = 0; i < g.splits; ++i) {
-    const float li = ml[2 * i + 1], mi = ml[2 * i];
-    if (li == 0.0f) continue;
-    const float w = mi == top ? 1.0f : __builtin_amdgcn_exp2f(mi - top);
-    sum += w * li;
-    const float* o = g.part + (row * g.splits + i) * D;
+  float top = kLowest, sum = 0.0f;
+  if (mine) {
+    const float* ml = g.part_ml + row * g.splits * 2;
+    for (int i = lane; i < g.splits; i += 64)
+      if (ml[2 * i + 1] != 0.0f) top = fmaxf(top, ml[2 * i]);
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int d = u * 128 + 2 * lane;
-      if (d < D) {
-        const float2 x = *reinterpret_cast<const float2*>(o + d);
-        acc[u][0] += w * x.x;
-        acc[u][1] += w * x.y;
+    for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    for (int i0 = 0; i0 < g.splits; i0 += 64) {
+      // lane i holds the weight of split i0 + i
+      float w = 0.0f, li = 0.0f;
+      if (i0 + lane < g.splits) {
+        li = ml[2 * (i0 + lane) + 1];
+        const float mi = ml[2 * (i0 + lane)];
+        w = li == 0.0f ? 0.0f : mi == top ? 1.0f : __builtin_amdgcn_exp2f(mi - top);
+        li = li == 0.0f ? 0.0f : w * li;
+      }
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) li += __shfl_xor(li, off, 64);
+      sum += li;
+      const int n = min(g.splits - i0, 64);
+      const float* o = g.part + (row * g.splits + i0) * D;
+#pragma unroll 4
+      for (int i = sub; i < n; i += WPR) {
+        const float wi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), i));
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          const int d = u * 128 + 2 * lane;
+          if (d < D) {
+            const float2 x = *reinterpret_cast<const float2*>(o + i * D + d);
+            acc[u][0] += wi == 0.0f ? 0.0f : wi * x.x;
+            acc[u][1] += wi == 0.0f ? 0.0f : wi * x.y;
+          }
+        }
       }
     }
+  }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) part[wave][u][lane] = acc[u];
+    __syncthreads();
+    if (sub != 0 || !mine) return;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+#pragma unroll
+      for (int w = 1; w < WPR; ++w) acc[u] += part[wave + w][u][lane];
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -983,15 +1062,12 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs g, i
 // Host
 // ---------------------------------------------------------------------------
 struct Plan {
-  int nq;                       // 16-row tiles of attention_kernel
+  int nq;                       // 16-row tiles of attention_few_kernel
   bool tiles;                   // some request may have more than kFewRows rows
-  bool few;                     // some request may have no more
-  int64_t row_tiles, tile_rows; // of attention_tile_kernel
+  int64_t row_tiles;            // of a request of many rows
   int64_t splits, chunk;
   int64_t bytes;                // workspace
 };
-
-constexpr int kWaves = 4;
 
 mx_status_t plan_attention(int64_t tokens, int heads, int kv_heads, int dim, int64_t requests, int64_t max_q,
                            int64_t max_kv, int64_t window, Plan& p) {
@@ -1003,45 +1079,52 @@ mx_status_t plan_attention(int64_t tokens, int heads, int kv_heads, int dim, int
   const int64_t cus = device_cus();
   if (cus <= 0) return MX_ERR_LAUNCH;
   const int64_t group = heads / kv_heads, reqs = std::max<int64_t>(requests, 1);
-  const int64_t rows = std::max<int64_t>(std::min(max_q, tokens) * group, 1);
+  max_q = std::min(max_q, tokens);
+  const int64_t rows = std::max<int64_t>(max_q * group, 1);
   p.tiles = rows > kFewRows;
-  p.few = !p.tiles || requests > 1;
-  p.nq = std::min<int64_t>(rows, p.tiles ? kFewRows : rows) <= 16 ? 1 : 2;
-  p.tile_rows = dim > 128 ? 128 : 256;
-  p.row_tiles = p.tiles ? (rows + p.tile_rows - 1) / p.tile_rows : 1;
-  // keys that one row tile can see
+  p.nq = rows <= 16 ? 1 : 2;
+  const int64_t tile_rows = dim > 128 ? 128 : 256;
+  p.row_tiles = p.tiles ? (rows + tile_rows - 1) / tile_rows : 0;
+  // keys that one workgroup's rows can see
   int64_t keys = max_kv;
-  if (window > 0) keys = std::min(keys, window + (p.tiles ? p.tile_rows : kFewRows) / group + 33);
+  if (window > 0) keys = std::min(keys, window + (p.tiles ? tile_rows : kFewRows) / group + 33);
   keys = std::max<int64_t>((keys + 31) / 32 * 32, 32);
-  // Splits: enough workgroups for three of attention_kernel on every CU, or one and a half of
-  // attention_tile_kernel (one fits a CU), but none with less than two steps a wave or four tiles.
-  const int64_t base = p.tiles ? std::min(reqs * p.row_tiles, tokens * group / p.tile_rows + reqs) * kv_heads
-                               : reqs * kv_heads;
-  const int64_t want = std::max<int64_t>(1, (p.tiles ? cus + cus / 2 : 3 * cus) / base);
+  // Splits.  Requests of many rows: one workgroup and a half for every CU (one fits); if all other
+  // requests have one token, (tokens - requests) / (max_q - 1) of them have many.  Requests of few
+  // rows: kFewPerCu for every CU, two at a time, so that uneven lengths even out.  No split has less
+  // than 256 keys, two steps for each of four waves.
+  int64_t want = 1;
+  if (p.tiles) {
+    const int64_t many = std::max<int64_t>(1, std::min(reqs, (tokens - reqs + max_q - 2) / std::max<int64_t>(max_q - 1, 1)));
+    want = (cus + cus / 2) / (many * p.row_tiles * kv_heads);
+  }
+  if (!p.tiles || reqs > 1) want = std::max(want, (kFewPerCu * cus + reqs * kv_heads - 1) / (reqs * kv_heads));
+  if (p.tiles) want = std::min<int64_t>(want, 8);
+  want = std::max<int64_t>(want, 1);
   p.chunk = std::max<int64_t>((keys + want - 1) / want, 256);
   p.chunk = (p.chunk + 127) / 128 * 128;
   p.splits = (keys + p.chunk - 1) / p.chunk;
   p.bytes = p.splits > 1 ? tokens * heads * p.splits * (dim + 2) * 4 : 0;
-  if (reqs * kv_heads * p.row_tiles > 0x7FFFFFFF / p.splits) return MX_ERR_SHAPE;
+  if (reqs * kv_heads * (p.row_tiles + 1) > 0x7FFFFFFF / p.splits) return MX_ERR_SHAPE;
   return MX_OK;
 }
 
 template <int DT, int D>
 void launch_attention(const Plan& p, AttnArgs g, int64_t requests, hipStream_t stream) {
+  const int64_t per_tile = requests * g.kv_heads * p.splits;
   if (p.tiles) {
     constexpr int NW = D > 128 ? 4 : 8;
-    const unsigned grid = unsigned(requests * g.kv_heads * p.row_tiles * p.splits);
-    attention_tile_kernel<DT, D, NW><<<grid, 64 * NW, 0, stream>>>(g);
+    g.tile_blocks = per_tile * p.row_tiles;
+    g.few_only = true;
+    attention_tile_kernel<DT, D, NW><<<unsigned(g.tile_blocks + per_tile), 64 * NW, 0, stream>>>(g);
+  } else if (p.nq == 1) {
+    attention_few_kernel<DT, D, 1, 4><<<unsigned(per_tile), 256, 0, stream>>>(g);
+  } else {
+    attention_few_kernel<DT, D, 2, 4><<<unsigned(per_tile), 256, 0, stream>>>(g);
   }
-  if (p.few) {
-    g.few_only = p.tiles;
-    g.row_tiles = 1;
-    const unsigned grid = unsigned(requests * g.kv_heads * p.splits);
-    if (p.nq == 1) attention_kernel<DT, D, 1, kWaves><<<grid, 64 * kWaves, 0, stream>>>(g);
-    else attention_kernel<DT, D, 2, kWaves><<<grid, 64 * kWaves, 0, stream>>>(g);
-  }
-  if (p.splits > 1)
-    attention_join_kernel<DT, D><<<unsigned((g.tokens * g.heads + 3) / 4), 256, 0, stream>>>(g, requests);
+  const int64_t rows = g.tokens * g.heads;
+  if (p.splits >= 8) attention_join_kernel<DT, D, 4><<<unsigned(rows), 256, 0, stream>>>(g, requests);
+  else if (p.splits > 1) attention_join_kernel<DT, D, 1><<<unsigned((rows + 3) / 4), 256, 0, stream>>>(g, requests);
 }
 
 }  // namespace mxk
@@ -1073,7 +1156,8 @@ extern "C" mx_status_t mx_paged_attention(const void* q, mx_dtype_t dtype, int64
   if (tokens == 0 || requests == 0) return MX_OK;
   if (!q || !cu || !lens || !out || (max_kv > 0 && !page_table)) return MX_ERR_NULL;
   if (cache->pages > 0 && (!cache->k || !cache->k_scales || !cache->v || !cache->v_scales)) return MX_ERR_NULL;
-  if (misaligned(q) || misaligned(out) || misaligned(cache->k) || misaligned(cache->v) || misaligned(workspace) ||
+  if (misaligned(q) || misaligned(out) || misaligned(cache->k) || misaligned(cache->v) ||
+      misaligned(cache->k_scales) || misaligned(cache->v_scales) || misaligned(workspace) ||
       (q_token_stride | q_head_stride) % 8)
     return MX_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(cu) | reinterpret_cast<uintptr_t>(lens) |

@@ -466,7 +466,8 @@ extern "C" mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dty
   const int size = elem_size(dtype);
   const uintptr_t kv = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
   if (kv % size || misaligned(table) || (reinterpret_cast<uintptr_t>(pos) & 3u) ||
-      (reinterpret_cast<uintptr_t>(slots) & 7u) || misaligned(cache->k) || misaligned(cache->v))
+      (reinterpret_cast<uintptr_t>(slots) & 7u) || misaligned(cache->k) || misaligned(cache->v) ||
+      misaligned(cache->k_scales) || misaligned(cache->v_scales))
     return MX_ERR_ALIGN;
   if (q && (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out)) % size) return MX_ERR_ALIGN;
   AppendArgs g = {};
