@@ -433,11 +433,12 @@ mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dtype, int64_t
  *   q      [tokens][heads][dim] BF16 or F16, 16-byte aligned rows (strides multiples of
  *          8 elements); heads a multiple of kv_heads.
  *   page_table  int32 [requests][table_cols], row stride table_stride; entries past a
- *          request's length, or before its window, are not read.  A query that sees a
+ *          request's length, or before its window, may hold anything.  A query that sees a
  *          token whose page number is outside [0, pages) or whose place is past
  *          table_cols gives NaN.
  *   cu     int32 [requests + 1], non-decreasing; tokens outside every request keep
  *          what out and lse held.
+ *          At most 65535 requests.
  *   max_q, max_kv  upper bounds of cu[r + 1] - cu[r] and lens[r] (host values: they
  *          size the grid).  A request that exceeds one of them gives NaN.
  *   out    [tokens][heads][dim] contiguous, type of q, 16-byte aligned; lse FP32

@@ -49,8 +49,15 @@ template <int DT> constexpr float kLift = DT == IN_F16 ? 7.0f : 0.0f;
 
 // Requests of up to so many rows (tokens x group) are taken by workgroups whose waves split the keys.
 constexpr int kFewRows = 32;
-constexpr int64_t kFewPerCu = 8;
 
+// Grid: x = kv head, y = request, z = split (and row tile).  The kv head runs
+// fastest: neighbouring workgroups go to different XCDs, so with 8 kv heads each
+// XCD's L2 serves one head's pages.
+//
+// A decoding call on short contexts is bound by latency: dependent loads, and code
+// that no workgroup has run yet comes from L2 at some 20 clocks an instruction.  So
+// what a workgroup runs once is kept short: no integer division (reciprocals come
+// from the host), the page numbers are read beside the lengths and not after them.
 struct AttnArgs {
   const void* q;
   int64_t q_ts, q_hs;
@@ -68,9 +75,10 @@ struct AttnArgs {
   int heads, kv_heads, group, page;
   int window;                   // 0: none
   int row_tiles, splits, chunk; // keys of a split, a multiple of 32
+  float inv_group;              // 1 / group
+  double inv_page16;            // 16 / page
   float c;                      // scale * log2(e)
-  int64_t tile_blocks;          // workgroups of attention_tile_kernel that take requests of many rows
-  bool few_only;                // few_rows leaves requests of more than kFewRows rows to them
+  bool few_only;                // few_rows leaves requests of more than kFewRows rows to tile_rows
 };
 
 template <int DT>
@@ -111,16 +119,22 @@ __device__ __forceinline__ uint32_t any_nan_code(uint32_t w) {   // nonzero if a
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
-// Row group (16 rows of one page and head) of keys key .. key + 15: -1 where no row sees them (not
-// read), -2 where the page number or its place is out of range.
-__device__ __forceinline__ int row_group(const AttnArgs& g, const int32_t* __restrict__ table, int hk, int key, int lo,
-                                         int hi) {
+// Page table column of a key: floor(x / d) as (x + 1/2) / d in FP64 (x < 2^27).
+__device__ __forceinline__ int page_column(const AttnArgs& g, int key) {
+  return int((double(key >> 4) + 0.5) * g.inv_page16);
+}
+
+// Entry of a column of a request's row of the page table; -1 past its end.
+__device__ __forceinline__ int page_entry(const AttnArgs& g, const int32_t* __restrict__ table, int col) {
+  return col < g.table_cols ? table[col] : -1;
+}
+
+// Row group (16 rows of one page and head) of keys key .. key + 15 in page `entry`, column col: -1
+// where no row sees them (not read), -2 where the page number is out of range.
+__device__ __forceinline__ int row_group(const AttnArgs& g, int hk, int key, int col, int entry, int lo, int hi) {
   if (key >= hi || key + 16 <= lo) return -1;
-  const int col = key / g.page;
-  if (col >= g.table_cols) return -2;
-  const int32_t p = table[col];
-  if (p < 0 || p >= g.pages) return -2;
-  return int((int64_t(p) * g.kv_heads + hk) * (g.page / 16) + (key - col * g.page) / 16);
+  if (entry < 0 || entry >= g.pages) return -2;
+  return (entry * g.kv_heads + hk) * (g.page >> 4) + ((key - col * g.page) >> 4);
 }
 
 // NaN for all rows of one kv head of a request that exceeds what the caller announced.
@@ -187,7 +201,7 @@ template <int D, int NQ, int NW> struct FewLds {
 // w, w + NW, ... of the split: no wave waits for another before the end.  The next
 // step's bytes are loaded while this one is computed.
 template <int DT, int D, int NQ, int NW>
-__device__ __forceinline__ void few_rows(const AttnArgs& g, int64_t block, FewLds<D, NQ, NW>& lds) {
+__device__ __forceinline__ void few_rows(const AttnArgs& g, int split, FewLds<D, NQ, NW>& lds) {
   using L = Deal<D>;
   using SL = ScaleLoad<D>;
   using T = uint16_t;
@@ -197,18 +211,15 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int64_t block, FewLd
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, quarter = lane >> 4;
 
-  // the kv head runs fastest over the grid: neighbouring workgroups go to different
-  // XCDs, so with 8 kv heads each XCD's L2 serves one head's pages
-  const int hk = int(block % g.kv_heads); block /= g.kv_heads;
-  const int split = int(block % g.splits);
-  const int64_t req = block / g.splits;
-  const int G = g.group;
-
-  const int64_t t0 = min(max(int64_t(g.cu[req]), int64_t(0)), g.tokens);
-  const int64_t t1 = min(max(int64_t(g.cu[req + 1]), t0), g.tokens);
-  const int m = int(t1 - t0), kv = max(g.lens[req], 0);
-  if (g.few_only && int64_t(m) * G > kFewRows) return;     // attention_tile_kernel's own
-  if (m > g.max_q || kv > g.max_kv) {            // not what the grid was sized for
+  const int hk = blockIdx.x, req = blockIdx.y, G = g.group;
+  const int32_t* table = g.table + req * g.table_stride;
+  // without a window the split's first key does not depend on the length: its pages come meanwhile
+  int key = split * g.chunk + lane * 16, col = page_column(g, key);
+  int entry = page_entry(g, table, col);
+  const int t0 = min(max(g.cu[req], 0), int(g.tokens)), t1 = min(max(g.cu[req + 1], t0), int(g.tokens));
+  const int m = t1 - t0, kv = max(g.lens[req], 0);
+  if (g.few_only && int64_t(m) * G > kFewRows) return;     // tile_rows' own
+  if (__builtin_expect(m > g.max_q || kv > g.max_kv, 0)) {   // not what the grid was sized for
     refuse_request<DT, D>(g, t0, int64_t(m) * G, hk, split);
     return;
   }
@@ -218,23 +229,24 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int64_t block, FewLd
   const int hi_all = kv;
   const int lo = g.window ? max(kv - m - g.window + 1, 0) : 0;
   const int64_t start64 = int64_t(lo & ~31) + int64_t(split) * g.chunk;
-  if (split > 0 && start64 >= hi_all) {
+  if (__builtin_expect(split > 0 && start64 >= hi_all, 0)) {
     empty_split(g, t0, 0, rows, hk, split);
     return;
   }
   const int start = int(start64), hi = int(min(int64_t(hi_all), start64 + g.chunk));
 
   // this lane's rows: where q is, and the keys (first, last] a row sees
-  int last[NQ], first[NQ];
+  int last[NQ], first[NQ], orow[NQ];
   u32x4_t qf[NQ][kFrags];
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     const int row = n * 16 + r;
     const int rr = min(row, rows - 1);
-    const int i = rr / G, head = hk * G + (rr - i * G);
+    const int i = int((float(rr) + 0.5f) * g.inv_group), head = hk * G + (rr - i * G);   // rr < 32: exact
+    orow[n] = (t0 + i) * g.heads + head;
     last[n] = row < rows ? kv - m + i : -1;
     first[n] = g.window ? max(kv - m + i - g.window + 1, 0) : 0;
-    const T* q = static_cast<const T*>(g.q) + (t0 + i) * g.q_ts + head * g.q_hs;
+    const T* q = static_cast<const T*>(g.q) + int64_t(t0 + i) * g.q_ts + head * g.q_hs;
 #pragma unroll
     for (int s = 0; s < kFrags; ++s) {
       const int d = s / 2 * 64 + (s / 2 * 2 + 1 < kFrags ? 16 * quarter + 8 * (s & 1) : 8 * quarter);
@@ -260,16 +272,23 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int64_t block, FewLd
     uint32_t v[8][L::kWords], vs[SL::kV];
   };
   // row group of keys 16 i .. 16 i + 15 of the current window of 1024 keys, held by lane i
-  int groups = -1, window = -1;
-  const int32_t* table = g.table + req * g.table_stride;
+  int window = 0;
+  if (g.window) {
+    key = start + lane * 16;
+    col = page_column(g, key);
+    entry = page_entry(g, table, col);
+  }
+  int groups = row_group(g, hk, key, col, entry, lo, hi);
   const int blk_a = (L::kA * r) / 32, blk_b = (16 * L::kA + L::kB * r) / 32;   // blocks of the lane's runs
   auto load = [&](Raw& raw, int step) {
-    if (step >> 5 != window) {
+    if (__builtin_expect(step >> 5 != window, 0)) {
       window = step >> 5;
-      groups = row_group(g, table, hk, start + 1024 * window + lane * 16, lo, hi);
+      key = start + 1024 * window + lane * 16;
+      col = page_column(g, key);
+      groups = row_group(g, hk, key, col, page_entry(g, table, col), lo, hi);
     }
     const int ga = __builtin_amdgcn_readlane(groups, 2 * (step & 31)), gb = __builtin_amdgcn_readlane(groups, 2 * (step & 31) + 1);
-    if ((ga & gb) >= 0) {          // a group that is not read borrows the other's addresses
+    if (__builtin_expect((ga & gb) >= 0, 1)) {   // a group that is not read borrows the other's addresses
       const int64_t a16 = int64_t(ga < 0 ? gb : ga) * 16, b16 = int64_t(gb < 0 ? ga : gb) * 16;
       const int64_t krow = ((r & 8) ? b16 : a16) + 8 * ((r >> 2) & 1) + (r & 3);
       const int64_t vrow = ((quarter & 2) ? b16 : a16) + 8 * (quarter & 1);
@@ -327,7 +346,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int64_t block, FewLd
         }
       }
     }
-    if ((ga | gb) < 0) {           // keys of a bad page are NaN, and so is what sees them; its values count as 0
+    if (__builtin_expect((ga | gb) < 0, 0)) {    // keys of a bad page are NaN, and so is what sees them; its values count as 0
       const int grp = (r & 8) ? gb : ga;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -438,7 +457,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int64_t block, FewLd
       // A NaN value that some rows see and others do not: 0 * NaN would reach them all.  Such values
       // are taken out, and put into the outputs of the rows that see them where a product of marks
       // (E4M3 1.0 at scale 1) and visibility finds any.
-      if (__ballot(nan != 0)) {
+      if (__builtin_expect(__ballot(nan != 0) != 0, 0)) {
         uint32_t clean[8][L::kWords], clean_sc[8][L::kScales];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -524,12 +543,12 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int64_t block, FewLd
 
   const int steps = (hi - start + 31) / 32;
   if (wave < steps) {
-    constexpr bool kAhead = D * NQ <= 256;       // two steps' bytes fit the registers
+    constexpr bool kAhead = D * NQ <= 128;       // two steps' bytes fit the registers
     Raw raw;
     if constexpr (kAhead) load(raw, wave);
     for (int step = wave; step < steps; step += NW) {
       if constexpr (kAhead) {
-        Raw next = raw;
+        Raw next;                                // not from raw: that would wait for raw's loads
         if (step + NW < steps) load(next, step + NW);
         compute(raw, start + 32 * step);
         raw = next;
@@ -550,10 +569,24 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int64_t block, FewLd
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    float top = kLowest;
+    // quarter i reads waves i, i + 4, ...
+    float mw[NW / 4], lw[NW / 4], top = kLowest, sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) top = fmaxf(top, lds.m[w][n * 16 + r]);
-    const float a = mref[n] == top ? 1.0f : __builtin_amdgcn_exp2f(mref[n] - top);
+    for (int k = 0; k < NW / 4; ++k) {
+      mw[k] = lds.m[quarter + 4 * k][n * 16 + r];
+      lw[k] = lds.l[quarter + 4 * k][n * 16 + r];
+      top = fmaxf(top, mw[k]);
+    }
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+#pragma unroll
+    for (int k = 0; k < NW / 4; ++k)
+      sum += lw[k] == 0.0f ? 0.0f : mw[k] == top ? lw[k] : lw[k] * __builtin_amdgcn_exp2f(mw[k] - top);
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+    float a = mref[n] == top ? 1.0f : __builtin_amdgcn_exp2f(mref[n] - top);
+    if (g.splits == 1) a = sum == 0.0f ? 0.0f : a * __builtin_amdgcn_rcpf(sum);
+    if (wave == 0 && quarter == 0 && n * 16 + r < rows) put_stats<DT>(g, orow[n], split, top, sum);
     // the lane holds channels kA (4 quarter + v) + t of the first run, likewise of the second
     float* dst = lds.o[wave][n * 16 + r];
 #pragma unroll
@@ -572,32 +605,22 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int64_t block, FewLd
   __syncthreads();
   for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * NW) {
     const int row = i / (D / 4), d = i % (D / 4) * 4;
-    float top = kLowest, sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) top = fmaxf(top, lds.m[w][row]);
     v4f x = {0, 0, 0, 0};
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float lw = lds.l[w][row];
-      if (lw != 0.0f) sum += lw * (lds.m[w][row] == top ? 1.0f : __builtin_amdgcn_exp2f(lds.m[w][row] - top));
-      x += *reinterpret_cast<const v4f*>(&lds.o[w][row][d]);
-    }
-    const int64_t to = (t0 + row / G) * g.heads + hk * G + row % G;
-    if (g.splits == 1) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      *reinterpret_cast<u32x2_t*>(static_cast<T*>(g.out) + to * D + d) =
-          u32x2_t{pack2<DT>(x[0] * inv, x[1] * inv), pack2<DT>(x[2] * inv, x[3] * inv)};
-    } else {
+    for (int w = 0; w < NW; ++w) x += *reinterpret_cast<const v4f*>(&lds.o[w][row][d]);
+    const int at = int((float(row) + 0.5f) * g.inv_group);
+    const int64_t to = int64_t(t0 + at) * g.heads + hk * G + (row - at * G);
+    if (g.splits == 1)
+      *reinterpret_cast<u32x2_t*>(static_cast<T*>(g.out) + to * D + d) = u32x2_t{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])};
+    else
       *reinterpret_cast<v4f*>(g.part + (to * g.splits + split) * D + d) = x;
-    }
-    if (d == 0) put_stats<DT>(g, to, split, top, sum);
   }
 }
 
 template <int DT, int D, int NQ, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void attention_few_kernel(const AttnArgs g) {
   __shared__ FewLds<D, NQ, NW> lds;
-  few_rows<DT, D, NQ, NW>(g, blockIdx.x, lds);
+  few_rows<DT, D, NQ, NW>(g, blockIdx.z, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -637,7 +660,7 @@ template <int D> struct TileLds {
 };
 
 template <int DT, int D, int NW>
-__device__ __forceinline__ void tile_rows(const AttnArgs& g, int64_t b, TileLds<D>& shared) {
+__device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared) {
   using L = Deal32<D>;
   using T = uint16_t;
   constexpr int kSteps = D / 16;                 // K steps of S^T
@@ -653,21 +676,19 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int64_t b, TileLds<
   const bool decodes_k = NW == 4 || wave < 4, decodes_v = NW == 4 || wave >= 4;
   const int r = lane & 31, h = lane >> 5;
 
-  const int hk = int(b % g.kv_heads); b /= g.kv_heads;
-  const int split = int(b % g.splits); b /= g.splits;
-  const int rt = int(b % g.row_tiles);
-  const int64_t req = b / g.row_tiles;
-  const int G = g.group;
+  const int hk = blockIdx.x, req = blockIdx.y, G = g.group;
+  const int rt = g.row_tiles - 1 - blockIdx.z / g.splits;   // the last rows see most keys: they begin first
+  const int split = blockIdx.z % g.splits;
   const int64_t t0 = min(max(int64_t(g.cu[req]), int64_t(0)), g.tokens);
   const int64_t t1 = min(max(int64_t(g.cu[req + 1]), t0), g.tokens);
   const int m = int(t1 - t0), kv = max(g.lens[req], 0);
-  const int64_t rows = int64_t(m) * G, row0 = int64_t(rt) * kRows;
+  const int rows = int(min(int64_t(m) * G, int64_t(0x7FFFFFFF))), row0 = rt * kRows;
   if (rows <= kFewRows || row0 >= rows) return;  // requests of few rows are few_rows' own
   if (m > g.max_q || kv > g.max_kv) {            // not what the grid was sized for
     if (rt == 0) refuse_request<DT, D>(g, t0, rows, hk, split);
     return;
   }
-  const int i0 = int(row0 / G), i1 = int((min(row0 + kRows, rows) - 1) / G);
+  const int i0 = row0 / G, i1 = (min(row0 + kRows, rows) - 1) / G;
   const int hi_all = max(kv - m + i1 + 1, 0);
   const int lo = g.window ? max(kv - m + i0 - g.window + 1, 0) : 0;
   const int64_t start64 = int64_t(lo & ~31) + int64_t(split) * g.chunk;
@@ -684,11 +705,10 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int64_t b, TileLds<
   u32x4_t qf[kSteps];
   int wlast_min, wfirst_max;
   {
-    const int64_t row = row0 + wave * 32 + r;
+    const int row = row0 + wave * 32 + r;
     const bool real = row < rows;
-    const int64_t rr = real ? row : rows - 1;
-    const int i = int(rr / G);
-    const int64_t head = int64_t(hk) * G + (rr - int64_t(i) * G);
+    const int rr = real ? row : rows - 1;
+    const int i = rr / G, head = hk * G + (rr - i * G);
     orow = real ? (t0 + i) * g.heads + head : -1;
     last = real ? kv - m + i : -1;
     first = g.window ? max(kv - m + i - g.window + 1, 0) : 0;
@@ -720,7 +740,10 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int64_t b, TileLds<
   int groups = -1;
   const int32_t* table = g.table + req * g.table_stride;
   auto load = [&](int tile0) {
-    if (((tile0 - start) & 1023) == 0) groups = row_group(g, table, hk, tile0 + lane * 16, lo, hi);
+    if (((tile0 - start) & 1023) == 0) {
+      const int key = tile0 + lane * 16, col = page_column(g, key);
+      groups = row_group(g, hk, key, col, page_entry(g, table, col), lo, hi);
+    }
     const int grp = __builtin_amdgcn_readlane(groups, ((tile0 - start) & 1023) / 16 + part);
     if (grp >= 0) {
       const uint8_t* k = g.kc + int64_t(grp) * 16 * D;
@@ -982,8 +1005,9 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int64_t b, TileLds<
 template <int DT, int D, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_tile_kernel(const AttnArgs g) {
   __shared__ union { TileLds<D> tile; FewLds<D, 2, NW> few; } lds;
-  if (int64_t(blockIdx.x) < g.tile_blocks) tile_rows<DT, D, NW>(g, blockIdx.x, lds.tile);
-  else few_rows<DT, D, 2, NW>(g, blockIdx.x - g.tile_blocks, lds.few);
+  const int few_from = g.row_tiles * g.splits;
+  if (int(blockIdx.z) < few_from) tile_rows<DT, D, NW>(g, lds.tile);
+  else few_rows<DT, D, 2, NW>(g, blockIdx.z - few_from, lds.few);
 }
 
 // Joins the splits of one row: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
@@ -1062,7 +1086,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs g, i
 // Host
 // ---------------------------------------------------------------------------
 struct Plan {
-  int nq;                       // 16-row tiles of attention_few_kernel
+  int nq, waves;                // 16-row tiles and waves of attention_few_kernel
   bool tiles;                   // some request may have more than kFewRows rows
   int64_t row_tiles;            // of a request of many rows
   int64_t splits, chunk;
@@ -1089,38 +1113,46 @@ mx_status_t plan_attention(int64_t tokens, int heads, int kv_heads, int dim, int
   int64_t keys = max_kv;
   if (window > 0) keys = std::min(keys, window + (p.tiles ? tile_rows : kFewRows) / group + 33);
   keys = std::max<int64_t>((keys + 31) / 32 * 32, 32);
-  // Splits.  Requests of many rows: one workgroup and a half for every CU (one fits); if all other
-  // requests have one token, (tokens - requests) / (max_q - 1) of them have many.  Requests of few
-  // rows: kFewPerCu for every CU, two at a time, so that uneven lengths even out.  No split has less
-  // than 256 keys, two steps for each of four waves.
+  // Splits.  Requests of few rows: workgroups of eight waves, one for every CU (measured against two
+  // and more: 191 to 193 us for 4 requests of 131072 keys against 195 to 215; uneven lengths of 64
+  // requests even out by themselves, 134 us), none with less than 512 keys, two steps a wave.  Calls
+  // that would leave most of the CUs idle even at 256 keys take workgroups of four waves with 256
+  // keys: code that is new to an instruction cache is fetched by fewer waves at a time (1 request
+  // of 1021 keys: 9.6 us, with eight waves 11.3 to 12.4).
+  // Requests of many rows: one workgroup and a half for every CU (one fits); if all other requests
+  // have one token, (tokens - requests) / (max_q - 1) of them have many.
+  const int64_t base = reqs * kv_heads;
+  p.waves = !p.tiles && base * ((keys + 255) / 256) <= cus / 4 ? 4 : 8;
   int64_t want = 1;
   if (p.tiles) {
     const int64_t many = std::max<int64_t>(1, std::min(reqs, (tokens - reqs + max_q - 2) / std::max<int64_t>(max_q - 1, 1)));
     want = (cus + cus / 2) / (many * p.row_tiles * kv_heads);
   }
-  if (!p.tiles || reqs > 1) want = std::max(want, (kFewPerCu * cus + reqs * kv_heads - 1) / (reqs * kv_heads));
+  if (!p.tiles || reqs > 1) want = std::max(want, (cus + base - 1) / base);
   if (p.tiles) want = std::min<int64_t>(want, 8);
+  if (p.waves == 4) want = keys;
   want = std::max<int64_t>(want, 1);
-  p.chunk = std::max<int64_t>((keys + want - 1) / want, 256);
+  p.chunk = std::max<int64_t>((keys + want - 1) / want, p.waves == 4 ? 256 : 512);
   p.chunk = (p.chunk + 127) / 128 * 128;
   p.splits = (keys + p.chunk - 1) / p.chunk;
   p.bytes = p.splits > 1 ? tokens * heads * p.splits * (dim + 2) * 4 : 0;
-  if (reqs * kv_heads * (p.row_tiles + 1) > 0x7FFFFFFF / p.splits) return MX_ERR_SHAPE;
+  if (reqs > 65535 || (p.row_tiles + 1) * p.splits > 65535 || tokens * heads > 0x7FFFFFFF) return MX_ERR_SHAPE;
   return MX_OK;
 }
 
 template <int DT, int D>
 void launch_attention(const Plan& p, AttnArgs g, int64_t requests, hipStream_t stream) {
-  const int64_t per_tile = requests * g.kv_heads * p.splits;
+  const dim3 grid(unsigned(g.kv_heads), unsigned(requests), unsigned(p.splits * (p.row_tiles + 1)));
   if (p.tiles) {
     constexpr int NW = D > 128 ? 4 : 8;
-    g.tile_blocks = per_tile * p.row_tiles;
     g.few_only = true;
-    attention_tile_kernel<DT, D, NW><<<unsigned(g.tile_blocks + per_tile), 64 * NW, 0, stream>>>(g);
+    attention_tile_kernel<DT, D, NW><<<grid, 64 * NW, 0, stream>>>(g);
   } else if (p.nq == 1) {
-    attention_few_kernel<DT, D, 1, 4><<<unsigned(per_tile), 256, 0, stream>>>(g);
+    if (p.waves == 4) attention_few_kernel<DT, D, 1, 4><<<grid, 256, 0, stream>>>(g);
+    else attention_few_kernel<DT, D, 1, 8><<<grid, 512, 0, stream>>>(g);
   } else {
-    attention_few_kernel<DT, D, 2, 4><<<unsigned(per_tile), 256, 0, stream>>>(g);
+    constexpr int NW = D > 128 ? 4 : 8;
+    attention_few_kernel<DT, D, 2, NW><<<grid, 64 * NW, 0, stream>>>(g);
   }
   const int64_t rows = g.tokens * g.heads;
   if (p.splits >= 8) attention_join_kernel<DT, D, 4><<<unsigned(rows), 256, 0, stream>>>(g, requests);
@@ -1180,6 +1212,8 @@ extern "C" mx_status_t mx_paged_attention(const void* q, mx_dtype_t dtype, int64
   g.heads = heads; g.kv_heads = cache->kv_heads; g.group = heads / cache->kv_heads; g.page = cache->page;
   g.window = int(std::min<int64_t>(window, int64_t(1) << 30));
   g.row_tiles = int(p.row_tiles); g.splits = int(p.splits); g.chunk = int(p.chunk);
+  g.inv_group = 1.0f / float(g.group);
+  g.inv_page16 = 16.0 / g.page;
   g.c = scale * 1.44269504088896340736f;
   auto run = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
