@@ -50,7 +50,7 @@ template <int DT> constexpr float kLift = DT == IN_F16 ? 7.0f : 0.0f;
 // Requests of up to so many rows (tokens x group) are taken by workgroups whose waves split the keys.
 constexpr int kFewRows = 32;
 
-// Grid: x = kv head, y = request, z = split (and row tile).  The kv head runs
+// Grid: x = kv head, y = place in the list of work, z = split.  The kv head runs
 // fastest: neighbouring workgroups go to different XCDs, so with 8 kv heads each
 // XCD's L2 serves one head's pages.
 //
@@ -69,16 +69,19 @@ struct AttnArgs {
   const int32_t* lens;
   void* out;
   float* lse;
-  float* part;                  // [tokens * heads][splits][dim] unnormalised outputs
-  float* part_ml;               // [tokens * heads][splits][2] reference exponent and sum
+  float* part;                  // [tokens * heads][slots][dim] unnormalised outputs
+  float* part_ml;               // [tokens * heads][slots][2] reference exponent and sum; a negative
+                                // sum in slot 0: the row is done
   int64_t tokens, max_q, max_kv;
-  int heads, kv_heads, group, page;
+  int requests, heads, kv_heads, group, page;
   int window;                   // 0: none
-  int row_tiles, splits, chunk; // keys of a split, a multiple of 32
+  int slots;                    // partial results a row has room for
+  // how requests of few and of many rows split their keys: how often, and the keys of a split (a multiple of 64)
+  int few_splits, few_chunk, tile_splits, tile_chunk;
   float inv_group;              // 1 / group
   double inv_page16;            // 16 / page
   float c;                      // scale * log2(e)
-  bool few_only;                // few_rows leaves requests of more than kFewRows rows to tile_rows
+  int tile_units;               // most row tiles that requests of many rows can have
 };
 
 template <int DT>
@@ -119,6 +122,36 @@ __device__ __forceinline__ uint32_t any_nan_code(uint32_t w) {   // nonzero if a
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
+// The request that holds unit `want` of a list in which request i has count(new tokens of i) units;
+// `want` becomes the unit's place within it.  -1: the list is shorter.  A launch then has no workgroups
+// without work between those with some, which the dispatcher would deal to the same few shader engines
+// where requests of one kind recur at a stride.
+template <class F>
+__device__ __forceinline__ int find_request(const AttnArgs& g, int& want, F count) {
+  const int lane = threadIdx.x & 63;
+  for (int r0 = 0; r0 < g.requests; r0 += 64) {
+    int n = 0;
+    if (r0 + lane < g.requests) {
+      const int t0 = min(max(g.cu[r0 + lane], 0), int(g.tokens));
+      n = count(min(max(g.cu[r0 + lane + 1], t0), int(g.tokens)) - t0);
+    }
+    int sum = n;                                 // of this and the lanes before
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int x = __shfl_up(sum, off, 64);
+      if (lane >= off) sum += x;
+    }
+    const uint64_t at = __ballot(sum > want);
+    if (at) {
+      const int i = __builtin_ctzll(at);
+      want -= __builtin_amdgcn_readlane(sum - n, i);
+      return r0 + i;
+    }
+    want -= __builtin_amdgcn_readlane(sum, 63);
+  }
+  return -1;
+}
+
 // Page table column of a key: floor(x / d) as (x + 1/2) / d in FP64 (x < 2^27).
 __device__ __forceinline__ int page_column(const AttnArgs& g, int key) {
   return int((double(key >> 4) + 0.5) * g.inv_page16);
@@ -139,17 +172,13 @@ __device__ __forceinline__ int row_group(const AttnArgs& g, int hk, int key, int
 
 // NaN for all rows of one kv head of a request that exceeds what the caller announced.
 template <int DT, int D>
-__device__ __forceinline__ void refuse_request(const AttnArgs& g, int64_t t0, int64_t rows, int hk, int split) {
+__device__ __forceinline__ void refuse_request(const AttnArgs& g, int64_t t0, int64_t rows, int hk) {
   const float nan = __uint_as_float(0x7FC00000u);
   for (int64_t i = threadIdx.x; i < rows; i += blockDim.x) {
     const int64_t row = (t0 + i / g.group) * g.heads + hk * g.group + i % g.group;
-    if (g.splits > 1) {
-      g.part_ml[(row * g.splits + split) * 2] = split ? kLowest : 0.0f;
-      g.part_ml[(row * g.splits + split) * 2 + 1] = split ? 0.0f : nan;
-    } else {
-      for (int d = 0; d < D; ++d) static_cast<uint16_t*>(g.out)[row * D + d] = DT == IN_BF16 ? 0x7FC0u : 0x7E00u;
-      if (g.lse) g.lse[row] = nan;
-    }
+    for (int d = 0; d < D; ++d) static_cast<uint16_t*>(g.out)[row * D + d] = DT == IN_BF16 ? 0x7FC0u : 0x7E00u;
+    if (g.lse) g.lse[row] = nan;
+    if (g.slots > 1) g.part_ml[row * g.slots * 2 + 1] = -1.0f;
   }
 }
 
@@ -157,8 +186,8 @@ __device__ __forceinline__ void refuse_request(const AttnArgs& g, int64_t t0, in
 __device__ __forceinline__ void empty_split(const AttnArgs& g, int64_t t0, int64_t row0, int64_t row1, int hk, int split) {
   for (int64_t i = row0 + threadIdx.x; i < row1; i += blockDim.x) {
     const int64_t row = (t0 + i / g.group) * g.heads + hk * g.group + i % g.group;
-    g.part_ml[(row * g.splits + split) * 2] = kLowest;
-    g.part_ml[(row * g.splits + split) * 2 + 1] = 0.0f;
+    g.part_ml[(row * g.slots + split) * 2] = kLowest;
+    g.part_ml[(row * g.slots + split) * 2 + 1] = 0.0f;
   }
 }
 
@@ -168,14 +197,22 @@ __device__ __forceinline__ float log_sum(float m, float l) {
   return l == 0.0f ? -inf : m == inf ? inf : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
+// A row's statistics: the final ones of an unsplit request, or those of a split; the last
+// split also clears the slots that this kind of request does not use.
 template <int DT>
-__device__ __forceinline__ void put_stats(const AttnArgs& g, int64_t row, int split, float m, float l) {
-  if (g.splits > 1) {
-    g.part_ml[(row * g.splits + split) * 2] = m;
-    g.part_ml[(row * g.splits + split) * 2 + 1] = l;
-  } else if (g.lse) {
-    g.lse[row] = log_sum(m, l);
+__device__ __forceinline__ void put_stats(const AttnArgs& g, int64_t row, int split, int splits, float m, float l) {
+  float* ml = g.part_ml + (row * g.slots + split) * 2;
+  if (splits > 1) {
+    ml[0] = m;
+    ml[1] = l;
+    for (int i = splits; split == splits - 1 && i < g.slots; ++i) {
+      ml[2 * (i - split)] = kLowest;
+      ml[2 * (i - split) + 1] = 0.0f;
+    }
+    return;
   }
+  if (g.lse) g.lse[row] = log_sum(m, l);
+  if (g.slots > 1) ml[1] = -1.0f;
 }
 
 // ---------------------------------------------------------------------------
@@ -201,7 +238,7 @@ template <int D, int NQ, int NW> struct FewLds {
 // w, w + NW, ... of the split: no wave waits for another before the end.  The next
 // step's bytes are loaded while this one is computed.
 template <int DT, int D, int NQ, int NW>
-__device__ __forceinline__ void few_rows(const AttnArgs& g, int split, FewLds<D, NQ, NW>& lds) {
+__device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, FewLds<D, NQ, NW>& lds) {
   using L = Deal<D>;
   using SL = ScaleLoad<D>;
   using T = uint16_t;
@@ -211,16 +248,15 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int split, FewLds<D,
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, quarter = lane >> 4;
 
-  const int hk = blockIdx.x, req = blockIdx.y, G = g.group;
+  const int hk = blockIdx.x, G = g.group;
   const int32_t* table = g.table + req * g.table_stride;
   // without a window the split's first key does not depend on the length: its pages come meanwhile
-  int key = split * g.chunk + lane * 16, col = page_column(g, key);
+  int key = split * g.few_chunk + lane * 16, col = page_column(g, key);
   int entry = page_entry(g, table, col);
   const int t0 = min(max(g.cu[req], 0), int(g.tokens)), t1 = min(max(g.cu[req + 1], t0), int(g.tokens));
   const int m = t1 - t0, kv = max(g.lens[req], 0);
-  if (g.few_only && int64_t(m) * G > kFewRows) return;     // tile_rows' own
   if (__builtin_expect(m > g.max_q || kv > g.max_kv, 0)) {   // not what the grid was sized for
-    refuse_request<DT, D>(g, t0, int64_t(m) * G, hk, split);
+    if (split == 0) refuse_request<DT, D>(g, t0, int64_t(m) * G, hk);
     return;
   }
   const int rows = m * G;
@@ -228,12 +264,14 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int split, FewLds<D,
   // keys that some row sees
   const int hi_all = kv;
   const int lo = g.window ? max(kv - m - g.window + 1, 0) : 0;
-  const int64_t start64 = int64_t(lo & ~31) + int64_t(split) * g.chunk;
+  const int64_t start64 = int64_t(lo & ~31) + int64_t(split) * g.few_chunk;
   if (__builtin_expect(split > 0 && start64 >= hi_all, 0)) {
     empty_split(g, t0, 0, rows, hk, split);
+    if (split == g.few_splits - 1)
+      for (int i = g.few_splits; i < g.slots; ++i) empty_split(g, t0, 0, rows, hk, i);
     return;
   }
-  const int start = int(start64), hi = int(min(int64_t(hi_all), start64 + g.chunk));
+  const int start = int(start64), hi = int(min(int64_t(hi_all), start64 + g.few_chunk));
 
   // this lane's rows: where q is, and the keys (first, last] a row sees
   int last[NQ], first[NQ], orow[NQ];
@@ -585,8 +623,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int split, FewLds<D,
     sum += __shfl_xor(sum, 16, 64);
     sum += __shfl_xor(sum, 32, 64);
     float a = mref[n] == top ? 1.0f : __builtin_amdgcn_exp2f(mref[n] - top);
-    if (g.splits == 1) a = sum == 0.0f ? 0.0f : a * __builtin_amdgcn_rcpf(sum);
-    if (wave == 0 && quarter == 0 && n * 16 + r < rows) put_stats<DT>(g, orow[n], split, top, sum);
+    if (g.few_splits == 1) a = sum == 0.0f ? 0.0f : a * __builtin_amdgcn_rcpf(sum);
+    if (wave == 0 && quarter == 0 && n * 16 + r < rows) put_stats<DT>(g, orow[n], split, g.few_splits, top, sum);
     // the lane holds channels kA (4 quarter + v) + t of the first run, likewise of the second
     float* dst = lds.o[wave][n * 16 + r];
 #pragma unroll
@@ -610,17 +648,17 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int split, FewLds<D,
     for (int w = 0; w < NW; ++w) x += *reinterpret_cast<const v4f*>(&lds.o[w][row][d]);
     const int at = int((float(row) + 0.5f) * g.inv_group);
     const int64_t to = int64_t(t0 + at) * g.heads + hk * G + (row - at * G);
-    if (g.splits == 1)
+    if (g.few_splits == 1)
       *reinterpret_cast<u32x2_t*>(static_cast<T*>(g.out) + to * D + d) = u32x2_t{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])};
     else
-      *reinterpret_cast<v4f*>(g.part + (to * g.splits + split) * D + d) = x;
+      *reinterpret_cast<v4f*>(g.part + (to * g.slots + split) * D + d) = x;
   }
 }
 
 template <int DT, int D, int NQ, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void attention_few_kernel(const AttnArgs g) {
   __shared__ FewLds<D, NQ, NW> lds;
-  few_rows<DT, D, NQ, NW>(g, blockIdx.z, lds);
+  few_rows<DT, D, NQ, NW>(g, blockIdx.y, blockIdx.z, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -653,55 +691,58 @@ __device__ __forceinline__ v16f_t mfma32(u32x4_t a, u32x4_t b, v16f_t acc) {
 //     16-key step are keys 8 h .. 8 h + 7, the ones it feeds as P^T.
 //   - fragments are 1040 bytes apart: lanes that write 8 fragments of one key then
 //     meet 8 different groups of banks.
-template <int D> struct TileLds {
+template <int D, int NW> struct TileLds {
   static constexpr int kFrag = 1040;
-  alignas(16) uint8_t codes[2][D / 4 * kFrag];
-  int nan_tile[2][4];
+  union {
+    struct {
+      alignas(16) uint8_t k[2][D / 8 * kFrag], v[2][D / 8 * kFrag];
+      int nan_tile[2][4];
+    };
+    float out[NW][32][D + 4];
+  };
 };
 
 template <int DT, int D, int NW>
-__device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared) {
+__device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, int split, TileLds<D, NW>& lds) {
   using L = Deal32<D>;
   using T = uint16_t;
   constexpr int kSteps = D / 16;                 // K steps of S^T
   constexpr int kTiles = D / 32;                 // 32-channel tiles of O^T
-  constexpr int kFrag = TileLds<D>::kFrag;
-  constexpr int kFragsK = 2 * kSteps, kFrags = kFragsK + 4 * kTiles;
+  constexpr int kFrag = TileLds<D, NW>::kFrag;
   constexpr int kRows = 32 * NW;
+  constexpr int kAheadK = 4;                     // fragments of keys read ahead
   constexpr int kKLoads = (D + 63) / 64;         // 16-byte loads of a lane for 16 keys
-  auto& lds = shared.codes;
-  auto& nan_tile = shared.nan_tile;
+  auto& nan_tile = lds.nan_tile;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = wave & 3;                     // row group of a tile that this wave decodes
   const bool decodes_k = NW == 4 || wave < 4, decodes_v = NW == 4 || wave >= 4;
   const int r = lane & 31, h = lane >> 5;
 
-  const int hk = blockIdx.x, req = blockIdx.y, G = g.group;
-  const int rt = g.row_tiles - 1 - blockIdx.z / g.splits;   // the last rows see most keys: they begin first
-  const int split = blockIdx.z % g.splits;
+  const int hk = blockIdx.x, G = g.group;
   const int64_t t0 = min(max(int64_t(g.cu[req]), int64_t(0)), g.tokens);
   const int64_t t1 = min(max(int64_t(g.cu[req + 1]), t0), g.tokens);
   const int m = int(t1 - t0), kv = max(g.lens[req], 0);
   const int rows = int(min(int64_t(m) * G, int64_t(0x7FFFFFFF))), row0 = rt * kRows;
-  if (rows <= kFewRows || row0 >= rows) return;  // requests of few rows are few_rows' own
   if (m > g.max_q || kv > g.max_kv) {            // not what the grid was sized for
-    if (rt == 0) refuse_request<DT, D>(g, t0, rows, hk, split);
+    if (rt == 0 && split == 0) refuse_request<DT, D>(g, t0, rows, hk);
     return;
   }
   const int i0 = row0 / G, i1 = (min(row0 + kRows, rows) - 1) / G;
   const int hi_all = max(kv - m + i1 + 1, 0);
   const int lo = g.window ? max(kv - m + i0 - g.window + 1, 0) : 0;
-  const int64_t start64 = int64_t(lo & ~31) + int64_t(split) * g.chunk;
+  const int64_t start64 = int64_t(lo & ~31) + int64_t(split) * g.tile_chunk;
   if (split > 0 && start64 >= hi_all) {
     empty_split(g, t0, row0, min(row0 + kRows, rows), hk, split);
+    if (split == g.tile_splits - 1)
+      for (int i = g.tile_splits; i < g.slots; ++i) empty_split(g, t0, row0, min(row0 + kRows, rows), hk, i);
     return;
   }
-  const int start = int(start64), hi = int(min(int64_t(hi_all), start64 + g.chunk));
+  const int start = int(start64), hi = int(min(int64_t(hi_all), start64 + g.tile_chunk));
   // keys in [all_from, all_to) are seen by every row of the workgroup
   const int all_from = g.window ? max(kv - m + i1 - g.window + 1, 0) : 0, all_to = min(hi, kv - m + i0 + 1);
 
   int last, first;
-  int64_t orow;
+  int orow;
   u32x4_t qf[kSteps];
   int wlast_min, wfirst_max;
   {
@@ -709,7 +750,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
     const bool real = row < rows;
     const int rr = real ? row : rows - 1;
     const int i = rr / G, head = hk * G + (rr - i * G);
-    orow = real ? (t0 + i) * g.heads + head : -1;
+    orow = real ? int(t0 + i) * g.heads + head : -1;
     last = real ? kv - m + i : -1;
     first = g.window ? max(kv - m + i - g.window + 1, 0) : 0;
     wlast_min = real ? last : 0x7FFFFFFF;
@@ -734,9 +775,12 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
     for (int v = 0; v < 16; ++v) o[t][v] = 0.0f;
 
   // ---- this wave's 16 keys or values of a tile
-  uint4 rk[kKLoads];
-  uint32_t rks[kKLoads];
-  uint32_t rv[8][L::kA == 8 ? 2 : 1], rvb[8], rvs[8], rvsb[8];
+  // (a wave that decodes only keys or only values holds them in the same registers)
+  constexpr int kWordsV = L::kA == 8 ? 2 : 1, kRuns = L::kB ? 2 : 1;
+  constexpr int kAtV = NW == 8 ? 0 : 4 * kKLoads, kAtVs = NW == 8 ? 0 : kKLoads;
+  uint32_t raw[std::max(4 * kKLoads, kAtV + 8 * (kWordsV + kRuns - 1))], sc[std::max(kKLoads, kAtVs + 8 * kRuns)];
+  auto rv = [&](int j, int w) -> uint32_t& { return raw[kAtV + 8 * w + j]; };    // word w of key j; w == kWordsV: second run
+  auto rvs = [&](int j, int run) -> uint32_t& { return sc[kAtVs + 8 * run + j]; };
   int groups = -1;
   const int32_t* table = g.table + req * g.table_stride;
   auto load = [&](int tile0) {
@@ -753,8 +797,9 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
         for (int u = 0; u < kKLoads; ++u) {
           const int c = lane + 64 * u;           // 16-byte chunk of the 16 rows
           if (D % 64 == 0 || c < D) {
-            rk[u] = *reinterpret_cast<const uint4*>(k + 16 * c);
-            rks[u] = ks[c / 2];                  // two chunks to a block of 32
+            const uint4 w = *reinterpret_cast<const uint4*>(k + 16 * c);
+            raw[4 * u] = w.x; raw[4 * u + 1] = w.y; raw[4 * u + 2] = w.z; raw[4 * u + 3] = w.w;
+            sc[u] = ks[c / 2];                   // two chunks to a block of 32
           }
         }
       }
@@ -766,49 +811,53 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
         const uint8_t* a = v + j * D + L::kA * r;
         if constexpr (L::kA == 8) {
           const uint2 w = *reinterpret_cast<const uint2*>(a);
-          rv[j][0] = w.x; rv[j][1] = w.y;
+          rv(j, 0) = w.x; rv(j, 1) = w.y;
         } else if constexpr (L::kA == 4) {
-          rv[j][0] = *reinterpret_cast<const uint32_t*>(a);
+          rv(j, 0) = *reinterpret_cast<const uint32_t*>(a);
         } else {
-          rv[j][0] = *reinterpret_cast<const uint16_t*>(a);
+          rv(j, 0) = *reinterpret_cast<const uint16_t*>(a);
         }
-        rvs[j] = vs[j * (D / 32) + (L::kA * r) / 32];
+        rvs(j, 0) = vs[j * (D / 32) + (L::kA * r) / 32];
         if constexpr (L::kB) {
           const uint8_t* e = v + j * D + 32 * L::kA + L::kB * r;
-          if constexpr (L::kB == 2) rvb[j] = *reinterpret_cast<const uint16_t*>(e);
-          else rvb[j] = *e;
-          rvsb[j] = vs[j * (D / 32) + (32 * L::kA + L::kB * r) / 32];
+          if constexpr (L::kB == 2) rv(j, kWordsV) = *reinterpret_cast<const uint16_t*>(e);
+          else rv(j, kWordsV) = *e;
+          rvs(j, 1) = vs[j * (D / 32) + (32 * L::kA + L::kB * r) / 32];
         }
       }
     } else {                                     // keys of a bad page are NaN, and so is what sees them
+      if (decodes_k) {
 #pragma unroll
-      for (int u = 0; u < kKLoads; ++u) {
-        rk[u] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-        rks[u] = 127;
+        for (int u = 0; u < 4 * kKLoads; ++u) raw[u] = 0x7F7F7F7Fu;
+#pragma unroll
+        for (int u = 0; u < kKLoads; ++u) sc[u] = 127;
       }
+      if (decodes_v) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        rv[j][0] = rvb[j] = 0;
-        if constexpr (L::kA == 8) rv[j][1] = 0;
-        rvs[j] = rvsb[j] = 127;
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+          for (int w = 0; w < kWordsV + kRuns - 1; ++w) rv(j, w) = 0;
+#pragma unroll
+          for (int w = 0; w < kRuns; ++w) rvs(j, w) = 127;
+        }
       }
     }
   };
   auto decode = [&](int tile0, int buf) {
-    uint8_t* base = lds[buf];
+    uint8_t* base = lds.k[buf];
     if (decodes_k)
 #pragma unroll
     for (int u = 0; u < kKLoads; ++u) {
       const int c = lane + 64 * u;
       const int key = c / kSteps, s = c % kSteps;
       const int row = ((key >> 2) & 1) * 8 + (key >> 3) * 4 + (key & 3) + 16 * (part & 1);
-      const uint32_t sc = rks[u] << 23;
+      const uint32_t scale = sc[u] << 23;
       uint8_t* dst = base + ((part >> 1) * kSteps + s) * kFrag + row * 16;
       if (D % 64 == 0 || c < D) {
-        *reinterpret_cast<u32x4_t*>(dst) = u32x4_t{decode2<DT, false>(rk[u].x, sc), decode2<DT, true>(rk[u].x, sc),
-                                                   decode2<DT, false>(rk[u].y, sc), decode2<DT, true>(rk[u].y, sc)};
-        *reinterpret_cast<u32x4_t*>(dst + 512) = u32x4_t{decode2<DT, false>(rk[u].z, sc), decode2<DT, true>(rk[u].z, sc),
-                                                         decode2<DT, false>(rk[u].w, sc), decode2<DT, true>(rk[u].w, sc)};
+        *reinterpret_cast<u32x4_t*>(dst) = u32x4_t{decode2<DT, false>(raw[4 * u + 0], scale), decode2<DT, true>(raw[4 * u + 0], scale),
+                                                   decode2<DT, false>(raw[4 * u + 1], scale), decode2<DT, true>(raw[4 * u + 1], scale)};
+        *reinterpret_cast<u32x4_t*>(dst + 512) = u32x4_t{decode2<DT, false>(raw[4 * u + 2], scale), decode2<DT, true>(raw[4 * u + 2], scale),
+                                                         decode2<DT, false>(raw[4 * u + 3], scale), decode2<DT, true>(raw[4 * u + 3], scale)};
       }
     }
     if (!decodes_v) return;
@@ -820,28 +869,28 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const bool keep = uint32_t(j) - from < many;
-        rv[j][0] = keep ? rv[j][0] : 0u;
-        if constexpr (L::kA == 8) rv[j][1] = keep ? rv[j][1] : 0u;
-        rvs[j] = keep ? rvs[j] : 127u;
-        nan |= any_nan_code(rv[j][0]) | (rvs[j] == 255u ? 1u : 0u);
-        if constexpr (L::kA == 8) nan |= any_nan_code(rv[j][1]);
-        if constexpr (L::kB) {
-          rvb[j] = keep ? rvb[j] : 0u;
-          rvsb[j] = keep ? rvsb[j] : 127u;
-          nan |= any_nan_code(rvb[j]) | (rvsb[j] == 255u ? 1u : 0u);
+#pragma unroll
+        for (int w = 0; w < kWordsV + kRuns - 1; ++w) {
+          rv(j, w) = keep ? rv(j, w) : 0u;
+          nan |= any_nan_code(rv(j, w));
+        }
+#pragma unroll
+        for (int w = 0; w < kRuns; ++w) {
+          rvs(j, w) = keep ? rvs(j, w) : 127u;
+          nan |= rvs(j, w) == 255u ? 1u : 0u;
         }
       }
     }
     const bool any = __ballot(nan != 0) != 0;
     if (lane == 0) nan_tile[buf][part] = any;
-    uint8_t* vb = base + (kFragsK + part) * kFrag + lane * 16;   // fragment (tile, step) at kFragsK + 4 tile + step
-    auto pair = [&](const uint32_t (&w)[8], const uint32_t (&sc)[8], auto hi_half, int tile, bool both) {
+    uint8_t* vb = lds.v[buf] + part * kFrag + lane * 16;        // fragment (tile, step) at 4 tile + step
+    auto pair = [&](int w, int run, auto hi_half, int tile, bool both) {
       constexpr bool HI = decltype(hi_half)::value;
       u32x4_t a, c;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t x = decode2<DT, HI>(w[2 * j], sc[2 * j] << 23);
-        const uint32_t y = decode2<DT, HI>(w[2 * j + 1], sc[2 * j + 1] << 23);
+        const uint32_t x = decode2<DT, HI>(rv(2 * j, w), rvs(2 * j, run) << 23);
+        const uint32_t y = decode2<DT, HI>(rv(2 * j + 1, w), rvs(2 * j + 1, run) << 23);
         a[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
         c[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
       }
@@ -849,14 +898,11 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
       if (both) *reinterpret_cast<u32x4_t*>(vb + 4 * (tile + 1) * kFrag) = c;
     };
 #pragma unroll
-    for (int w = 0; w < (L::kA == 8 ? 2 : 1); ++w) {
-      uint32_t x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = rv[j][w];
-      pair(x, rvs, std::false_type{}, 4 * w, true);
-      if constexpr (L::kA >= 4) pair(x, rvs, std::true_type{}, 4 * w + 2, true);
+    for (int w = 0; w < kWordsV; ++w) {
+      pair(w, 0, std::false_type{}, 4 * w, true);
+      if constexpr (L::kA >= 4) pair(w, 0, std::true_type{}, 4 * w + 2, true);
     }
-    if constexpr (L::kB) pair(rvb, rvsb, std::false_type{}, L::kA, L::kB == 2);
+    if constexpr (L::kB) pair(kWordsV, 1, std::false_type{}, L::kA, L::kB == 2);
   };
 
   // A tile with NaN values that some rows of the workgroup see and others do not: 0 * NaN would reach
@@ -880,7 +926,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
                  (uint32_t(16 * u + 2 * j + 1) - from < many ? kOne << 16 : 0u);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        u32x4_t mark = nans(*reinterpret_cast<const u32x4_t*>(lds[buf] + (kFragsK + 4 * t + u) * kFrag + lane * 16));
+        u32x4_t mark = nans(*reinterpret_cast<const u32x4_t*>(lds.v[buf] + (4 * t + u) * kFrag + lane * 16));
         mark &= kOne | kOne << 16;
         v16f_t hits;
 #pragma unroll
@@ -895,24 +941,38 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
       }
     }
     __syncthreads();
-    for (int f = kFragsK + wave; f < kFrags; f += NW) {
-      u32x4_t* at = reinterpret_cast<u32x4_t*>(lds[buf] + f * kFrag + lane * 16);
+    for (int f = wave; f < 4 * kTiles; f += NW) {
+      u32x4_t* at = reinterpret_cast<u32x4_t*>(lds.v[buf] + f * kFrag + lane * 16);
       *at &= ~nans(*at);
     }
     __syncthreads();
   };
 
-  auto compute = [&](int tile0, int buf) {
-    const uint8_t* base = lds[buf] + lane * 16;
+  u32x4_t p[4];                                  // weights of the tile last scored
+  auto score = [&](int tile0, int buf) {
+    const uint8_t* base = lds.k[buf] + lane * 16;
     // ---- S^T
+    // kAheadK fragments are read ahead of the matrix unit; the two 32-key tiles take turns, so that no
+    // product waits for the one before
     v16f_t s[2];
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
+    for (int v = 0; v < 16; ++v) s[0][v] = s[1][v] = 0.0f;
+    auto fragment = [&](int i) {
+      return *reinterpret_cast<const u32x4_t*>(base + ((i & 1) * kSteps + (i >> 1)) * kFrag);
+    };
+    u32x4_t kf[kAheadK];
 #pragma unroll
-      for (int v = 0; v < 16; ++v) s[kt][v] = 0.0f;
+    for (int i = 0; i < kAheadK; ++i) kf[i] = fragment(i);
 #pragma unroll
-      for (int f = 0; f < kSteps; ++f)
-        s[kt] = mfma32<DT>(*reinterpret_cast<const u32x4_t*>(base + (kt * kSteps + f) * kFrag), qf[f], s[kt]);
+    for (int i = 0; i < 2 * kSteps; ++i) {
+      s[i & 1] = mfma32<DT>(kf[i % kAheadK], qf[i >> 1], s[i & 1]);
+      if (i + kAheadK < 2 * kSteps) kf[i % kAheadK] = fragment(i + kAheadK);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, kAheadK, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * kSteps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      if (i + kAheadK < 2 * kSteps) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
     // ---- masks: value 8 i + j of s[kt] is key 32 kt + 16 i + 8 h + j of the tile
     const uint32_t from = uint32_t(first - tile0 - 8 * h), many = uint32_t(max(min(last, hi - 1) - first + 1, 0));
@@ -936,7 +996,6 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
       for (int t = 0; t < kTiles; ++t) o[t] *= a;
     }
     // ---- weights
-    u32x4_t p[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       float e[8];
@@ -945,13 +1004,14 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
       l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
       p[u] = u32x4_t{pack2<DT>(e[0], e[1]), pack2<DT>(e[2], e[3]), pack2<DT>(e[4], e[5]), pack2<DT>(e[6], e[7])};
     }
-    // ---- O^T
-    const uint8_t* vbase = base + kFragsK * kFrag;
+  };
+  auto add_values = [&](int buf) {              // O^T
+    const uint8_t* base = lds.v[buf] + lane * 16;
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
-        o[t] = mfma32<DT>(*reinterpret_cast<const u32x4_t*>(vbase + (4 * t + u) * kFrag), p[u], o[t]);
+        o[t] = mfma32<DT>(*reinterpret_cast<const u32x4_t*>(base + (4 * t + u) * kFrag), p[u], o[t]);
   };
 
   if (start < hi) {
@@ -961,59 +1021,84 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, TileLds<D>& shared)
     __syncthreads();
     int buf = 0;
     for (int tile0 = start; tile0 < hi; tile0 += 64) {
+      if (nan_tile[buf][0] | nan_tile[buf][1] | nan_tile[buf][2] | nan_tile[buf][3]) take_nans(tile0, buf);
       if (tile0 + 64 < hi) {
         decode(tile0 + 64, buf ^ 1);
         if (tile0 + 128 < hi) load(tile0 + 128);
       }
-      if (nan_tile[buf][0] | nan_tile[buf][1] | nan_tile[buf][2] | nan_tile[buf][3]) take_nans(tile0, buf);
-      compute(tile0, buf);
+      score(tile0, buf);
+      add_values(buf);
       __syncthreads();
       buf ^= 1;
     }
   }
 
-  // ---- outputs: the lane holds channels kA c + t of the first run (c = 8 (v / 4) + 4 h + v % 4), likewise of the second
+  // ---- outputs.  The lane holds channels kA c + t of the first run (c = 8 (v / 4) + 4 h + v % 4), likewise
+  // of the second, of one row; through LDS, whole rows are stored at a time.
   l += __shfl_xor(l, 32, 64);
-  if (orow < 0) return;
-  const bool direct = g.splits == 1;
-  const float inv = direct ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+  const bool direct = g.tile_splits == 1;
+  const float scale = direct ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+  if (h == 0 && orow >= 0) put_stats<DT>(g, orow, split, g.tile_splits, mref, l);
+  __syncthreads();                               // the tiles are done with
   auto put = [&](int base, int tile0, auto kWidth) {
     constexpr int W = decltype(kWidth)::value;
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
-      const int64_t d = base + W * (8 * (v >> 2) + 4 * h + (v & 3));
-      if (direct) {
-        T* dst = static_cast<T*>(g.out) + orow * D + d;
-        if constexpr (W == 1) *dst = T(pack2<DT>(o[tile0][v] * inv, 0.0f));
-        else
+      float* dst = &lds.out[wave][r][base + W * (8 * (v >> 2) + 4 * h + (v & 3))];
+      if constexpr (W >= 4) {
 #pragma unroll
-          for (int t = 0; t < W; t += 2)
-            *reinterpret_cast<uint32_t*>(dst + t) = pack2<DT>(o[tile0 + t][v] * inv, o[tile0 + t + (W > 1)][v] * inv);
+        for (int t = 0; t < W; t += 4)
+          *reinterpret_cast<v4f*>(dst + t) = v4f{o[tile0 + t][v], o[tile0 + t + 1][v], o[tile0 + t + 2][v],
+                                                 o[tile0 + t + 3][v]} * scale;
       } else {
-        float* dst = g.part + (orow * g.splits + split) * D + d;
 #pragma unroll
-        for (int t = 0; t < W; ++t) dst[t] = o[tile0 + t][v];
+        for (int t = 0; t < W; ++t) dst[t] = o[tile0 + t][v] * scale;
       }
     }
   };
   put(0, 0, std::integral_constant<int, L::kA>{});
   if constexpr (L::kB) put(32 * L::kA, L::kA, std::integral_constant<int, L::kB>{});
-  if (h == 0) put_stats<DT>(g, orow, split, mref, l);
+  wave_lds_fence();
+#pragma unroll 4
+  for (int i = lane; i < 32 * (D / 4); i += 64) {
+    const int row = i / (D / 4), d = i % (D / 4) * 4;
+    const int64_t to = __shfl(orow, row, 64);
+    if (to < 0) continue;
+    const v4f x = *reinterpret_cast<const v4f*>(&lds.out[wave][row][d]);
+    if (direct)
+      *reinterpret_cast<u32x2_t*>(static_cast<T*>(g.out) + to * D + d) = u32x2_t{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])};
+    else
+      *reinterpret_cast<v4f*>(g.part + (to * g.slots + split) * D + d) = x;
+  }
 }
 
-// Requests of many rows, and in the same launch, behind them, the others of the call.
+// Requests of many rows, and in the same launch, behind them, the others of the call: y counts row
+// tiles times splits, then requests of few rows times splits.
 template <int DT, int D, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4))) void attention_tile_kernel(const AttnArgs g) {
-  __shared__ union { TileLds<D> tile; FewLds<D, 2, NW> few; } lds;
-  const int few_from = g.row_tiles * g.splits;
-  if (int(blockIdx.z) < few_from) tile_rows<DT, D, NW>(g, lds.tile);
-  else few_rows<DT, D, 2, NW>(g, blockIdx.z - few_from, lds.few);
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(D > 128 ? 1 : 2, D > 128 ? 1 : 2))) void attention_tile_kernel(const AttnArgs g) {
+  __shared__ union { TileLds<D, NW> tile; FewLds<D, 2, NW> few; } lds;
+  const int G = g.group;
+  int unit = blockIdx.z * gridDim.y + blockIdx.y;
+  if (unit < g.tile_units * g.tile_splits) {
+    const int split = unit % g.tile_splits;
+    unit /= g.tile_splits;
+    const int req = find_request(g, unit, [&](int m) {
+      const int64_t rows = int64_t(m) * G;
+      return rows > kFewRows ? int((rows + 32 * NW - 1) / (32 * NW)) : 0;
+    });
+    if (req >= 0) tile_rows<DT, D, NW>(g, req, unit, split, lds.tile);
+  } else {
+    unit -= g.tile_units * g.tile_splits;
+    const int split = unit % g.few_splits;
+    unit /= g.few_splits;
+    const int req = find_request(g, unit, [&](int m) { return m > 0 && int64_t(m) * G <= kFewRows ? 1 : 0; });
+    if (req >= 0) few_rows<DT, D, 2, NW>(g, req, split, lds.few);
+  }
 }
 
 // Joins the splits of one row: o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // WPR waves per row take every WPR-th split; a lane takes channels 2 lane, 2 lane + 1 of
-// each 128.  Outputs of splits without keys were never written: they are loaded with the
-// others (the loads need no waiting between them) and dropped.
+// each 128.  Outputs of splits without keys were never written and are not read.
 template <int DT, int D, int WPR>
 __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs g, int64_t requests) {
   constexpr int kPer = (D + 127) / 128;
@@ -1021,22 +1106,23 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs g, i
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, sub = wave % WPR;
   const int64_t row = int64_t(blockIdx.x) * (4 / WPR) + wave / WPR;
   const int64_t token = row / g.heads;
-  const bool mine = row < g.tokens * g.heads && token >= g.cu[0] && token < g.cu[requests];
+  const bool mine = row < g.tokens * g.heads && token >= g.cu[0] && token < g.cu[requests] &&
+                    !(g.part_ml[row * g.slots * 2 + 1] < 0.0f);
   if (WPR == 1 && !mine) return;
   v2f acc[kPer];
 #pragma unroll
   for (int u = 0; u < kPer; ++u) acc[u] = v2f{0, 0};
   float top = kLowest, sum = 0.0f;
   if (mine) {
-    const float* ml = g.part_ml + row * g.splits * 2;
-    for (int i = lane; i < g.splits; i += 64)
+    const float* ml = g.part_ml + row * g.slots * 2;
+    for (int i = lane; i < g.slots; i += 64)
       if (ml[2 * i + 1] != 0.0f) top = fmaxf(top, ml[2 * i]);
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-    for (int i0 = 0; i0 < g.splits; i0 += 64) {
+    for (int i0 = 0; i0 < g.slots; i0 += 64) {
       // lane i holds the weight of split i0 + i
       float w = 0.0f, li = 0.0f;
-      if (i0 + lane < g.splits) {
+      if (i0 + lane < g.slots) {
         li = ml[2 * (i0 + lane) + 1];
         const float mi = ml[2 * (i0 + lane)];
         w = li == 0.0f ? 0.0f : mi == top ? 1.0f : __builtin_amdgcn_exp2f(mi - top);
@@ -1045,20 +1131,33 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs g, i
 #pragma unroll
       for (int off = 32; off >= 1; off >>= 1) li += __shfl_xor(li, off, 64);
       sum += li;
-      const int n = min(g.splits - i0, 64);
-      const float* o = g.part + (row * g.splits + i0) * D;
-#pragma unroll 4
-      for (int i = sub; i < n; i += WPR) {
-        const float wi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), i));
+      const float* o = g.part + (row * g.slots + i0) * D;
+      uint64_t left = __ballot(w != 0.0f);       // slots that hold something (NaN weights too)
+      for (int i = 0; i < sub; ++i) left &= left - 1;
+      while (left) {
+        // up to four slots, loads first
+        float wi[4];
+        float2 x[4][kPer];
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-          const int d = u * 128 + 2 * lane;
-          if (d < D) {
-            const float2 x = *reinterpret_cast<const float2*>(o + i * D + d);
-            acc[u][0] += wi == 0.0f ? 0.0f : wi * x.x;
-            acc[u][1] += wi == 0.0f ? 0.0f : wi * x.y;
+        for (int k = 0; k < 4; ++k) {
+          const int i = left ? __builtin_ctzll(left) : 0;
+          wi[k] = left ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), i)) : 0.0f;
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            const int d = u * 128 + 2 * lane;
+            x[k][u] = make_float2(0.0f, 0.0f);
+            if (left && d < D) x[k][u] = *reinterpret_cast<const float2*>(o + i * D + d);
           }
+#pragma unroll
+          for (int j = 0; j < WPR; ++j) left &= left - 1;
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            acc[u][0] += wi[k] * x[k][u].x;
+            acc[u][1] += wi[k] * x[k][u].y;
+          }
       }
     }
   }
@@ -1088,10 +1187,15 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs g, i
 struct Plan {
   int nq, waves;                // 16-row tiles and waves of attention_few_kernel
   bool tiles;                   // some request may have more than kFewRows rows
-  int64_t row_tiles;            // of a request of many rows
-  int64_t splits, chunk;
+  int tile_waves;               // of attention_tile_kernel: 32 rows each
+  int64_t tile_units;           // most row tiles that requests of many rows can have
+  int64_t few_splits, few_chunk, tile_splits, tile_chunk, slots;
   int64_t bytes;                // workspace
 };
+
+constexpr int64_t cut(int64_t keys, int64_t splits, int64_t least) {   // keys of a split
+  return (std::max((keys + splits - 1) / splits, least) + 127) / 128 * 128;
+}
 
 mx_status_t plan_attention(int64_t tokens, int heads, int kv_heads, int dim, int64_t requests, int64_t max_q,
                            int64_t max_kv, int64_t window, Plan& p) {
@@ -1099,54 +1203,85 @@ mx_status_t plan_attention(int64_t tokens, int heads, int kv_heads, int dim, int
   if (tokens < 0 || requests < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || heads > 65536) return MX_ERR_SHAPE;
   if (dim != 64 && dim != 96 && dim != 128 && dim != 192 && dim != 256) return MX_ERR_SHAPE;
   if (max_q < 0 || max_kv < 0 || window < 0) return MX_ERR_ARG;
-  if (tokens > lim || requests > lim || max_kv > lim || max_q > lim) return MX_ERR_SHAPE;
+  if (tokens > lim || requests > 65535 || max_kv > lim || max_q > lim || tokens * heads > 0x7FFFFFFF) return MX_ERR_SHAPE;
   const int64_t cus = device_cus();
   if (cus <= 0) return MX_ERR_LAUNCH;
-  const int64_t group = heads / kv_heads, reqs = std::max<int64_t>(requests, 1);
+  const int64_t group = heads / kv_heads, reqs = std::max<int64_t>(requests, 1), base = reqs * kv_heads;
   max_q = std::min(max_q, tokens);
   const int64_t rows = std::max<int64_t>(max_q * group, 1);
   p.tiles = rows > kFewRows;
   p.nq = rows <= 16 ? 1 : 2;
-  const int64_t tile_rows = dim > 128 ? 128 : 256;
-  p.row_tiles = p.tiles ? (rows + tile_rows - 1) / tile_rows : 0;
-  // keys that one workgroup's rows can see
-  int64_t keys = max_kv;
-  if (window > 0) keys = std::min(keys, window + (p.tiles ? tile_rows : kFewRows) / group + 33);
-  keys = std::max<int64_t>((keys + 31) / 32 * 32, 32);
-  // Splits.  Requests of few rows: workgroups of eight waves, one for every CU (measured against two
-  // and more: 191 to 193 us for 4 requests of 131072 keys against 195 to 215; uneven lengths of 64
-  // requests even out by themselves, 134 us), none with less than 512 keys, two steps a wave.  Calls
+  // keys that the rows of one workgroup can see
+  auto seen = [&](int64_t n) {
+    const int64_t keys = window > 0 ? std::min(max_kv, window + n / group + 33) : max_kv;
+    return std::max<int64_t>((keys + 63) / 64 * 64, 64);
+  };
+  // Requests of few rows: workgroups of eight waves, one for every CU (measured against two and
+  // more: 191 to 193 us for 4 requests of 131072 keys against 195 to 215; uneven lengths of 64
+  // requests even out by themselves, 135 us), none with less than 512 keys, two steps a wave.  Calls
   // that would leave most of the CUs idle even at 256 keys take workgroups of four waves with 256
   // keys: code that is new to an instruction cache is fetched by fewer waves at a time (1 request
   // of 1021 keys: 9.6 us, with eight waves 11.3 to 12.4).
-  // Requests of many rows: one workgroup and a half for every CU (one fits); if all other requests
-  // have one token, (tokens - requests) / (max_q - 1) of them have many.
-  const int64_t base = reqs * kv_heads;
+  int64_t keys = seen(kFewRows);
   p.waves = !p.tiles && base * ((keys + 255) / 256) <= cus / 4 ? 4 : 8;
-  int64_t want = 1;
+  // Beside requests of many rows, of which there are (tokens - requests) / (max_q - 1) if all others have
+  // one token: at most 8 splits, since every row of the call has room for as many partial results.
+  int64_t many = 0, few_wgs = base, most = keys;
   if (p.tiles) {
-    const int64_t many = std::max<int64_t>(1, std::min(reqs, (tokens - reqs + max_q - 2) / std::max<int64_t>(max_q - 1, 1)));
-    want = (cus + cus / 2) / (many * p.row_tiles * kv_heads);
+    many = std::max<int64_t>(1, std::min(reqs, (tokens - reqs + max_q - 2) / std::max<int64_t>(max_q - 1, 1)));
+    few_wgs = (reqs - many) * kv_heads;
+    most = few_wgs ? 8 : 1;
   }
-  if (!p.tiles || reqs > 1) want = std::max(want, (cus + base - 1) / base);
-  if (p.tiles) want = std::min<int64_t>(want, 8);
-  if (p.waves == 4) want = keys;
-  want = std::max<int64_t>(want, 1);
-  p.chunk = std::max<int64_t>((keys + want - 1) / want, p.waves == 4 ? 256 : 512);
-  p.chunk = (p.chunk + 127) / 128 * 128;
-  p.splits = (keys + p.chunk - 1) / p.chunk;
-  p.bytes = p.splits > 1 ? tokens * heads * p.splits * (dim + 2) * 4 : 0;
-  if (reqs > 65535 || (p.row_tiles + 1) * p.splits > 65535 || tokens * heads > 0x7FFFFFFF) return MX_ERR_SHAPE;
+  p.few_chunk = p.waves == 4 ? 256 : cut(keys, std::min(most, (cus + few_wgs - 1) / std::max<int64_t>(few_wgs, 1)), 512);
+  p.few_splits = (keys + p.few_chunk - 1) / p.few_chunk;
+  // Requests of many rows.  Workgroups of eight waves (one fits a CU) where they fill the CUs: a tile of
+  // keys is decoded for twice the rows (2048 tokens over 32768: 1079 us, with four waves 1121).  Fewer
+  // are spread better by workgroups of four waves, of which two fit a CU up to 128 channels (300 tokens
+  // alone: 14.8 us, with eight waves 17.9).
+  // Then the number of splits with the least estimate of rounds over the CUs plus partial results: a tile of
+  // 64 keys takes 1.5 us (3 to 4 us with 192 or 256 channels, where one wave a SIMD has nothing to
+  // overlap with), a workgroup's beginning and end 7 us, a partial result of 256 rows of 128 channels 0.05 us
+  // of the memory's time, a join 5 us.
+  p.tile_units = 0;
+  p.tile_splits = 1;
+  p.tile_chunk = 64;
+  p.tile_waves = 4;
+  if (p.tiles) {
+    if (dim <= 128 && many * ((rows + 255) / 256) * kv_heads >= cus) p.tile_waves = 8;
+    const int64_t tile_rows = 32 * p.tile_waves, room = p.tile_waves == 4 && dim <= 128 ? 2 * cus : cus;
+    p.tile_units = tokens * group / tile_rows + std::min(reqs, tokens * group / (kFewRows + 1));
+    keys = seen(tile_rows);
+    const int64_t wgs = many * ((rows + tile_rows - 1) / tile_rows) * kv_heads;
+    const double tile = dim > 128 ? dim / 64.0 : 1.5 * dim / 128.0, part = 0.05 * double(tile_rows) / 256.0 * dim / 128.0;
+    double least = 0.0;
+    for (int64_t n = 1; n <= 16; ++n) {
+      const int64_t chunk = cut(keys, n, 256);
+      if (n > 1 && (keys + chunk - 1) / chunk < n) break;
+      const double cost = double((wgs * n + room - 1) / room) * (double((chunk + 63) / 64) * tile + 7.0) +
+                          (n > 1 ? double(wgs * n) * part + 5.0 : 0.0);
+      if (n == 1 || cost < least) {
+        least = cost;
+        p.tile_splits = n;
+        p.tile_chunk = chunk;
+      }
+    }
+  }
+  p.slots = std::max(p.few_splits, p.tile_splits);
+  p.bytes = p.slots > 1 ? tokens * heads * p.slots * (dim + 2) * 4 : 0;
+  if (p.few_splits > 65535 || p.tile_units * p.tile_splits + reqs * p.few_splits > (1 << 24)) return MX_ERR_SHAPE;
   return MX_OK;
 }
 
 template <int DT, int D>
 void launch_attention(const Plan& p, AttnArgs g, int64_t requests, hipStream_t stream) {
-  const dim3 grid(unsigned(g.kv_heads), unsigned(requests), unsigned(p.splits * (p.row_tiles + 1)));
+  const dim3 grid(unsigned(g.kv_heads), unsigned(requests), unsigned(p.few_splits));
   if (p.tiles) {
-    constexpr int NW = D > 128 ? 4 : 8;
-    g.few_only = true;
-    attention_tile_kernel<DT, D, NW><<<grid, 64 * NW, 0, stream>>>(g);
+    const unsigned units = unsigned(p.tile_units * p.tile_splits + requests * p.few_splits), y = std::min(units, 32768u);
+    const dim3 work(unsigned(g.kv_heads), y, (units + y - 1) / y);
+    if constexpr (D <= 128) {
+      if (p.tile_waves == 8) attention_tile_kernel<DT, D, 8><<<work, 512, 0, stream>>>(g);
+    }
+    if (p.tile_waves == 4) attention_tile_kernel<DT, D, 4><<<work, 256, 0, stream>>>(g);
   } else if (p.nq == 1) {
     if (p.waves == 4) attention_few_kernel<DT, D, 1, 4><<<grid, 256, 0, stream>>>(g);
     else attention_few_kernel<DT, D, 1, 8><<<grid, 512, 0, stream>>>(g);
@@ -1155,8 +1290,8 @@ void launch_attention(const Plan& p, AttnArgs g, int64_t requests, hipStream_t s
     attention_few_kernel<DT, D, 2, NW><<<grid, 64 * NW, 0, stream>>>(g);
   }
   const int64_t rows = g.tokens * g.heads;
-  if (p.splits >= 8) attention_join_kernel<DT, D, 4><<<unsigned(rows), 256, 0, stream>>>(g, requests);
-  else if (p.splits > 1) attention_join_kernel<DT, D, 1><<<unsigned((rows + 3) / 4), 256, 0, stream>>>(g, requests);
+  if (p.slots >= 8 && !p.tiles) attention_join_kernel<DT, D, 4><<<unsigned(rows), 256, 0, stream>>>(g, requests);
+  else if (p.slots > 1) attention_join_kernel<DT, D, 1><<<unsigned((rows + 3) / 4), 256, 0, stream>>>(g, requests);
 }
 
 }  // namespace mxk
@@ -1207,11 +1342,13 @@ extern "C" mx_status_t mx_paged_attention(const void* q, mx_dtype_t dtype, int64
   g.table = page_table; g.table_stride = table_stride; g.table_cols = table_cols;
   g.cu = cu; g.lens = lens; g.out = out; g.lse = lse;
   g.part = static_cast<float*>(workspace);
-  g.part_ml = g.part ? g.part + tokens * heads * p.splits * cache->dim : nullptr;
+  g.part_ml = g.part ? g.part + tokens * heads * p.slots * cache->dim : nullptr;
   g.tokens = tokens; g.max_q = max_q; g.max_kv = max_kv;
   g.heads = heads; g.kv_heads = cache->kv_heads; g.group = heads / cache->kv_heads; g.page = cache->page;
   g.window = int(std::min<int64_t>(window, int64_t(1) << 30));
-  g.row_tiles = int(p.row_tiles); g.splits = int(p.splits); g.chunk = int(p.chunk);
+  g.requests = int(requests); g.tile_units = int(p.tile_units); g.slots = int(p.slots);
+  g.few_splits = int(p.few_splits); g.few_chunk = int(p.few_chunk);
+  g.tile_splits = int(p.tile_splits); g.tile_chunk = int(p.tile_chunk);
   g.inv_group = 1.0f / float(g.group);
   g.inv_page16 = 16.0 / g.page;
   g.c = scale * 1.44269504088896340736f;
