@@ -10,6 +10,7 @@
 #include "mx_device.hpp"
 #include "mx_launch.hpp"
 
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -67,6 +68,26 @@ __global__ __launch_bounds__(256) void rope_table_kernel(const TableArgs g) {
 // ---------------------------------------------------------------------------
 // Rotation
 // ---------------------------------------------------------------------------
+// n / d for n < 2^31 as floor(n m / 2^(31 + s)), s = ceil(log2 d), m = ceil(2^(31 + s) / d) < 2^32: the
+// excess m d - 2^(31 + s) is below 2^s, so n times it is below 2^(31 + s).  A thread here moves a few
+// dozen bytes, which a division by the compiler (20 instructions, over 100 in 64 bits) would outweigh.
+struct Divisor {
+  uint32_t m, shift, d;
+  Divisor(uint32_t by = 1) : m(0), shift(0), d(by) {
+    uint32_t s = 0;
+    while ((uint64_t(1) << s) < by) ++s;
+    if (by > 1) {
+      m = uint32_t(((uint64_t(1) << (31 + s)) + by - 1) / by);
+      shift = s - 1;
+    }
+  }
+  __device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t& rest) const {
+    const uint32_t q = d == 1 ? n : __umulhi(n, m) >> shift;
+    rest = n - q * d;
+    return q;
+  }
+};
+
 struct RopeArgs {
   const void* x;
   void* y;
@@ -75,8 +96,8 @@ struct RopeArgs {
   int64_t tokens, rows;
   int64_t xt, xh, yt, yh;       // strides in elements
   int heads, dim, rot;
-  int chunks;                   // V-element accesses a head needs: rot / 2 / V pairs and (dim - rot) / V copies
-  int head_groups;
+  Divisor chunks;               // V-element accesses a head needs: rot / 2 / V pairs and (dim - rot) / V copies
+  Divisor head_groups;
   bool inverse;
 };
 
@@ -100,10 +121,48 @@ __device__ __forceinline__ typename Elem<IN>::T narrow(float v) {
   else return __builtin_bit_cast(uint16_t, _Float16(v));
 }
 
-// V storage elements moved with one access of up to 16 bytes.
+// V storage elements moved with one access of up to 16 bytes, as 32-bit words (words and not elements:
+// arrays of 16-bit elements would be kept in LDS by the compiler, not in registers).
 template <int IN, int V>
-struct alignas(V * sizeof(typename Elem<IN>::T)) Pack {
-  typename Elem<IN>::T e[V];
+struct Pack {
+  using T = typename Elem<IN>::T;
+  static constexpr int kBytes = V * int(sizeof(T)), kWords = (kBytes + 3) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kBytes == 16) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else if constexpr (kBytes == 8) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x; w[1] = x.y;
+    } else if constexpr (kBytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *p;
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (kBytes == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+    else *p = T(w[0]);
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (IN == IN_F32) return widen<IN>(w[j]);
+    else return widen<IN>(T(w[j / 2] >> (16 * (j & 1))));
+  }
+  // elements 0 .. V - 1 from FP32 values
+  __device__ __forceinline__ void set(const float (&v)[V]) {
+    if constexpr (IN == IN_F32) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) w[j] = narrow<IN>(v[j]);
+    } else if constexpr (V == 1) {
+      w[0] = narrow<IN>(v[0]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) w[j] = uint32_t(narrow<IN>(v[2 * j])) | uint32_t(narrow<IN>(v[2 * j + 1])) << 16;
+    }
+  }
 };
 
 // The cos / sin pairs of pairs [i, i + V) of a table row; NaN where the position
@@ -136,27 +195,25 @@ __device__ __forceinline__ void load_cs(const float2* __restrict__ table, int64_
 // One thread: one chunk (V pairs, or V copied channels) of HPT heads of one
 // token.  The table entries are loaded once for all its heads.
 template <int IN, int V, bool HALF, int HPT>
-__device__ __forceinline__ void rope_item(const RopeArgs& g, int64_t id) {
+__device__ __forceinline__ void rope_item(const RopeArgs& g, uint32_t id) {
   using P = Pack<IN, V>;
   using T = typename Elem<IN>::T;
-  const int ch = int(id % g.chunks);
-  const int64_t rest = id / g.chunks;
-  const int hg = int(rest % g.head_groups);
-  const int64_t t = rest / g.head_groups;
+  uint32_t ch, hg;
+  const int64_t t = g.head_groups.divide(g.chunks.divide(id, ch), hg);
   if (t >= g.tokens) return;
-  const int h0 = hg * HPT, nh = min(HPT, g.heads - h0);
+  const int h0 = int(hg) * HPT, nh = min(HPT, g.heads - h0);
   const T* x = static_cast<const T*>(g.x) + t * g.xt + h0 * g.xh;
   T* y = static_cast<T*>(g.y) + t * g.yt + h0 * g.yh;
-  const int pairs = g.rot / 2, i = ch * V;
+  const int pairs = g.rot / 2, i = int(ch) * V;
   if (i >= pairs) {                // channels past the rotation
     const int c = g.rot + (i - pairs);
     P p[HPT];
 #pragma unroll
     for (int h = 0; h < HPT; ++h)
-      if (h < nh) p[h] = *reinterpret_cast<const P*>(x + h * g.xh + c);
+      if (h < nh) p[h].load(x + h * g.xh + c);
 #pragma unroll
     for (int h = 0; h < HPT; ++h)
-      if (h < nh) *reinterpret_cast<P*>(y + h * g.yh + c) = p[h];
+      if (h < nh) p[h].store(y + h * g.yh + c);
     return;
   }
   const int ca = HALF ? i : 2 * i, cb = HALF ? i + pairs : 2 * i + V;
@@ -164,43 +221,42 @@ __device__ __forceinline__ void rope_item(const RopeArgs& g, int64_t id) {
 #pragma unroll
   for (int h = 0; h < HPT; ++h)
     if (h < nh) {
-      a[h] = *reinterpret_cast<const P*>(x + h * g.xh + ca);
-      b[h] = *reinterpret_cast<const P*>(x + h * g.xh + cb);
+      a[h].load(x + h * g.xh + ca);
+      b[h].load(x + h * g.xh + cb);
     }
   float c[V], s[V];
   load_cs<V>(g.table, g.rows, pairs, g.pos[t], i, g.inverse, c, s);
 #pragma unroll
   for (int h = 0; h < HPT; ++h)
     if (h < nh) {
-      P oa, ob;
-      if constexpr (HALF) {
+      float oa[V], ob[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float u = widen<IN>(a[h].e[j]), w = widen<IN>(b[h].e[j]);
-          oa.e[j] = narrow<IN>(u * c[j] - w * s[j]);
-          ob.e[j] = narrow<IN>(w * c[j] + u * s[j]);
+      for (int j = 0; j < V; ++j) {
+        // half: pair j is (a_j, b_j); interleaved: elements 2 j, 2 j + 1 of a followed by b
+        const float u = HALF ? a[h].get(j) : 2 * j < V ? a[h].get(2 * j) : b[h].get(2 * j - V);
+        const float w = HALF ? b[h].get(j) : 2 * j + 1 < V ? a[h].get(2 * j + 1) : b[h].get(2 * j + 1 - V);
+        const float p = u * c[j] - w * s[j], q = w * c[j] + u * s[j];
+        if (HALF) {
+          oa[j] = p;
+          ob[j] = q;
+        } else {
+          if (2 * j < V) oa[2 * j] = p;
+          else ob[2 * j - V] = p;
+          if (2 * j + 1 < V) oa[2 * j + 1] = q;
+          else ob[2 * j + 1 - V] = q;
         }
-      } else {
-        T in[2 * V], out[2 * V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) { in[j] = a[h].e[j]; in[V + j] = b[h].e[j]; }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float u = widen<IN>(in[2 * j]), w = widen<IN>(in[2 * j + 1]);
-          out[2 * j] = narrow<IN>(u * c[j] - w * s[j]);
-          out[2 * j + 1] = narrow<IN>(w * c[j] + u * s[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) { oa.e[j] = out[j]; ob.e[j] = out[V + j]; }
       }
-      *reinterpret_cast<P*>(y + h * g.yh + ca) = oa;
-      *reinterpret_cast<P*>(y + h * g.yh + cb) = ob;
+      P out;
+      out.set(oa);
+      out.store(y + h * g.yh + ca);
+      out.set(ob);
+      out.store(y + h * g.yh + cb);
     }
 }
 
 template <int IN, int V, bool HALF, int HPT>
 __global__ __launch_bounds__(256) void rope_kernel(const RopeArgs g) {
-  rope_item<IN, V, HALF, HPT>(g, int64_t(blockIdx.x) * 256 + threadIdx.x);
+  rope_item<IN, V, HALF, HPT>(g, blockIdx.x * 256 + threadIdx.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -215,7 +271,9 @@ struct AppendArgs {
   uint8_t *kc, *ks, *vc, *vs;
   int64_t tokens, slot_count;
   int kv_heads, page, dim;
-  int64_t q_blocks, kv_blocks;  // workgroups that rotate q, then those of k, then those of v
+  double inv_page;
+  Divisor per_head, head_groups;
+  uint32_t q_blocks, kv_blocks; // workgroups that rotate q, then those of k, then those of v
 };
 
 // Channel ch of the rotated key, element by element (any layout and alignment).
@@ -231,82 +289,99 @@ __device__ __forceinline__ float rotated_one(const typename Elem<IN>::T* x, cons
   return first ? own * c - other * s : own * c + other * s;
 }
 
-// 8 consecutive channels of a key or value from ch on (ch a multiple of 8).  VEC:
-// rows are 16-byte aligned and, where there is a rotation, rot / 2 is a multiple of 8,
-// so a chunk lies in one half (or one run of interleaved pairs) and so does its partner.
-template <int IN, bool VEC, bool HALF>
-__device__ __forceinline__ void load_rotated8(const AppendArgs& g, const void* base, int64_t off, bool rotate,
-                                              int32_t pos, int ch, float (&v)[8]) {
+// One thread: 8 consecutive channels from ch on (a multiple of 8) of HPT heads of one
+// token's keys (ROTATE) or values.  VEC: rows are 16-byte aligned and, where there is a
+// rotation, rot / 2 is a multiple of 8, so a chunk lies in one half (or one run of
+// interleaved pairs) and so does its partner.  The four lanes of a quad hold one block of 32.
+template <int IN, bool VEC, bool HALF, int HPT, bool ROTATE>
+__device__ __forceinline__ void append_item(const AppendArgs& g, const void* base, int64_t ts, int64_t hs, uint8_t* codes,
+                                            uint8_t* scales, uint32_t id) {
   using T = typename Elem<IN>::T;
-  const T* x = static_cast<const T*>(base) + off;
-  if constexpr (VEC) {
-    load8<IN>(x, ch, v);
-    if (!rotate || ch >= g.q.rot) return;
-    const int half = g.q.rot / 2;
-    if constexpr (HALF) {
-      const bool first = ch < half;
-      const int i = first ? ch : ch - half;
-      float p[8], c[8], s[8];
-      load8<IN>(x, first ? ch + half : i, p);
-      load_cs<8>(g.q.table, g.q.rows, half, pos, i, !first, c, s);
-      // first: own c - other s; second: own c + other s, a subtraction of the negated product
+  uint32_t c8, hg;
+  const int64_t t = g.head_groups.divide(g.per_head.divide(id, c8), hg);
+  if (t >= g.tokens) return;                            // whole quads leave together
+  const int ch = int(c8) * 8, h0 = int(hg) * HPT;
+  const T* x = static_cast<const T*>(base) + t * ts + h0 * hs;
+  const int half = g.q.rot / 2;
+  const bool turn = ROTATE && ch < g.q.rot;
+  const bool first = !HALF || ch < half;                // of a pair's halves
+  const int i = HALF ? (first ? ch : ch - half) : ch / 2;
+  float v[HPT][8], c[8], s[8], p[HPT][HALF ? 8 : 1];
+  const int64_t slot = g.slots[t];
+  const int32_t pos = ROTATE ? g.q.pos[t] : 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] * c[j] - p[j] * s[j];
+  for (int h = 0; h < HPT; ++h) {
+    if (h0 + h >= g.kv_heads) continue;
+    if constexpr (VEC) {
+      load8<IN>(x + h * hs, ch, v[h]);
+      if constexpr (HALF)
+        if (turn) load8<IN>(x + h * hs, first ? ch + half : i, p[h]);
     } else {
-      float c[4], s[4];
-      load_cs<4>(g.q.table, g.q.rows, half, pos, ch / 2, false, c, s);
+      const bool ok = ROTATE && pos >= 0 && pos < g.q.rows;
+      const float2* row = ok ? g.q.table + int64_t(pos) * half : nullptr;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = v[2 * j], b = v[2 * j + 1];
-        v[2 * j] = a * c[j] - b * s[j];
-        v[2 * j + 1] = b * c[j] + a * s[j];
+      for (int j = 0; j < 8; ++j)
+        v[h][j] = ROTATE ? rotated_one<IN, HALF>(x + h * hs, row, ok, g.q.rot, ch + j) : widen<IN>(x[h * hs + ch + j]);
+    }
+  }
+  if constexpr (VEC && ROTATE) {
+    if (turn) {
+      if constexpr (HALF) {
+        // first half: own c - other s; second: own c + other s, a subtraction of the negated product
+        load_cs<8>(g.q.table, g.q.rows, half, pos, i, !first, c, s);
+#pragma unroll
+        for (int h = 0; h < HPT; ++h)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[h][j] = v[h][j] * c[j] - p[h][j] * s[j];
+      } else {
+        float c4[4], s4[4];
+        load_cs<4>(g.q.table, g.q.rows, half, pos, i, false, c4, s4);
+#pragma unroll
+        for (int h = 0; h < HPT; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float a = v[h][2 * j], b = v[h][2 * j + 1];
+            v[h][2 * j] = a * c4[j] - b * s4[j];
+            v[h][2 * j + 1] = b * c4[j] + a * s4[j];
+          }
       }
     }
-  } else {
-    const bool ok = rotate && pos >= 0 && pos < g.q.rows;
-    const float2* row = ok ? g.q.table + int64_t(pos) * (g.q.rot / 2) : nullptr;
+  }
+  const bool store = slot >= 0 && slot < g.slot_count;
+  const int64_t page = int64_t((double(slot) + 0.5) * g.inv_page);      // slot < 2^34: exact
+  const int64_t row0 = (page * g.kv_heads + h0) * g.page + (slot - page * g.page);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = rotate ? rotated_one<IN, HALF>(x, row, ok, g.q.rot, ch + j) : widen<IN>(x[ch + j]);
+  for (int h = 0; h < HPT; ++h) {
+    if (h0 + h >= g.kv_heads) continue;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = umax(m, abs_bits(v[h][j]));
+    m = quad_max(m);
+    uint32_t w[2];
+    const uint32_t scale = mx_encode_f32<E4M3, CEIL, 8>(v[h], m, w);
+    if (!store) continue;
+    const int64_t row = row0 + int64_t(h) * g.page;
+    *reinterpret_cast<uint2*>(codes + row * g.dim + ch) = make_uint2(w[0], w[1]);
+    if ((c8 & 3) == 0) scales[row * (g.dim / 32) + c8 / 4] = uint8_t(scale);
   }
 }
 
 // One launch does all three tensors: the first q_blocks workgroups rotate q, the
-// next kv_blocks rotate and encode k, the last kv_blocks encode v.  A thread
-// encodes 8 channels; the four lanes of a quad share a block's amax.
+// next kv_blocks rotate and encode k, the last kv_blocks encode v.
 template <int IN, int VQ, bool HALF, int HPT, bool VEC>
 __global__ __launch_bounds__(256) void append_kernel(const AppendArgs g) {
-  int64_t b = blockIdx.x;
+  uint32_t b = blockIdx.x;
   if (b < g.q_blocks) {
     rope_item<IN, VQ, HALF, HPT>(g.q, b * 256 + threadIdx.x);
     return;
   }
   b -= g.q_blocks;
-  const bool is_k = b < g.kv_blocks;
-  if (!is_k) b -= g.kv_blocks;
-  const int per_head = g.dim / 8;                       // a multiple of 4, so a quad stays in one block
-  const int64_t id = b * 256 + threadIdx.x;
-  const int c8 = int(id % per_head);
-  const int64_t rest = id / per_head;
-  const int h = int(rest % g.kv_heads);
-  const int64_t t = rest / g.kv_heads;
-  if (t >= g.tokens) return;                            // whole quads leave together
-  float v[8];
-  if (is_k) load_rotated8<IN, VEC, HALF>(g, g.k, t * g.kt + h * g.kh, g.q.table != nullptr,
-                                         g.q.table ? g.q.pos[t] : 0, 8 * c8, v);
-  else load_rotated8<IN, VEC, HALF>(g, g.v, t * g.vt + h * g.vh, false, 0, 8 * c8, v);
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = umax(m, abs_bits(v[j]));
-  m = quad_max(m);
-  uint32_t w[2];
-  const uint32_t scale = mx_encode_f32<E4M3, CEIL, 8>(v, m, w);
-  const int64_t slot = g.slots[t];
-  if (slot < 0 || slot >= g.slot_count) return;
-  const int64_t page = slot / g.page, at = slot - page * g.page;
-  const int64_t row = (page * g.kv_heads + h) * g.page + at;
-  *reinterpret_cast<uint2*>((is_k ? g.kc : g.vc) + row * g.dim + 8 * c8) = make_uint2(w[0], w[1]);
-  if ((c8 & 3) == 0) (is_k ? g.ks : g.vs)[row * (g.dim / 32) + c8 / 4] = uint8_t(scale);
+  if (b >= g.kv_blocks)
+    append_item<IN, VEC, HALF, HPT, false>(g, g.v, g.vt, g.vh, g.vc, g.vs, (b - g.kv_blocks) * 256 + threadIdx.x);
+  else if (g.q.table)
+    append_item<IN, VEC, HALF, HPT, true>(g, g.k, g.kt, g.kh, g.kc, g.ks, b * 256 + threadIdx.x);
+  else
+    append_item<IN, VEC, HALF, HPT, false>(g, g.k, g.kt, g.kh, g.kc, g.ks, b * 256 + threadIdx.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -341,8 +416,8 @@ void fill_rope(RopeArgs& g, const void* x, void* y, int64_t tokens, int heads, i
   g.x = x; g.y = y; g.pos = pos; g.table = reinterpret_cast<const float2*>(table);
   g.tokens = tokens; g.rows = rows; g.xt = xt; g.xh = xh; g.yt = yt; g.yh = yh;
   g.heads = heads; g.dim = dim; g.rot = rot; g.inverse = inverse;
-  g.chunks = (rot / 2 + dim - rot) / v;
-  g.head_groups = (heads + hpt - 1) / hpt;
+  g.chunks = Divisor(uint32_t((rot / 2 + dim - rot) / v));
+  g.head_groups = Divisor(uint32_t((heads + hpt - 1) / hpt));
 }
 
 inline mx_status_t launched() { return hipGetLastError() == hipSuccess ? MX_OK : MX_ERR_LAUNCH; }
@@ -431,19 +506,26 @@ extern "C" mx_status_t mx_rope(const void* x, mx_dtype_t dtype, int64_t tokens, 
   if (both % elem_size(dtype) || misaligned(table) || (reinterpret_cast<uintptr_t>(pos) & 3u)) return MX_ERR_ALIGN;
   const int v = rope_vector(dtype, dim, rot, x, y, x_token_stride, x_head_stride, y_token_stride, y_head_stride);
   const int hpt = heads_per_thread(tokens, heads, (rot / 2 + dim - rot) / v);
-  RopeArgs g;
-  fill_rope(g, x, y, tokens, heads, dim, x_token_stride, x_head_stride, y_token_stride, y_head_stride, pos, table, rows,
-            rot, inverse != 0, v, hpt);
-  const int64_t blocks = (tokens * g.head_groups * g.chunks + 255) / 256;
-  if (blocks > 0x7FFFFFFF) return MX_ERR_SHAPE;
-  with_type(dtype, [&](auto in) {
-    constexpr int IN = decltype(in)::value;
-    with_variant<IN>(v, hpt, [&](auto vv, auto hh) {
-      constexpr int V = decltype(vv)::value, H = decltype(hh)::value;
-      if (layout == MX_ROPE_HALF) rope_kernel<IN, V, true, H><<<unsigned(blocks), 256, 0, stream>>>(g);
-      else rope_kernel<IN, V, false, H><<<unsigned(blocks), 256, 0, stream>>>(g);
+  // thread numbers are kept below 2^31: longer inputs go in several launches
+  const int64_t per_token = int64_t((heads + hpt - 1) / hpt) * ((rot / 2 + dim - rot) / v);
+  const int64_t slab = int64_t(0x7FFFFE00) / per_token;
+  const int64_t size = elem_size(dtype);
+  for (int64_t t = 0; t < tokens; t += slab) {
+    const int64_t n = std::min(slab, tokens - t);
+    RopeArgs g;
+    fill_rope(g, static_cast<const uint8_t*>(x) + t * x_token_stride * size, static_cast<uint8_t*>(y) + t * y_token_stride * size,
+              n, heads, dim, x_token_stride, x_head_stride, y_token_stride, y_head_stride, pos + t, table, rows, rot,
+              inverse != 0, v, hpt);
+    const unsigned blocks = unsigned((n * per_token + 255) / 256);
+    with_type(dtype, [&](auto in) {
+      constexpr int IN = decltype(in)::value;
+      with_variant<IN>(v, hpt, [&](auto vv, auto hh) {
+        constexpr int V = decltype(vv)::value, H = decltype(hh)::value;
+        if (layout == MX_ROPE_HALF) rope_kernel<IN, V, true, H><<<blocks, 256, 0, stream>>>(g);
+        else rope_kernel<IN, V, false, H><<<blocks, 256, 0, stream>>>(g);
+      });
     });
-  });
+  }
   return launched();
 }
 
@@ -471,13 +553,15 @@ extern "C" mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dty
     return MX_ERR_ALIGN;
   if (q && (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out)) % size) return MX_ERR_ALIGN;
   AppendArgs g = {};
-  int vq = 16 / size, hpt = 1;
+  int64_t q_blocks = 0;
+  const int kv_heads = cache->kv_heads;
+  int vq = 16 / size, hpt = heads_per_thread(tokens, kv_heads, dim / 8);
   if (q) {
     vq = rope_vector(dtype, dim, rot, q, q_out, q_token_stride, q_head_stride, int64_t(heads) * dim, dim);
-    hpt = heads_per_thread(tokens, heads, (rot / 2 + dim - rot) / vq);
+    hpt = std::max(hpt, heads_per_thread(tokens, heads, (rot / 2 + dim - rot) / vq));
     fill_rope(g.q, q, q_out, tokens, heads, dim, q_token_stride, q_head_stride, int64_t(heads) * dim, dim, pos, table,
               rows, rot, false, vq, hpt);
-    g.q_blocks = (tokens * g.q.head_groups * g.q.chunks + 255) / 256;
+    q_blocks = (tokens * g.q.head_groups.d * g.q.chunks.d + 255) / 256;
   } else {
     g.q.table = reinterpret_cast<const float2*>(table);
     g.q.pos = pos;
@@ -490,9 +574,15 @@ extern "C" mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dty
   g.tokens = tokens;
   g.slot_count = cache->pages * cache->page;
   g.kv_heads = cache->kv_heads; g.page = cache->page; g.dim = dim;
-  g.kv_blocks = (tokens * cache->kv_heads * (dim / 8) + 255) / 256;
-  const int64_t blocks = g.q_blocks + 2 * g.kv_blocks;
-  if (blocks > 0x7FFFFFFF) return MX_ERR_SHAPE;
+  g.inv_page = 1.0 / cache->page;
+  g.per_head = Divisor(uint32_t(dim / 8));              // a multiple of 4, so a quad stays in one block of 32
+  g.head_groups = Divisor(uint32_t((kv_heads + hpt - 1) / hpt));
+  const int64_t kv_blocks = (tokens * g.head_groups.d * (dim / 8) + 255) / 256;
+  // thread numbers are kept below 2^31
+  if (q_blocks > 0x7FFFFF || kv_blocks > 0x7FFFFF) return MX_ERR_SHAPE;
+  g.q_blocks = uint32_t(q_blocks);
+  g.kv_blocks = uint32_t(kv_blocks);
+  const int64_t blocks = q_blocks + 2 * kv_blocks;
   // 16-byte loads of keys and values: aligned rows, and no 8-channel chunk across the rotation's borders
   const int64_t strides = k_token_stride | k_head_stride | v_token_stride | v_head_stride;
   const bool vec = (kv & 15u) == 0 && strides % (16 / size) == 0 && (!table || (rot / 2) % 8 == 0);
