@@ -784,12 +784,12 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
     for (int v = 0; v < 16; ++v) o[t][v] = 0.0f;
 
   // ---- this wave's 16 keys or values of a tile
-  // (a wave that decodes only keys or only values holds them in the same registers)
   constexpr int kWordsV = L::kA == 8 ? 2 : 1, kRuns = L::kB ? 2 : 1;
-  constexpr int kAtV = NW == 8 ? 0 : 4 * kKLoads, kAtVs = NW == 8 ? 0 : kKLoads;
-  uint32_t raw[std::max(4 * kKLoads, kAtV + 8 * (kWordsV + kRuns - 1))], sc[std::max(kKLoads, kAtVs + 8 * kRuns)];
-  auto rv = [&](int j, int w) -> uint32_t& { return raw[kAtV + 8 * w + j]; };    // word w of key j; w == kWordsV: second run
-  auto rvs = [&](int j, int run) -> uint32_t& { return sc[kAtVs + 8 * run + j]; };
+  uint32_t raw[4 * kKLoads], sc[kKLoads];                // keys
+  uint32_t rawv[8 * (kWordsV + kRuns - 1)], scv[8 * kRuns];
+  auto rv = [&](int j, int w) -> uint32_t& { return rawv[8 * w + j]; };          // word w of key j; w == kWordsV: second run
+  auto rvs = [&](int j, int run) -> uint32_t& { return scv[8 * run + j]; };
+  int pending = -1;                              // row group of what is loaded; negative: nothing to read
   int groups = -1;
   const int32_t* table = g.table + req * g.table_stride;
   auto load = [&](int tile0) {
@@ -797,8 +797,11 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
       const int key = tile0 + lane * 16, col = page_column(g, key);
       groups = row_group(g, hk, key, col, page_entry(g, table, col), lo, hi);
     }
-    const int grp = __builtin_amdgcn_readlane(groups, ((tile0 - start) & 1023) / 16 + part);
-    if (grp >= 0) {
+    pending = __builtin_amdgcn_readlane(groups, ((tile0 - start) & 1023) / 16 + part);
+    // What is loaded must reach its registers with no copy behind it, which would wait for the load: no other
+    // path writes them here, and a group that is not to be read loads group 0 (decode() puts it right)
+    if (g.pages > 0) {
+      const int grp = max(pending, 0);
       const uint8_t* k = g.kc + int64_t(grp) * 16 * D;
       const uint8_t* ks = g.ks + int64_t(grp) * 16 * (D / 32);
       if (decodes_k) {
@@ -812,7 +815,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
           }
         }
       }
-      if (!decodes_v) return;
+      if (decodes_v) {
       const uint8_t* v = g.vc + int64_t(grp) * 16 * D + 8 * h * D;
       const uint8_t* vs = g.vs + int64_t(grp) * 16 * (D / 32) + 8 * h * (D / 32);
 #pragma unroll
@@ -834,26 +837,24 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
           rvs(j, 1) = vs[j * (D / 32) + (32 * L::kA + L::kB * r) / 32];
         }
       }
-    } else {                                     // keys of a bad page are NaN, and so is what sees them
-      if (decodes_k) {
-#pragma unroll
-        for (int u = 0; u < 4 * kKLoads; ++u) raw[u] = 0x7F7F7F7Fu;
-#pragma unroll
-        for (int u = 0; u < kKLoads; ++u) sc[u] = 127;
-      }
-      if (decodes_v) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-#pragma unroll
-          for (int w = 0; w < kWordsV + kRuns - 1; ++w) rv(j, w) = 0;
-#pragma unroll
-          for (int w = 0; w < kRuns; ++w) rvs(j, w) = 127;
-        }
       }
     }
   };
   auto decode = [&](int tile0, int buf) {
     uint8_t* base = lds.k[buf];
+    if (__builtin_expect(pending < 0, 0)) {      // keys of a bad page are NaN, and so is what sees them
+#pragma unroll
+      for (int u = 0; u < 4 * kKLoads; ++u) raw[u] = 0x7F7F7F7Fu;
+#pragma unroll
+      for (int u = 0; u < kKLoads; ++u) sc[u] = 127;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int w = 0; w < kWordsV + kRuns - 1; ++w) rv(j, w) = 0;
+#pragma unroll
+        for (int w = 0; w < kRuns; ++w) rvs(j, w) = 127;
+      }
+    }
     if (decodes_k)
 #pragma unroll
     for (int u = 0; u < kKLoads; ++u) {
