@@ -697,8 +697,8 @@ __device__ __forceinline__ v16f_t mfma32(u32x4_t a, u32x4_t b, v16f_t acc) {
 //     meet 8 different groups of banks.
 // Bound by vector work beside the matrix unit: a tile of 256 rows x 64 keys x 128 channels
 // has 2048 clocks of matrix instructions and about as many of vector instructions on every
-// SIMD, and takes 4400.  Measured: 2048 tokens over 32768 keys (32 and 8 heads of 128
-// channels) in 1080 to 1110 us, 0.96 to 0.99 PFLOP/s; each wave reading the pages by itself
+// SIMD, and takes 4000.  Measured: 2048 tokens over 32768 keys (32 and 8 heads of 128
+// channels) in 975 to 1000 us, 1.07 to 1.09 PFLOP/s; each wave reading the pages by itself
 // took 2783 us.
 template <int D, int NW> struct TileLds {
   static constexpr int kFrag = 1040;
@@ -1005,7 +1005,10 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) o[t] *= a;
     }
-    // ---- weights
+    // ---- weights.  Of the two waves of a SIMD, the one that has come this far goes first until its values
+    // are added: it mixes matrix and vector instructions, the other has only matrix ones (2048 tokens over
+    // 32768: 983 us without, 975 with; workgroups of four waves lose 1% by it)
+    if constexpr (NW == 8) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       float e[8];
@@ -1038,6 +1041,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
       }
       score(tile0, buf);
       add_values(buf);
+      if constexpr (NW == 8) __builtin_amdgcn_s_setprio(0);
       __syncthreads();
       buf ^= 1;
     }
@@ -1246,7 +1250,7 @@ mx_status_t plan_attention(int64_t tokens, int heads, int kv_heads, int dim, int
   p.few_chunk = p.waves == 4 ? 256 : cut(keys, std::min(most, (cus + few_wgs - 1) / std::max<int64_t>(few_wgs, 1)), 512);
   p.few_splits = (keys + p.few_chunk - 1) / p.few_chunk;
   // Requests of many rows.  Workgroups of eight waves (one fits a CU) where they fill the CUs: a tile of
-  // keys is decoded for twice the rows (2048 tokens over 32768: 1079 us, with four waves 1121).  Fewer
+  // keys is decoded for twice the rows (2048 tokens over 32768: 4% less time).  Fewer
   // are spread better by workgroups of four waves, of which two fit a CU up to 128 channels (300 tokens
   // alone: 14.8 us, with eight waves 17.9).
   // Then the number of splits with the least estimate of rounds over the CUs plus partial results: a tile of
