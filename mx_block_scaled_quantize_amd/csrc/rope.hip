@@ -414,7 +414,7 @@ int rope_vector(mx_dtype_t dt, int dim, int rot, const void* x, const void* y, i
 // small call then has too few threads to cover the load latency: four from 2^18 chunks
 // on, 256 waves for every XCD.
 inline int heads_per_thread(int64_t tokens, int heads, int chunks) {
-  return tokens * heads * chunks >= (int64_t(1) << 18) && heads >= 4 ? 4 : 1;
+  return tokens * heads >= ((int64_t(1) << 18) + chunks - 1) / chunks && heads >= 4 ? 4 : 1;
 }
 
 void fill_rope(RopeArgs& g, const void* x, void* y, int64_t tokens, int heads, int dim, int64_t xt, int64_t xh,
@@ -513,7 +513,8 @@ extern "C" mx_status_t mx_rope(const void* x, mx_dtype_t dtype, int64_t tokens, 
   if (both % elem_size(dtype) || misaligned(table) || (reinterpret_cast<uintptr_t>(pos) & 3u)) return MX_ERR_ALIGN;
   const int v = rope_vector(dtype, dim, rot, x, y, x_token_stride, x_head_stride, y_token_stride, y_head_stride);
   const int hpt = heads_per_thread(tokens, heads, (rot / 2 + dim - rot) / v);
-  // thread numbers are kept below 2^31: longer inputs go in several launches
+  // thread numbers are kept below 2^31: longer inputs go in several launches (a token of 65536 heads of
+  // 65536 channels has 2^30 threads, as four heads go to each)
   const int64_t per_token = int64_t((heads + hpt - 1) / hpt) * ((rot / 2 + dim - rot) / v);
   const int64_t slab = int64_t(0x7FFFFE00) / per_token;
   const int64_t size = elem_size(dtype);
