@@ -446,8 +446,10 @@ mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dtype, int64_t
  *          [tokens][heads] or NULL.
  *   workspace  mx_paged_attention_workspace bytes (16-byte aligned; may be NULL when that is 0);
  *          its contents need no preparation and are not kept between calls.
- * Scores, softmax sums and outputs are accumulated in FP32; the softmax weights are
- * rounded to the type of q before the product with the values.  The cache's elements
+ * Scores, softmax sums and outputs are accumulated in FP32.  The softmax weights enter
+ * the product with the values as two terms of the type of q (16 bits and more together)
+ * for requests of up to 32 rows (query tokens x heads / kv_heads), rounded to that type
+ * for longer ones.  The cache's elements
  * are decoded to that type, exactly but for its range: with F16 queries, cached
  * magnitudes that round to 2^16 are infinite and those below 2^-24 fade out.  The
  * order of all sums is fixed by the arguments.

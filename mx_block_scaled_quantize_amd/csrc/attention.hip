@@ -108,6 +108,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2h_t));
 }
 
+// Half `HI` of a packed pair.
+template <int DT, bool HI>
+__device__ __forceinline__ float unpack(uint32_t w) {
+  if constexpr (DT == IN_BF16) return __uint_as_float(HI ? w & 0xFFFF0000u : w << 16);
+  else return float(__builtin_bit_cast(v2h_t, w)[HI ? 1 : 0]);
+}
+
 // How a value row of D channels is dealt to the 16 lanes of a row of the matrix
 // unit: kA contiguous channels each of the first 16 kA, then kB each of the rest,
 // powers of two, so that a lane's run lies in one block of 32.
@@ -566,8 +573,10 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, 
         for (int t = 0; t < kTiles; ++t) o[n][t] *= a;
       }
     }
-    // ---- weights
-    u32x4_t p[NQ];
+    // ---- weights, in two terms of the type of q: one alone is off by up to 2^-9 (BF16), which outputs of
+    // the same type would show (error against 64 bits 0.0023, with both 0.0017, the outputs' own rounding).
+    // The second product costs 1% where memory bounds (64 requests of 8192 keys: 135.0 us without, 136.3 with).
+    u32x4_t p[NQ], rest[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       float e[8];
@@ -575,11 +584,14 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, 
       for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j >> 2][j & 3], g.c, -mref[n]));
       l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
       p[n] = u32x4_t{pack2<DT>(e[0], e[1]), pack2<DT>(e[2], e[3]), pack2<DT>(e[4], e[5]), pack2<DT>(e[6], e[7])};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        rest[n][j] = pack2<DT>(e[2 * j] - unpack<DT, false>(p[n][j]), e[2 * j + 1] - unpack<DT, true>(p[n][j]));
     }
     // ---- O^T
     for_tiles([&](int t, u32x4_t a) {
 #pragma unroll
-      for (int n = 0; n < NQ; ++n) o[n][t] = mfma16<DT>(a, p[n], o[n][t]);
+      for (int n = 0; n < NQ; ++n) o[n][t] = mfma16<DT>(a, rest[n], mfma16<DT>(a, p[n], o[n][t]));
     });
   };
 
