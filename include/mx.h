@@ -436,7 +436,7 @@ mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dtype, int64_t
  *   page_table  int32 [requests][table_cols], row stride table_stride; entries past a
  *          request's length, or before its window, may hold anything.  A query that sees a
  *          token whose page number is outside [0, pages) or whose place is past
- *          table_cols gives NaN.
+ *          table_cols gives NaN.  NULL only where table_cols is 0.
  *   cu     int32 [requests + 1], non-decreasing; tokens outside every request keep
  *          what out and lse held.
  *          At most 65535 requests.

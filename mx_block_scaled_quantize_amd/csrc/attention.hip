@@ -1348,7 +1348,7 @@ extern "C" mx_status_t mx_paged_attention(const void* q, mx_dtype_t dtype, int64
   if (table_cols < 0 || table_stride < 0) return MX_ERR_SHAPE;
   if (max_q < 0 || max_kv < 0 || window < 0 || !(scale > 0.0f) || !std::isfinite(scale)) return MX_ERR_ARG;
   if (tokens == 0 || requests == 0) return MX_OK;
-  if (!q || !cu || !lens || !out || (max_kv > 0 && !page_table)) return MX_ERR_NULL;
+  if (!q || !cu || !lens || !out || (table_cols > 0 && !page_table)) return MX_ERR_NULL;
   if (cache->pages > 0 && (!cache->k || !cache->k_scales || !cache->v || !cache->v_scales)) return MX_ERR_NULL;
   if (misaligned(q) || misaligned(out) || misaligned(cache->k) || misaligned(cache->v) ||
       misaligned(cache->k_scales) || misaligned(cache->v_scales) || misaligned(workspace) ||
