@@ -1217,6 +1217,7 @@ struct Plan {
   int tile_waves;               // of attention_tile_kernel: 32 rows each
   int64_t tile_units;           // most row tiles that requests of many rows can have
   int64_t few_splits, few_chunk, tile_splits, tile_chunk, slots;
+  int64_t window;               // 0: none, or none that a request of max_kv tokens would notice
   int64_t bytes;                // workspace
 };
 
@@ -1233,6 +1234,8 @@ mx_status_t plan_attention(int64_t tokens, int heads, int kv_heads, int dim, int
   if (tokens > lim || requests > 65535 || max_kv > lim || max_q > lim || tokens * heads > 0x7FFFFFFF) return MX_ERR_SHAPE;
   const int64_t cus = device_cus();
   if (cus <= 0) return MX_ERR_LAUNCH;
+  // from here on below 2^30, so that sums with it do not overflow
+  p.window = window >= max_kv ? 0 : window;
   const int64_t group = heads / kv_heads, reqs = std::max<int64_t>(requests, 1), base = reqs * kv_heads;
   max_q = std::min(max_q, tokens);
   const int64_t rows = std::max<int64_t>(max_q * group, 1);
@@ -1240,7 +1243,7 @@ mx_status_t plan_attention(int64_t tokens, int heads, int kv_heads, int dim, int
   p.nq = rows <= 16 ? 1 : 2;
   // keys that the rows of one workgroup can see
   auto seen = [&](int64_t n) {
-    const int64_t keys = window > 0 ? std::min(max_kv, window + n / group + 33) : max_kv;
+    const int64_t keys = p.window > 0 ? std::min(max_kv, p.window + n / group + 33) : max_kv;
     return std::max<int64_t>((keys + 63) / 64 * 64, 64);
   };
   // Requests of few rows: workgroups of eight waves, one for every CU (measured against two and
@@ -1372,7 +1375,7 @@ extern "C" mx_status_t mx_paged_attention(const void* q, mx_dtype_t dtype, int64
   g.part_ml = g.part ? g.part + tokens * heads * p.slots * cache->dim : nullptr;
   g.tokens = tokens; g.max_q = max_q; g.max_kv = max_kv;
   g.heads = heads; g.kv_heads = cache->kv_heads; g.group = heads / cache->kv_heads; g.page = cache->page;
-  g.window = int(std::min<int64_t>(window, int64_t(1) << 30));
+  g.window = int(p.window);
   g.requests = int(requests); g.tile_units = int(p.tile_units); g.slots = int(p.slots);
   g.few_splits = int(p.few_splits); g.few_chunk = int(p.few_chunk);
   g.tile_splits = int(p.tile_splits); g.tile_chunk = int(p.tile_chunk);
