@@ -1149,9 +1149,11 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs g, i
     for (int i0 = 0; i0 < g.slots; i0 += 64) {
       // lane i holds the weight of split i0 + i
       float w = 0.0f, li = 0.0f;
+      bool held = false;
       if (i0 + lane < g.slots) {
         li = ml[2 * (i0 + lane) + 1];
         const float mi = ml[2 * (i0 + lane)];
+        held = li != 0.0f;
         w = li == 0.0f ? 0.0f : mi == top ? 1.0f : __builtin_amdgcn_exp2f(mi - top);
         li = li == 0.0f ? 0.0f : w * li;
       }
@@ -1159,7 +1161,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttnArgs g, i
       for (int off = 32; off >= 1; off >>= 1) li += __shfl_xor(li, off, 64);
       sum += li;
       const float* o = g.part + (row * g.slots + i0) * D;
-      uint64_t left = __ballot(w != 0.0f);       // slots that hold something (NaN weights too)
+      uint64_t left = __ballot(held);            // a weight that has vanished still brings a NaN of its slot
       for (int i = 0; i < sub; ++i) left &= left - 1;
       while (left) {
         // up to four slots, loads first
