@@ -451,8 +451,10 @@ mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dtype, int64_t
  * for requests of up to 32 rows (query tokens x heads / kv_heads), rounded to that type
  * for longer ones.  The cache's elements
  * are decoded to that type, exactly but for its range: with F16 queries, cached
- * magnitudes that round to 2^16 are infinite and those below 2^-24 fade out.  A value that is
- * NaN makes every query that sees it NaN, however small its weight.  The
+ * magnitudes that round to 2^16 are infinite and those below 2^-24 fade out (BF16: from 2^128 on).  A
+ * value that is NaN makes every query that sees it NaN, however small its weight, and an infinite
+ * one makes it infinite, or NaN where its weight is too small for the type of q; neither
+ * touches other queries.  The
  * order of all sums is fixed by the arguments.
  * Errors: MX_ERR_UNSUPPORTED (dtype), MX_ERR_SHAPE (also a workspace too small), MX_ERR_ARG (scale not finite > 0,
  * window, max_q or max_kv negative), MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */

@@ -108,12 +108,53 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, v2h_t));
 }
 
+// The same, rounded towards 0.
+template <int DT>
+__device__ __forceinline__ uint32_t chop2(float a, float b) {
+  if constexpr (DT == IN_BF16) return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+  else return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+}
+
+typedef uint16_t v2u_t __attribute__((ext_vector_type(2)));
+// The larger, the smaller halves (of numbers that are not negative, which compare as their bits do).
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(v2u_t, a), __builtin_bit_cast(v2u_t, b)));
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(v2u_t, a), __builtin_bit_cast(v2u_t, b)));
+}
+
 // Half `HI` of a packed pair.
 template <int DT, bool HI>
 __device__ __forceinline__ float unpack(uint32_t w) {
   if constexpr (DT == IN_BF16) return __uint_as_float(HI ? w & 0xFFFF0000u : w << 16);
   else return float(__builtin_bit_cast(v2h_t, w)[HI ? 1 : 0]);
 }
+
+// A weight of 0 times a value that is infinite or NaN would be NaN for rows that do not see it.  Such
+// elements are taken out of the product of weights and values; products of marks (1 in their places) with
+// 1 for every key that a row sees count them for the rows that do, once with +inf and NaN marked and once
+// with -inf and NaN, so that a NaN adds both infinities.
+template <int DT> constexpr uint32_t kOneBits = DT == IN_BF16 ? 0x3F80u : 0x3C00u;
+
+// Takes the elements that are infinite or NaN out of a decoded fragment and marks them.
+template <int DT>
+__device__ __forceinline__ void take_marks(u32x4_t& x, u32x4_t& plus, u32x4_t& minus) {
+  // added to a half without its sign: its top bit is set from infinity on
+  constexpr uint32_t kUp = (0x8000u - (DT == IN_BF16 ? 0x7F80u : 0x7C00u)) * 0x00010001u;
+  auto halves = [](uint32_t top) { return (top << 1) - (top >> 15); };       // all bits of the halves whose top bit is set
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t size = x[j] & 0x7FFF7FFFu, sign = x[j] & 0x80008000u;
+    const uint32_t odd = (size + kUp) & 0x80008000u, nan = (size + (kUp - 0x00010001u)) & odd;
+    plus[j] = halves(odd & (~sign | nan)) & (kOneBits<DT> * 0x00010001u);
+    minus[j] = halves(odd & (sign | nan)) & (kOneBits<DT> * 0x00010001u);
+    x[j] &= ~halves(odd);
+  }
+}
+
+// 0 for a count of 0, else infinity.
+__device__ __forceinline__ float infinity_of(float count) { return count * 0x1p127f * 0x1p127f; }
 
 // How a value row of D channels is dealt to the 16 lanes of a row of the matrix
 // unit: kA contiguous channels each of the first 16 kA, then kB each of the rest,
@@ -124,6 +165,20 @@ template <int D> struct Deal {
   static constexpr int kWordsA = kA / 4, kWordsB = kB ? 1 : 0, kWords = kWordsA + kWordsB;
   static constexpr int kScales = kB ? 2 : 1;
 };
+
+// The least power of two beyond the type of q, as a scale code, and the least scale code with which an element
+// of 2^8 (E4M3's largest is 448) gets there.
+template <int DT> constexpr uint32_t kBeyond = DT == IN_F16 ? 127 + 16 : 127 + 128;
+template <int DT> constexpr uint32_t kWideScale = kBeyond<DT> - 8;
+
+// The least magnitude of an E4M3 code that is NaN or, with a scale code, beyond the type of q: without compares,
+// whose masks would not fit the scalar registers where many keys are looked at.
+template <int DT>
+__device__ __forceinline__ uint32_t least_odd_code(uint32_t scale) {
+  const int e = int(kBeyond<DT> - scale);        // exponent from which an element is
+  const int normal = min((e + 7) * 8, 0x7F), subnormal = 8 >> min(max(-6 - e, 0), 3);
+  return uint32_t(max(normal, subnormal)) & (((scale + 1) >> 8) - 1);     // 0 for the scale NaN
+}
 
 __device__ __forceinline__ uint32_t any_nan_code(uint32_t w) {   // nonzero if a byte is an E4M3 NaN
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
@@ -452,32 +507,34 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, 
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int w = 0; w < L::kScales; ++w) vsc[j][w] = v_scale(raw, j, w);
-    // decodes channels of word w of the lane's run, all 8 keys, into two fragments
-    auto fragments = [&](int w, auto hi_half, u32x4_t& a, u32x4_t& c) {
+    // decodes channels of word w of the lane's run, all 8 keys, into two fragments; code(j, w, run) and
+    // scale(j, run) are key j's word and scale operand
+    auto fragments = [&](int w, auto hi_half, auto code, auto scale, u32x4_t& a, u32x4_t& c) {
       constexpr bool HI = decltype(hi_half)::value;
       const int run = L::kScales > 1 && w >= L::kWordsA ? 1 : 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t x = decode2<DT, HI>(raw.v[2 * j][w], vsc[2 * j][run]);
-        const uint32_t y = decode2<DT, HI>(raw.v[2 * j + 1][w], vsc[2 * j + 1][run]);
+        const uint32_t x = decode2<DT, HI>(code(2 * j, w, run), scale(2 * j, run));
+        const uint32_t y = decode2<DT, HI>(code(2 * j + 1, w, run), scale(2 * j + 1, run));
         a[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
         c[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
       }
     };
-    auto for_tiles = [&](auto f) {   // f(tile, fragment)
+    auto for_tiles = [&](auto code, auto scale, auto f) {   // f(tile, fragment)
 #pragma unroll
       for (int w = 0; w < L::kWords; ++w) {
         u32x4_t a, c;
-        fragments(w, std::false_type{}, a, c);
+        fragments(w, std::false_type{}, code, scale, a, c);
         f(4 * w, a); f(4 * w + 1, c);
         if (4 * w + 2 < kTiles) {
-          fragments(w, std::true_type{}, a, c);
+          fragments(w, std::true_type{}, code, scale, a, c);
           f(4 * w + 2, a); f(4 * w + 3, c);
         }
       }
     };
     // ---- masks: only a step that some row does not see whole needs them
-    if (key0 + 32 > all_to || key0 < all_from) {
+    const bool edge = key0 + 32 > all_to || key0 < all_from;
+    if (edge) {
       // key 8 quarter + j of the step is seen by row n iff unsigned(j - from) < many
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -486,67 +543,62 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, 
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[n][j >> 2][j & 3] = uint32_t(j) - from < many ? s[n][j >> 2][j & 3] : -__builtin_inff();
       }
-      // values that no row sees may be anything; the weight 0 must not meet a NaN there
+      // values that no row sees may be anything; the weight 0 must not meet an infinity or a NaN there
       const uint32_t from = uint32_t(lo - key0 - 8 * quarter), many = uint32_t(max(hi - lo, 0));
-      uint32_t nan = 0;
+      uint32_t nans = 0, widest = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const bool keep = uint32_t(j) - from < many;
 #pragma unroll
         for (int w = 0; w < L::kWords; ++w) {
           raw.v[j][w] = keep ? raw.v[j][w] : 0u;
-          nan |= any_nan_code(raw.v[j][w]);
+          nans |= any_nan_code(raw.v[j][w]);
         }
 #pragma unroll
         for (int w = 0; w < L::kScales; ++w) {
           vsc[j][w] = keep ? vsc[j][w] : 127u << 23;
-          nan |= (vsc[j][w] & 0x7F800000u) == 0x7F800000u ? 1u : 0u;
+          widest = umax(widest, vsc[j][w] & 0x7F800000u);
         }
       }
-      // A NaN value that some rows see and others do not: 0 * NaN would reach them all.  Such values
-      // are taken out, and put into the outputs of the rows that see them where a product of marks
-      // (E4M3 1.0 at scale 1) and visibility finds any.
-      if (__builtin_expect(__ballot(nan != 0) != 0, 0)) {
-        uint32_t clean[8][L::kWords], clean_sc[8][L::kScales];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-#pragma unroll
-          for (int w = 0; w < L::kWords; ++w) {
-            const bool all = (vsc[j][L::kScales > 1 && w >= L::kWordsA ? 1 : 0] & 0x7F800000u) == 0x7F800000u;
-            const uint32_t mark = all ? 0x01010101u : any_nan_code(raw.v[j][w]) >> 7;    // 1 in every NaN byte
-            clean[j][w] = raw.v[j][w] & ~(mark * 255u);
-            raw.v[j][w] = mark * 0x38u;
-          }
-#pragma unroll
-          for (int w = 0; w < L::kScales; ++w) {
-            clean_sc[j][w] = (vsc[j][w] & 0x7F800000u) == 0x7F800000u ? 127u << 23 : vsc[j][w];
-            vsc[j][w] = 127u << 23;
-          }
-        }
+      // values that are infinite or NaN go to the rows that see them; what is left of the step has none
+      if (__builtin_expect(__ballot(nans != 0 || widest >= kWideScale<DT> << 23) != 0, 0)) {
+        // all bits of the bytes of a word that are infinite or NaN; of those that are NaN
+        auto bytes = [](uint32_t top) { return (top << 1) - (top >> 7); };      // top bits to whole bytes
+        auto odd = [&](int j, int w, int run) {
+          asm volatile("" : "+v"(raw.v[j][w]), "+v"(vsc[j][run]));     // computed anew at every use: kept, it would take registers
+          return ((raw.v[j][w] & 0x7F7F7F7Fu) + (0x80u - least_odd_code<DT>((vsc[j][run] >> 23) & 255u)) * 0x01010101u) & 0x80808080u;
+        };
+        auto nan = [&](int j, int w, int run) {
+          return any_nan_code(raw.v[j][w]) | ((((vsc[j][run] >> 23) & 255u) + 1) >> 8) * 0x80808080u;
+        };
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-          float e[8];
-          const uint32_t mine = uint32_t(first[n] - key0 - 8 * quarter);
-          const uint32_t seen = uint32_t(max(min(last[n], hi - 1) - first[n] + 1, 0));
+          const uint32_t from = uint32_t(first[n] - key0 - 8 * quarter);
+          const uint32_t many = uint32_t(max(min(last[n], hi - 1) - first[n] + 1, 0));
+          u32x4_t see;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) e[j] = uint32_t(j) - mine < seen ? 1.0f : 0.0f;
-          const u32x4_t see = {pack2<DT>(e[0], e[1]), pack2<DT>(e[2], e[3]), pack2<DT>(e[4], e[5]), pack2<DT>(e[6], e[7])};
-          for_tiles([&](int t, u32x4_t a) {
-            const v4f hits = mfma16<DT>(a, see, v4f{0, 0, 0, 0});
+          for (int j = 0; j < 4; ++j)
+            see[j] = (uint32_t(2 * j) - from < many ? kOneBits<DT> : 0u) | (uint32_t(2 * j + 1) - from < many ? kOneBits<DT> << 16 : 0u);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {        // a count: all bits of `any` set where it is not zero
-              const int any = -__float_as_int(hits[v]) >> 31;
-              o[n][t][v] = __uint_as_float(__float_as_uint(o[n][t][v]) | (uint32_t(any) & 0x7FC00000u));
-            }
-            __builtin_amdgcn_sched_barrier(0);   // one tile at a time: this path shall cost no registers
-          });
+          for (int minus = 0; minus < 2; ++minus) {
+            const uint32_t sign = minus ? 0u : 0x80808080u;
+            const float big = minus ? -0x1p127f : 0x1p127f;
+            for_tiles([&](int j, int w, int run) {       // marks are E4M3 ones at scale 1
+                        return bytes(odd(j, w, run) & ((raw.v[j][w] ^ sign) | nan(j, w, run))) & 0x38383838u;
+                      }, [&](int, int) { return 127u << 23; }, [&](int t, u32x4_t a) {
+                        const v4f hits = mfma16<DT>(a, see, v4f{0, 0, 0, 0});
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) o[n][t][v] += hits[v] * big * 0x1p127f;
+                        __builtin_amdgcn_sched_barrier(0);   // one tile at a time: this path shall cost no registers
+                      });
+          }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
 #pragma unroll
-          for (int w = 0; w < L::kWords; ++w) raw.v[j][w] = clean[j][w];
+          for (int w = 0; w < L::kWords; ++w) raw.v[j][w] &= ~bytes(odd(j, w, L::kScales > 1 && w >= L::kWordsA ? 1 : 0));
 #pragma unroll
-          for (int w = 0; w < L::kScales; ++w) vsc[j][w] = clean_sc[j][w];
+          for (int w = 0; w < L::kScales; ++w) vsc[j][w] = (vsc[j][w] & 0x7F800000u) == 0x7F800000u ? 127u << 23 : vsc[j][w];
         }
       }
     }
@@ -566,7 +618,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, 
         x = fmaxf(x, __shfl_xor(x, 16, 64));
         x = fmaxf(x, __shfl_xor(x, 32, 64));
         const float next = fmaxf(mref[n], x - kLift<DT>);
-        const float a = mref[n] == next ? 1.0f : __builtin_amdgcn_exp2f(mref[n] - next);
+        // before the first score there is nothing to rescale but infinities, which 0 would make NaN
+        const float a = mref[n] == next || mref[n] == kLowest ? 1.0f : __builtin_amdgcn_exp2f(mref[n] - next);
         mref[n] = next;
         l[n] *= a;
 #pragma unroll
@@ -575,7 +628,11 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, 
     }
     // ---- weights, in two terms of the type of q: one alone is off by up to 2^-9 (BF16), which outputs of
     // the same type would show (error against 64 bits 0.0023, with both 0.0017, the outputs' own rounding).
-    // The second product costs 1% where memory bounds (64 requests of 8192 keys: 135.0 us without, 136.3 with).
+    // The second product costs 1% where memory bounds (64 requests of 8192 keys: 135.0 us without, 136.5 with).
+    // The first term is chopped and the second kept above 0 (2^-126 for BF16; 2^-24 for F16, where the first is
+    // not 0), so that an infinite value that every row sees makes infinities and no NaN: 0 times infinity.  A step
+    // that some row does not see whole has none left, and weights of 0 have to stay 0 there.
+    const uint32_t least = edge ? 0u : DT == IN_BF16 ? 0x00800080u : 0x00010001u;
     u32x4_t p[NQ], rest[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -583,13 +640,15 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, 
 #pragma unroll
       for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][j >> 2][j & 3], g.c, -mref[n]));
       l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-      p[n] = u32x4_t{pack2<DT>(e[0], e[1]), pack2<DT>(e[2], e[3]), pack2<DT>(e[4], e[5]), pack2<DT>(e[6], e[7])};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        rest[n][j] = pack2<DT>(e[2 * j] - unpack<DT, false>(p[n][j]), e[2 * j + 1] - unpack<DT, true>(p[n][j]));
+      for (int j = 0; j < 4; ++j) {
+        p[n][j] = chop2<DT>(e[2 * j], e[2 * j + 1]);
+        const uint32_t lost = pack2<DT>(e[2 * j] - unpack<DT, false>(p[n][j]), e[2 * j + 1] - unpack<DT, true>(p[n][j]));
+        rest[n][j] = max2(lost, DT == IN_F16 ? min2(p[n][j], least) : least);
+      }
     }
     // ---- O^T
-    for_tiles([&](int t, u32x4_t a) {
+    for_tiles([&](int j, int w, int) { return raw.v[j][w]; }, [&](int j, int run) { return vsc[j][run]; }, [&](int t, u32x4_t a) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) o[n][t] = mfma16<DT>(a, rest[n], mfma16<DT>(a, p[n], o[n][t]));
     });
@@ -717,7 +776,7 @@ template <int D, int NW> struct TileLds {
   union {
     struct {
       alignas(16) uint8_t k[2][D / 8 * kFrag], v[2][D / 8 * kFrag];
-      int nan_tile[2][4];
+      int odd_tile[2][4];
     };
     float out[NW][32][D + 4];
   };
@@ -733,7 +792,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
   constexpr int kRows = 32 * NW;
   constexpr int kAheadK = 4;                     // fragments of keys read ahead
   constexpr int kKLoads = (D + 63) / 64;         // 16-byte loads of a lane for 16 keys
-  auto& nan_tile = lds.nan_tile;
+  auto& odd_tile = lds.odd_tile;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = wave & 3;                     // row group of a tile that this wave decodes
   const bool decodes_k = NW == 4 || wave < 4, decodes_v = NW == 4 || wave >= 4;
@@ -883,9 +942,9 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
       }
     }
     if (!decodes_v) return;
-    // values that no row sees may be anything; the weight 0 must not meet a NaN there
+    // values that no row sees may be anything; the weight 0 must not meet an infinity or a NaN there
     const int key0 = tile0 + 16 * part;
-    uint32_t nan = 0;
+    uint32_t odd = 0;
     if (tile0 < all_from || tile0 + 64 > all_to) {
       const uint32_t from = uint32_t(lo - key0 - 8 * h), many = uint32_t(max(hi - lo, 0));
 #pragma unroll
@@ -894,17 +953,17 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
 #pragma unroll
         for (int w = 0; w < kWordsV + kRuns - 1; ++w) {
           rv(j, w) = keep ? rv(j, w) : 0u;
-          nan |= any_nan_code(rv(j, w));
+          odd |= any_nan_code(rv(j, w));
         }
 #pragma unroll
         for (int w = 0; w < kRuns; ++w) {
           rvs(j, w) = keep ? rvs(j, w) : 127u;
-          nan |= rvs(j, w) == 255u ? 1u : 0u;
+          odd |= rvs(j, w) >= kWideScale<DT> ? 1u : 0u;
         }
       }
     }
-    const bool any = __ballot(nan != 0) != 0;
-    if (lane == 0) nan_tile[buf][part] = any;
+    const bool any = __ballot(odd != 0) != 0;
+    if (lane == 0) odd_tile[buf][part] = any;
     uint8_t* vb = lds.v[buf] + part * kFrag + lane * 16;        // fragment (tile, step) at 4 tile + step
     auto pair = [&](int w, int run, auto hi_half, int tile, bool both) {
       constexpr bool HI = decltype(hi_half)::value;
@@ -927,45 +986,41 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
     if constexpr (L::kB) pair(kWordsV, 1, std::false_type{}, L::kA, L::kB == 2);
   };
 
-  // A tile with NaN values that some rows of the workgroup see and others do not: 0 * NaN would reach
-  // those.  The NaNs are put into the outputs of the rows that see them, where a product of marks and
-  // visibility finds any, and then taken out of the tile.
-  auto take_nans = [&](int tile0, int buf) {
-    constexpr uint32_t kInfBits = DT == IN_BF16 ? 0x7F80u : 0x7C00u, kOne = DT == IN_BF16 ? 0x3F80u : 0x3C00u;
-    auto nans = [](u32x4_t x) {                  // all bits of the NaN halves
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[j] = ((x[j] & 0x7FFFu) > kInfBits ? 0xFFFFu : 0u) | (((x[j] >> 16) & 0x7FFFu) > kInfBits ? 0xFFFF0000u : 0u);
-      return x;
-    };
+  // A tile with infinite or NaN values that some rows of the workgroup see and others do not: the outputs of
+  // those that do get them, and the tile is left without them.
+  auto take_odd = [&](int tile0, int buf) {
     const uint32_t from = uint32_t(first - tile0 - 8 * h), many = uint32_t(max(min(last, hi - 1) - first + 1, 0));
 #pragma nounroll
     for (int u = 0; u < 4; ++u) {
       u32x4_t see;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        see[j] = (uint32_t(16 * u + 2 * j) - from < many ? kOne : 0u) |
-                 (uint32_t(16 * u + 2 * j + 1) - from < many ? kOne << 16 : 0u);
+        see[j] = (uint32_t(16 * u + 2 * j) - from < many ? kOneBits<DT> : 0u) |
+                 (uint32_t(16 * u + 2 * j + 1) - from < many ? kOneBits<DT> << 16 : 0u);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        u32x4_t mark = nans(*reinterpret_cast<const u32x4_t*>(lds.v[buf] + (4 * t + u) * kFrag + lane * 16));
-        mark &= kOne | kOne << 16;
-        v16f_t hits;
+        u32x4_t x = *reinterpret_cast<const u32x4_t*>(lds.v[buf] + (4 * t + u) * kFrag + lane * 16);
+        u32x4_t plus, minus;
+        take_marks<DT>(x, plus, minus);
+        v16f_t zero;
 #pragma unroll
-        for (int v = 0; v < 16; ++v) hits[v] = 0.0f;
-        hits = mfma32<DT>(mark, see, hits);
+        for (int v = 0; v < 16; ++v) zero[v] = 0.0f;
+        const v16f_t up = mfma32<DT>(plus, see, zero);
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int any = -__float_as_int(hits[v]) >> 31;
-          o[t][v] = __uint_as_float(__float_as_uint(o[t][v]) | (uint32_t(any) & 0x7FC00000u));
-        }
-        __builtin_amdgcn_sched_barrier(0);       // one fragment at a time: this path shall cost no registers
+        for (int v = 0; v < 16; ++v) o[t][v] += infinity_of(up[v]);
+        __builtin_amdgcn_sched_barrier(0);       // one product at a time: this path shall cost no registers
+        const v16f_t down = mfma32<DT>(minus, see, zero);
+#pragma unroll
+        for (int v = 0; v < 16; ++v) o[t][v] -= infinity_of(down[v]);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     __syncthreads();
     for (int f = wave; f < 4 * kTiles; f += NW) {
       u32x4_t* at = reinterpret_cast<u32x4_t*>(lds.v[buf] + f * kFrag + lane * 16);
-      *at &= ~nans(*at);
+      u32x4_t x = *at, plus, minus;
+      take_marks<DT>(x, plus, minus);
+      *at = x;
     }
     __syncthreads();
   };
@@ -1011,7 +1066,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
     top *= g.c;
     if (__ballot(top > mref + (kLift<DT> + kSlack))) {
       const float next = fmaxf(mref, fmaxf(top, __shfl_xor(top, 32, 64)) - kLift<DT>);
-      const float a = mref == next ? 1.0f : __builtin_amdgcn_exp2f(mref - next);
+      const float a = mref == next || mref == kLowest ? 1.0f : __builtin_amdgcn_exp2f(mref - next);
       mref = next;
       l *= a;
 #pragma unroll
@@ -1046,7 +1101,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
     __syncthreads();
     int buf = 0;
     for (int tile0 = start; tile0 < hi; tile0 += 64) {
-      if (nan_tile[buf][0] | nan_tile[buf][1] | nan_tile[buf][2] | nan_tile[buf][3]) take_nans(tile0, buf);
+      if (odd_tile[buf][0] | odd_tile[buf][1] | odd_tile[buf][2] | odd_tile[buf][3]) take_odd(tile0, buf);
       if (tile0 + 64 < hi) {
         decode(tile0 + 64, buf ^ 1);
         if (tile0 + 128 < hi) load(tile0 + 128);
