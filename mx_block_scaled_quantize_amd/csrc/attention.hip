@@ -1072,7 +1072,12 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& g, int req, int rt, in
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) o[t] *= a;
     }
-    // ---- weights.  Of the two waves of a SIMD, the one that has come this far goes first until its values
+    // ---- weights, rounded to the type of q: off by up to 2^-9 (BF16), so that the error against 64 bits is
+    // 0.0023 where the outputs' own rounding is 0.0017.  Both ways to 0.0017 cost the matrix unit's time here
+    // (2048 tokens over 32768 keys, 974 us): a second term as for few rows 1377 us, F16 weights and values where
+    // the scales allow 1026 us.  The sum of the weights is that of the unrounded ones, which the log-sum-exp
+    // needs; roundings to even leave it unbiased.
+    // Of the two waves of a SIMD, the one that has come this far goes first until its values
     // are added: it mixes matrix and vector instructions, the other has only matrix ones (2048 tokens over
     // 32768: 983 us without, 975 with; workgroups of four waves lose 1% by it)
     if constexpr (NW == 8) __builtin_amdgcn_s_setprio(1);
