@@ -5,8 +5,8 @@ Argument marshalling only (of the rotary and cache operators by ``_bind.so``, fr
 ``csrc/bind.cpp``, which costs a call less time than ctypes).  Every step of the computation runs in the HIP
 kernels of ``libmx.so`` (built from ``csrc/`` by ``_build.py``); PyTorch only
 provides device memory and the current HIP stream.  There is no CPU fallback:
-importing this module without the built libraries, or passing host tensors,
-raises.
+importing this module without the built library, calling those operators without
+the binding, or passing host tensors, raises.
 
 The functions carry the names of the C entry points declared in
 ``include/mx.h`` and return freshly allocated output tensors:
@@ -47,11 +47,26 @@ if not os.path.exists(LIB_PATH):
 # torch is imported first so that its HIP runtime is the one libmx binds to
 lib = ctypes.CDLL(LIB_PATH)
 
+
+class _NoBinding:
+    """Stands for a binding that is missing or does not load (it is bound to one Python and one torch, which the
+    ctypes calls of the quantizers and GEMMs are not): whatever is called of it raises."""
+
+    def __init__(self, reason):
+        self._reason = reason
+
+    def set_check(self, check):
+        pass
+
+    def __getattr__(self, name):
+        raise ImportError(f"the binding {os.path.join(_HERE, '_bind.so')} is missing or does not load: build it first "
+                          "(python -c 'import __graft_entry__ as g; g.build()')") from self._reason
+
+
 try:
     from . import _bind
 except ImportError as e:
-    raise ImportError(f"the binding {os.path.join(_HERE, '_bind.so')} is missing or does not load: build it first "
-                      "(python -c 'import __graft_entry__ as g; g.build()')") from e
+    _bind = _NoBinding(e)
 
 # ---------------------------------------------------------------- enums (include/mx.h)
 FMT = {"e4m3": 0, "e5m2": 1, "e2m1": 2, "e2m3": 3, "e3m2": 4}

@@ -72,14 +72,15 @@ def build(verbose=False):
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         bind = ex.submit(_compile_bind)
         objs = list(ex.map(_compile, srcs))
-        bind_obj, torch_lib = bind.result()
     tmp = LIB + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    # torch's libraries are loaded before the binding is; libmx lies beside it
+    # libmx is there even if the binding cannot be built.  torch's libraries are loaded before the binding is; libmx
+    # lies beside it
+    bind_obj, torch_lib = bind.result()
     tmp = BIND + ".tmp"
     _run(["g++", "-shared", "-o", tmp, bind_obj, f"-L{PKG}", "-lmx", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu",
           "-lc10", "-lc10_hip", "-lamdhip64", "-Wl,-rpath,$ORIGIN"], "link of _bind.so")
