@@ -444,20 +444,47 @@ def mx_rope_table(rows, rot, base=1e4, scaling="none", factor=1.0, orig_len=0, d
     return out
 
 
+class _Rope(torch.autograd.Function):
+    """The rotation is linear in x and orthogonal: its backward pass is the rotation the other way."""
+
+    @staticmethod
+    def forward(ctx, x, pos, table, layout, inverse):
+        ctx.save_for_backward(pos, table)
+        ctx.layout, ctx.inverse = layout, inverse
+        return _bind.rope(x, pos, table, layout, inverse, None)
+
+    @staticmethod
+    def backward(ctx, grad):
+        pos, table = ctx.saved_tensors
+        if grad.stride(2) != 1:       # of a sum, say: expanded from one number
+            grad = grad.contiguous()
+        return _rope(grad, pos, table, ctx.layout, not ctx.inverse), None, None, None, None
+
+
+def _rope(x, pos, table, layout, inverse, out=None):
+    if isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out cannot be given for an x that needs a gradient")
+        return _Rope.apply(x, pos, table, layout, inverse)
+    return _bind.rope(x, pos, table, layout, inverse, out)
+
+
 def mx_rope(x, pos, table, layout="half", inverse=False, out=None):
     """x [tokens][heads][dim] (float32, bfloat16 or float16, any strides but the channels') with
     its first rot channels turned by the table rows of pos (int32 [tokens]).
 
     layout "half" pairs channel i with i + rot / 2, "interleaved" 2i with 2i + 1.  inverse=True
     turns back, which is also the backward pass: grad_x = mx_rope(grad_y, pos, table, layout,
-    inverse=True).  out may be x itself (in place)."""
-    return _bind.rope(x, pos, table, _lookup(ROPE_LAYOUT, layout, "rotary layout"), inverse, out)
+    inverse=True).  Autograd takes that way by itself for an x that needs a gradient (the table
+    gets none).  out may be x itself (in place); an x that needs a gradient takes no out."""
+    return _rope(x, pos, table, _lookup(ROPE_LAYOUT, layout, "rotary layout"), inverse, out)
 
 
 def mx_kv_append(k, v, cache, slots, pos=None, table=None, layout="half", q=None, q_out=None):
     """Stores tokens in the cache: k rotated (if table is given) and MXFP8-encoded, v encoded, at
     slots (int64 [tokens]; slot s is token s % page of page s // page, a slot outside the cache is
-    skipped).  With q (table needed) returns q rotated, [tokens][heads][dim], from the same launch."""
+    skipped).  With q (table needed) returns q rotated, [tokens][heads][dim], from the same launch.
+    For serving: no gradient flows through it."""
     return _bind.kv_append(k, v, *cache, slots, pos, table, _lookup(ROPE_LAYOUT, layout, "rotary layout"), q, q_out)
 
 
@@ -474,7 +501,7 @@ def mx_paged_attention(q, cache, page_table, cu, lens, window=0, scale=None, lse
     max_q, max_kv  upper bounds of the query and cached tokens of a request.  Left out, they are
                 read from cu and lens, which waits for the GPU: give them in serving loops.
     Returns out [tokens][heads][dim], or (out, lse [tokens][heads] float32).  Queries that see
-    nothing give 0 and -inf."""
+    nothing give 0 and -inf.  For serving: no gradient flows through it."""
     if max_q is None:
         max_q = int((cu[1:] - cu[:-1]).max()) if lens.numel() else 0
     if max_kv is None:
