@@ -39,6 +39,12 @@ double real(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v != 0;
+}
+
 mx_dtype_t dtype_of(const at::Tensor& t) {
   switch (t.scalar_type()) {
     case at::kFloat: return MX_F32;
@@ -150,6 +156,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check_heads(x, "x", dev);
   check_table(table, dev);
   check_vector(pos, "pos", at::kInt, x.size(0), dev);
+  const bool inverse = truth(a[4]);
   OnDevice on(dev);
   at::Tensor out;
   if (a[5] == Py_None) {
@@ -163,7 +170,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check_status(mx_rope(x.data_ptr(), dt, x.size(0), narrow_int(x.size(1), "heads"), narrow_int(x.size(2), "dim"), x.stride(0),
                        x.stride(1), static_cast<const int32_t*>(pos.data_ptr()), static_cast<const float*>(table.data_ptr()),
                        table.size(0), narrow_int(2 * table.size(1), "rot"), mx_rope_layout_t(integer(a[3])),
-                       PyObject_IsTrue(a[4]), out.data_ptr(), out.stride(0), out.stride(1), on.stream));
+                       inverse, out.data_ptr(), out.stride(0), out.stride(1), on.stream));
   return THPVariable_Wrap(std::move(out));
   END_HANDLE_TH_ERRORS
 }
@@ -249,7 +256,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     "page_table must be an int32 tensor [requests][pages] with contiguous rows");
   const int64_t window = integer(a[8]), max_q = integer(a[11]), max_kv = integer(a[12]);
   const double scale = a[9] == Py_None ? 1.0 / std::sqrt(double(cache.dim)) : real(a[9]);
-  const int want_lse = PyObject_IsTrue(a[10]);
+  const bool want_lse = truth(a[10]);
   OnDevice on(dev);
   at::Tensor out, lse, space;
   if (a[13] == Py_None) {

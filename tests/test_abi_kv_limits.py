@@ -15,3 +15,15 @@ def test_attention_needs_the_columns_that_it_is_told_of():
     assert attention(table=None, max_kv=0) == NULL
     assert attention(table=None, max_kv=0, cols=0) == LAUNCH      # accepted: no device here to launch on
     assert attention(table=None, cols=0) == LAUNCH
+
+
+def test_flags_without_a_truth_value():
+    """Whose __bool__ raises: that error, not a result with an error set."""
+    x, pos, t = torch.zeros(4, 2, 64), torch.zeros(4, dtype=torch.int32), torch.zeros(8, 32, 2)
+    c = mxa.KVCache(*(torch.zeros((2, 2, 16, n), dtype=torch.uint8) for n in (64, 2, 64, 2)))
+    both = torch.zeros(2, dtype=torch.bool)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        mxa.mx_rope(x, pos, t, inverse=both)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        mxa.mx_paged_attention(x.bfloat16(), c, pos.view(2, 2), torch.zeros(3, dtype=torch.int32), pos[:2], lse=both, max_q=1,
+                               max_kv=1)
