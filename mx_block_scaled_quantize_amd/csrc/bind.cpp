@@ -60,6 +60,9 @@ void check_heads(const at::Tensor& t, const char* name, const at::Device& dev) {
   TORCH_CHECK_VALUE(t.device() == dev, name, " must be on the device of the other arguments");
 }
 
+// Stride of a dimension; 0 where it has one element, whose stride means nothing but would decide on alignment.
+int64_t stride_of(const at::Tensor& t, int dim) { return t.size(dim) > 1 ? t.stride(dim) : 0; }
+
 void check_vector(const at::Tensor& t, const char* name, at::ScalarType dt, int64_t n, const at::Device& dev) {
   TORCH_CHECK_VALUE(t.scalar_type() == dt && t.dim() == 1 && t.size(0) == n && t.is_contiguous() && t.device() == dev, name,
                     " must be a contiguous ", dt, " vector of length ", n, " on the device of the other arguments");
@@ -167,10 +170,11 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(out.sizes() == x.sizes() && out.scalar_type() == x.scalar_type(),
                       "out must have the shape and dtype of x");
   }
-  check_status(mx_rope(x.data_ptr(), dt, x.size(0), narrow_int(x.size(1), "heads"), narrow_int(x.size(2), "dim"), x.stride(0),
-                       x.stride(1), static_cast<const int32_t*>(pos.data_ptr()), static_cast<const float*>(table.data_ptr()),
-                       table.size(0), narrow_int(2 * table.size(1), "rot"), mx_rope_layout_t(integer(a[3])),
-                       inverse, out.data_ptr(), out.stride(0), out.stride(1), on.stream));
+  check_status(mx_rope(x.data_ptr(), dt, x.size(0), narrow_int(x.size(1), "heads"), narrow_int(x.size(2), "dim"),
+                       stride_of(x, 0), stride_of(x, 1), static_cast<const int32_t*>(pos.data_ptr()),
+                       static_cast<const float*>(table.data_ptr()), table.size(0), narrow_int(2 * table.size(1), "rot"),
+                       mx_rope_layout_t(integer(a[3])), inverse, out.data_ptr(), stride_of(out, 0), stride_of(out, 1),
+                       on.stream));
   return THPVariable_Wrap(std::move(out));
   END_HANDLE_TH_ERRORS
 }
@@ -223,13 +227,13 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     q = t.data_ptr();
     heads = t.size(1);
-    qt = t.stride(0);
-    qh = t.stride(1);
+    qt = stride_of(t, 0);
+    qh = stride_of(t, 1);
     if (heads == 0) q = nullptr;
   }
-  check_status(mx_kv_append(k.data_ptr(), v.data_ptr(), dt, tokens, k.stride(0), k.stride(1), v.stride(0), v.stride(1), &cache,
-                            static_cast<const int64_t*>(slots.data_ptr()), pos, table, rows, narrow_int(rot, "rot"),
-                            mx_rope_layout_t(integer(a[9])), q, narrow_int(heads, "heads"), qt, qh,
+  check_status(mx_kv_append(k.data_ptr(), v.data_ptr(), dt, tokens, stride_of(k, 0), stride_of(k, 1), stride_of(v, 0),
+                            stride_of(v, 1), &cache, static_cast<const int64_t*>(slots.data_ptr()), pos, table, rows,
+                            narrow_int(rot, "rot"), mx_rope_layout_t(integer(a[9])), q, narrow_int(heads, "heads"), qt, qh,
                             out.defined() ? out.data_ptr() : nullptr, on.stream));
   if (!out.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(std::move(out));
@@ -271,10 +275,11 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                             max_kv, window, &need));
   if (need) space = at::empty({need}, q.options().dtype(at::kByte));
   check_status(mx_paged_attention(
-      q.data_ptr(), dt, tokens, int(heads), q.stride(0), q.stride(1), &cache, static_cast<const int32_t*>(pages.data_ptr()),
-      pages.stride(0), pages.size(1), static_cast<const int32_t*>(cu.data_ptr()),
-      static_cast<const int32_t*>(lens.data_ptr()), requests, max_q, max_kv, window, float(scale), out.data_ptr(),
-      want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, need ? space.data_ptr() : nullptr, need, on.stream));
+      q.data_ptr(), dt, tokens, int(heads), stride_of(q, 0), stride_of(q, 1), &cache,
+      static_cast<const int32_t*>(pages.data_ptr()), pages.stride(0), pages.size(1),
+      static_cast<const int32_t*>(cu.data_ptr()), static_cast<const int32_t*>(lens.data_ptr()), requests, max_q, max_kv,
+      window, float(scale), out.data_ptr(), want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
+      need ? space.data_ptr() : nullptr, need, on.stream));
   if (!want_lse) return THPVariable_Wrap(std::move(out));
   THPObjectPtr o(THPVariable_Wrap(std::move(out))), s(THPVariable_Wrap(std::move(lse)));
   if (!o || !s) throw python_error();

@@ -20,3 +20,17 @@ def test_tables_without_columns(m):
     sees[-1] = True
     assert out[sees].isnan().all() and lse[sees].isnan().all()
     assert (out[~sees] == 0).all() and (lse[~sees] == -float("inf")).all()
+
+
+@pytest.mark.parametrize("heads", [8, 1])
+def test_strides_of_single_tokens_and_heads(heads):
+    """The stride of a dimension of one element means nothing, though it is no multiple of 16 bytes."""
+    p = Problem([(1, 50)] if heads > 1 else [(3, 50)], heads, 1, 64)
+    q = p.q.contiguous()
+    odd = q.as_strided(q.shape, (3, 64, 1) if heads > 1 else (64, 3, 1))
+    args = p.gpu_args()
+    want = mxa.mx_paged_attention(q, *args, max_q=3, max_kv=50)
+    assert torch.equal(mxa.mx_paged_attention(odd, *args, max_q=3, max_kv=50), want)
+    table, pos = mxa.mx_rope_table(64, 64), args[3][:1] if heads > 1 else torch.arange(3, dtype=torch.int32, device=dev())
+    assert torch.equal(mxa.mx_rope(odd, pos, table), mxa.mx_rope(q, pos, table))
+    assert odd.data_ptr() == q.data_ptr()
