@@ -416,8 +416,7 @@ mx_status_t mx_rope(const void* x, mx_dtype_t dtype, int64_t tokens, int heads, 
  *   pos      int32 [tokens], table [rows][rot / 2][2] as for mx_rope; table NULL: no
  *            rotation (q must be NULL, pos is ignored).
  *   q_out    [tokens][heads][dim] contiguous.
- * Errors: as mx_rope; MX_ERR_SHAPE for a cache shape that is not offered, or tokens x heads x
- * dim beyond 2^33. */
+ * Errors: as mx_rope; MX_ERR_SHAPE for a cache shape that is not offered. */
 mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dtype, int64_t tokens, int64_t k_token_stride,
                          int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                          const mx_kv_cache_t* cache, const int64_t* slots, const int32_t* pos, const float* table,

@@ -560,50 +560,59 @@ extern "C" mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dty
       misaligned(cache->k_scales) || misaligned(cache->v_scales))
     return MX_ERR_ALIGN;
   if (q && (reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out)) % size) return MX_ERR_ALIGN;
-  AppendArgs g = {};
-  int64_t q_blocks = 0;
   const int kv_heads = cache->kv_heads;
   int vq = 16 / size, hpt = heads_per_thread(tokens, kv_heads, dim / 8);
+  int64_t q_threads = 0;                                // of a token
   if (q) {
     vq = rope_vector(dtype, dim, rot, q, q_out, q_token_stride, q_head_stride, int64_t(heads) * dim, dim);
-    hpt = std::max(hpt, heads_per_thread(tokens, heads, (rot / 2 + dim - rot) / vq));
-    fill_rope(g.q, q, q_out, tokens, heads, dim, q_token_stride, q_head_stride, int64_t(heads) * dim, dim, pos, table,
-              rows, rot, false, vq, hpt);
-    q_blocks = (tokens * g.q.head_groups.d * g.q.chunks.d + 255) / 256;
-  } else {
-    g.q.table = reinterpret_cast<const float2*>(table);
-    g.q.pos = pos;
-    g.q.rows = rows;
-    g.q.rot = rot;
+    const int chunks = (rot / 2 + dim - rot) / vq;
+    hpt = std::max(hpt, heads_per_thread(tokens, heads, chunks));
+    q_threads = int64_t((heads + hpt - 1) / hpt) * chunks;
   }
-  g.k = k; g.v = v; g.kt = k_token_stride; g.kh = k_head_stride; g.vt = v_token_stride; g.vh = v_head_stride;
-  g.slots = slots;
-  g.kc = cache->k; g.ks = cache->k_scales; g.vc = cache->v; g.vs = cache->v_scales;
-  g.tokens = tokens;
-  g.slot_count = cache->pages * cache->page;
-  g.kv_heads = cache->kv_heads; g.page = cache->page; g.dim = dim;
-  g.inv_page = 1.0 / cache->page;
-  g.per_head = Divisor(uint32_t(dim / 8));              // a multiple of 4, so a quad stays in one block of 32
-  g.head_groups = Divisor(uint32_t((kv_heads + hpt - 1) / hpt));
-  const int64_t kv_blocks = (tokens * g.head_groups.d * (dim / 8) + 255) / 256;
-  // thread numbers are kept below 2^31
-  if (q_blocks > 0x7FFFFF || kv_blocks > 0x7FFFFF) return MX_ERR_SHAPE;
-  g.q_blocks = uint32_t(q_blocks);
-  g.kv_blocks = uint32_t(kv_blocks);
-  const int64_t blocks = q_blocks + 2 * kv_blocks;
+  const int64_t kv_threads = int64_t((kv_heads + hpt - 1) / hpt) * (dim / 8);
   // 16-byte loads of keys and values: aligned rows, and no 8-channel chunk across the rotation's borders
   const int64_t strides = k_token_stride | k_head_stride | v_token_stride | v_head_stride;
   const bool vec = (kv & 15u) == 0 && strides % (16 / size) == 0 && (!table || (rot / 2) % 8 == 0);
-  with_type(dtype, [&](auto in) {
-    constexpr int IN = decltype(in)::value;
-    with_variant<IN>(vq, hpt, [&](auto vv, auto hh) {
-      constexpr int V = decltype(vv)::value, H = decltype(hh)::value;
-      const bool half = layout == MX_ROPE_HALF;
-      if (vec && half) append_kernel<IN, V, true, H, true><<<unsigned(blocks), 256, 0, stream>>>(g);
-      else if (vec) append_kernel<IN, V, false, H, true><<<unsigned(blocks), 256, 0, stream>>>(g);
-      else if (half) append_kernel<IN, V, true, H, false><<<unsigned(blocks), 256, 0, stream>>>(g);
-      else append_kernel<IN, V, false, H, false><<<unsigned(blocks), 256, 0, stream>>>(g);
+  // thread numbers, and those of all three tensors together, are kept below 2^31: longer inputs go in several
+  // launches (a token of 65536 heads of 256 channels has 2^23 threads)
+  const int64_t slab = int64_t(0x7FFFFC00) / (q_threads + 2 * kv_threads);
+  for (int64_t t = 0; t < tokens; t += slab) {
+    const int64_t n = std::min(slab, tokens - t);
+    AppendArgs g = {};
+    if (q) {
+      fill_rope(g.q, static_cast<const uint8_t*>(q) + t * q_token_stride * size, static_cast<uint8_t*>(q_out) + t * heads * dim * size,
+                n, heads, dim, q_token_stride, q_head_stride, int64_t(heads) * dim, dim, pos + t, table, rows, rot, false, vq, hpt);
+    } else {
+      g.q.table = reinterpret_cast<const float2*>(table);
+      g.q.pos = table ? pos + t : nullptr;
+      g.q.rows = rows;
+      g.q.rot = rot;
+    }
+    g.k = static_cast<const uint8_t*>(k) + t * k_token_stride * size;
+    g.v = static_cast<const uint8_t*>(v) + t * v_token_stride * size;
+    g.kt = k_token_stride; g.kh = k_head_stride; g.vt = v_token_stride; g.vh = v_head_stride;
+    g.slots = slots + t;
+    g.kc = cache->k; g.ks = cache->k_scales; g.vc = cache->v; g.vs = cache->v_scales;
+    g.tokens = n;
+    g.slot_count = cache->pages * cache->page;
+    g.kv_heads = kv_heads; g.page = cache->page; g.dim = dim;
+    g.inv_page = 1.0 / cache->page;
+    g.per_head = Divisor(uint32_t(dim / 8));            // a multiple of 4, so a quad stays in one block of 32
+    g.head_groups = Divisor(uint32_t((kv_heads + hpt - 1) / hpt));
+    g.q_blocks = uint32_t((n * q_threads + 255) / 256);
+    g.kv_blocks = uint32_t((n * kv_threads + 255) / 256);
+    const unsigned blocks = g.q_blocks + 2 * g.kv_blocks;
+    with_type(dtype, [&](auto in) {
+      constexpr int IN = decltype(in)::value;
+      with_variant<IN>(vq, hpt, [&](auto vv, auto hh) {
+        constexpr int V = decltype(vv)::value, H = decltype(hh)::value;
+        const bool half = layout == MX_ROPE_HALF;
+        if (vec && half) append_kernel<IN, V, true, H, true><<<blocks, 256, 0, stream>>>(g);
+        else if (vec) append_kernel<IN, V, false, H, true><<<blocks, 256, 0, stream>>>(g);
+        else if (half) append_kernel<IN, V, true, H, false><<<blocks, 256, 0, stream>>>(g);
+        else append_kernel<IN, V, false, H, false><<<blocks, 256, 0, stream>>>(g);
+      });
     });
-  });
+  }
   return launched();
 }

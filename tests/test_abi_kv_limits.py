@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from tests.test_abi_kv import LAUNCH, NULL, attention, mxa  # noqa: F401
+from tests.test_abi_kv import FAKE, LAUNCH, NULL, append, attention, cache, mxa  # noqa: F401
 
 if torch.cuda.is_available():
     pytest.skip("argument-validation tests use fake device addresses; CPU only", allow_module_level=True)
@@ -27,3 +27,10 @@ def test_flags_without_a_truth_value():
     with pytest.raises(RuntimeError, match="ambiguous"):
         mxa.mx_paged_attention(x.bfloat16(), c, pos.view(2, 2), torch.zeros(3, dtype=torch.int32), pos[:2], lse=both, max_q=1,
                                max_kv=1)
+
+
+@pytest.mark.parametrize("kw", [dict(tokens=1 << 26, heads=1, q=FAKE + 2), dict(tokens=1 << 31),
+                                dict(tokens=1 << 26, cache=cache(kv_heads=64))])
+def test_appends_of_any_length(kw):
+    """Lengths beyond one launch's thread numbers are cut into several; there is no device here to launch on."""
+    assert append(**kw) == LAUNCH
