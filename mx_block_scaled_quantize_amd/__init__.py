@@ -501,7 +501,8 @@ def mx_paged_attention(q, cache, page_table, cu, lens, window=0, scale=None, lse
     max_q, max_kv  upper bounds of the query and cached tokens of a request.  Left out, they are
                 read from cu and lens, which waits for the GPU: give them in serving loops.
     Returns out [tokens][heads][dim], or (out, lse [tokens][heads] float32).  Queries that see
-    nothing give 0 and -inf.  For serving: no gradient flows through it."""
+    nothing give 0 and -inf.  Tokens outside every request (padding) are not written: they hold what
+    out held, without out anything.  For serving: no gradient flows through it."""
     if max_q is None:
         max_q = int((cu[1:] - cu[:-1]).max()) if lens.numel() else 0
     if max_kv is None:

@@ -201,6 +201,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (rotate) {
     const at::Tensor& t = tensor(a[8], "table");
     check_table(t, dev);
+    // a null table stands for no rotation in the library, and one without rows has no address
+    TORCH_CHECK_VALUE(t.size(0) > 0, "a rotation needs a table with rows");
     TORCH_CHECK_VALUE(a[7] != Py_None, "a rotation needs pos");
     const at::Tensor& p = tensor(a[7], "pos");
     check_vector(p, "pos", at::kInt, tokens, dev);

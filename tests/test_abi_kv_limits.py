@@ -34,3 +34,11 @@ def test_flags_without_a_truth_value():
 def test_appends_of_any_length(kw):
     """Lengths beyond one launch's thread numbers are cut into several; there is no device here to launch on."""
     assert append(**kw) == LAUNCH
+
+
+def test_append_refuses_a_table_without_rows():
+    """It has no address, which the library takes for a call without rotation: the keys would be stored unturned."""
+    x, pos = torch.zeros(4, 2, 64), torch.zeros(4, dtype=torch.int32)
+    c = mxa.KVCache(*(torch.zeros((2, 2, 16, n), dtype=torch.uint8) for n in (64, 2, 64, 2)))
+    with pytest.raises(ValueError, match="rows"):
+        mxa.mx_kv_append(x, x, c, pos.long(), pos, torch.zeros(0, 32, 2))
