@@ -444,7 +444,9 @@ mx_status_t mx_kv_append(const void* k, const void* v, mx_dtype_t dtype, int64_t
  *   out    [tokens][heads][dim] contiguous, type of q, 16-byte aligned; lse FP32
  *          [tokens][heads] or NULL.
  *   workspace  mx_paged_attention_workspace bytes (16-byte aligned; may be NULL when that is 0);
- *          its contents need no preparation and are not kept between calls.
+ *          its contents need no preparation and are not kept between calls.  Where some request
+ *          is split, every row (token and head) of the call has room for as many partial results:
+ *          8192 tokens of 32 heads beside one that decodes over 131072 keys need 1.1 GB.
  * Scores, softmax sums and outputs are accumulated in FP32.  The softmax weights enter
  * the product with the values as two terms of the type of q (16 bits and more together)
  * for requests of up to 32 rows (query tokens x heads / kv_heads), rounded to that type

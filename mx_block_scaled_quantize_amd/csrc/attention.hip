@@ -55,7 +55,7 @@ constexpr int kFewRows = 32;
 // XCD's L2 serves one head's pages.
 //
 // A decoding call on short contexts is bound by latency: dependent loads, and code
-// that no workgroup has run yet comes from L2 at some 20 clocks an instruction.  So
+// that no workgroup has run yet, which has to come from L2 first.  So
 // what a workgroup runs once is kept short: no integer division (reciprocals come
 // from the host), the page numbers are read beside the lengths and not after them.
 struct AttnArgs {
@@ -298,11 +298,13 @@ template <int D, int NQ, int NW> struct FewLds {
 
 // One request, kv head and split of up to 16 NQ rows.  Wave w takes the 32-key steps
 // w, w + NW, ... of the split: no wave waits for another before the end.  Bound by
-// memory: a step of 128 channels is 8.4 KB and some 300 vector instructions, about half
-// of the time its bytes take.  The next step's bytes are loaded while this one is computed
-// where the registers allow it (1 request of 1021 keys: 9.6 us, without 11.6; long contexts
-// differ by 1%).  Measured with 32 query and 8 kv heads of 128 channels: 64 requests of 1650
-// to 8192 keys 135 us (4.9 TB/s), 4 of 118000 to 131072 keys 185 to 192 us (5.5 to 5.7 TB/s).
+// memory: a step of 128 channels is 8.4 KB and some 340 vector instructions, and the vector
+// units are busy 26% of the time, the matrix units 9% (64 requests of 8192 keys).  The next step's
+// bytes are loaded while this one is computed where the registers allow it (1 request of 1021
+// keys: 9.6 us, without 11.6; long contexts differ by 1%).  Measured with 32 query and 8 kv heads of
+// 128 channels: 64 requests of 1650 to 8192 keys 136 us (4.9 TB/s), 4 of 118000 to 131072 keys 185 us
+// (5.7 TB/s), 16 of 5 new tokens over 8192 keys 60 us.  192 and 256 channels: 64 requests of up to
+// 8192 keys 204 and 260 us.
 template <int DT, int D, int NQ, int NW>
 __device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, FewLds<D, NQ, NW>& lds) {
   using L = Deal<D>;
@@ -768,9 +770,10 @@ __device__ __forceinline__ v16f_t mfma32(u32x4_t a, u32x4_t b, v16f_t acc) {
 //     meet 8 different groups of banks.
 // Bound by vector work beside the matrix unit: a tile of 256 rows x 64 keys x 128 channels
 // has 2048 clocks of matrix instructions and about as many of vector instructions on every
-// SIMD, and takes 4000.  Measured: 2048 tokens over 32768 keys (32 and 8 heads of 128
-// channels) in 975 to 1000 us, 1.07 to 1.09 PFLOP/s; each wave reading the pages by itself
-// took 2783 us.
+// SIMD, which overlap little: each kind is busy 46 to 48% of 4200 clocks.  Measured: 2048 tokens
+// over 32768 keys (32 and 8 heads of 128 channels) in 964 to 1031 us on different cards, 1.03 to
+// 1.10 PFLOP/s; each wave reading the pages by itself took 2783 us.  With 256 channels one wave a
+// SIMD has nothing to overlap with: matrix unit 21%, vector unit 34% (600 tokens over 8192 keys, 294 to 301 us).
 template <int D, int NW> struct TileLds {
   static constexpr int kFrag = 1040;
   union {
@@ -1310,7 +1313,7 @@ mx_status_t plan_attention(int64_t tokens, int heads, int kv_heads, int dim, int
   };
   // Requests of few rows: workgroups of eight waves, one for every CU (measured against two and
   // more: 191 to 193 us for 4 requests of 131072 keys against 195 to 215; uneven lengths of 64
-  // requests even out by themselves, 135 us), none with less than 512 keys, two steps a wave.  Calls
+  // requests even out by themselves, 136 us), none with less than 512 keys, two steps a wave.  Calls
   // that would leave most of the CUs idle even at 256 keys take workgroups of four waves with 256
   // keys: code that is new to an instruction cache is fetched by fewer waves at a time (1 request
   // of 1021 keys: 9.6 us, with eight waves 11.3 to 12.4).

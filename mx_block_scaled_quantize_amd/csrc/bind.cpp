@@ -2,9 +2,10 @@
 // append, paged attention) with the interpreter's own C interface.
 //
 // A decoding step makes a few of these calls per layer, each on kernels of a few
-// microseconds, so what a call costs before its launch counts: marshalling in
-// Python takes 12 to 22 us (with ctypes), this 3 to 6.  Checks of tensors are here, those
-// of scalars in the library; the arithmetic is in libmx as everywhere else.
+// microseconds, so what a call costs before its launch counts: a call among others takes 4.3
+// to 7 us with this (one append, one small rotation), which marshalling in Python would
+// multiply.  Checks of tensors are here, those of scalars in the library; the arithmetic is in
+// libmx as everywhere else.
 
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>

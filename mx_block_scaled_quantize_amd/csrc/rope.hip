@@ -32,8 +32,8 @@ struct TableArgs {
 // complex product, z_{n+1} = z_n w, whose error grows by about 2^-52 a step and
 // so stays far below the FP32 result's rounding.  Consecutive lanes hold
 // consecutive pairs, so a row is written with contiguous 8-byte stores.  Measured:
-// 131072 rows of 64 pairs in 12.5 us, 5.4 TB/s written, what the memory takes; 8192 rows
-// in 5 us, the launch.
+// 131072 rows of 64 pairs in 12.8 us, 5.2 TB/s written, what the memory takes; 8192 rows
+// in 5.5 us, the launch.
 template <int kRun>
 __global__ __launch_bounds__(256) void rope_table_kernel(const TableArgs g) {
   const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
@@ -197,7 +197,7 @@ __device__ __forceinline__ void load_cs(const float2* __restrict__ table, int64_
 // One thread: one chunk (V pairs, or V copied channels) of HPT heads of one
 // token.  The table entries are loaded once for all its heads (for every head, a
 // table row would be twice a BF16 head's bytes).  Measured: 8192 tokens of 32 heads of
-// 128 BF16 channels in 27.8 us, 5.0 TB/s, which is the rate of a plain copy.
+// 128 BF16 channels in 28.6 us, 4.8 TB/s, near the rate of a plain copy (5.1).
 template <int IN, int V, bool HALF, int HPT>
 __device__ __forceinline__ void rope_item(const RopeArgs& g, uint32_t id) {
   using P = Pack<IN, V>;
@@ -372,8 +372,8 @@ __device__ __forceinline__ void append_item(const AppendArgs& g, const void* bas
 
 // One launch does all three tensors: the first q_blocks workgroups rotate q, the
 // next kv_blocks rotate and encode k, the last kv_blocks encode v.  Measured: 8192
-// tokens of 32 + 8 + 8 heads of 128 BF16 channels in 41 to 45 us, 4.2 to 4.6 TB/s; one
-// token 6.7 us, of which the kernel is 3 and the call the rest.
+// tokens of 32 + 8 + 8 heads of 128 BF16 channels in 45 us, 4.2 TB/s; one
+// token 6.6 us, of which the kernel is 2.4 and the call the rest.
 template <int IN, int VQ, bool HALF, int HPT, bool VEC>
 __global__ __launch_bounds__(256) void append_kernel(const AppendArgs g) {
   uint32_t b = blockIdx.x;
