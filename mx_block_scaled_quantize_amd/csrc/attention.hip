@@ -124,6 +124,11 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(v2u_t, a), __builtin_bit_cast(v2u_t, b)));
 }
 
+// Differences of halves, 0 where they would be negative.
+__device__ __forceinline__ uint32_t less2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(__builtin_bit_cast(v2u_t, a), __builtin_bit_cast(v2u_t, b)));
+}
+
 // Half `HI` of a packed pair.
 template <int DT, bool HI>
 __device__ __forceinline__ float unpack(uint32_t w) {
@@ -631,10 +636,11 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, 
     // ---- weights, in two terms of the type of q: one alone is off by up to 2^-9 (BF16), which outputs of
     // the same type would show (error against 64 bits 0.0023, with both 0.0017, the outputs' own rounding).
     // The second product costs 1% where memory bounds (64 requests of 8192 keys: 135.0 us without, 136.5 with).
-    // The first term is chopped and the second kept above 0 (2^-126 for BF16; 2^-24 for F16, where the first is
-    // not 0), so that an infinite value that every row sees makes infinities and no NaN: 0 times infinity.  A step
-    // that some row does not see whole has none left, and weights of 0 have to stay 0 there.
-    const uint32_t least = edge ? 0u : DT == IN_BF16 ? 0x00800080u : 0x00010001u;
+    // The first term is chopped and the second kept above 0 where the first is (at 2^-16 of it for BF16, from the
+    // bits of its exponent; at 2^-24 for F16), so that an infinite value that every row sees makes infinities
+    // and no NaN: 0 times infinity.  A step that some row does not see whole has none left, and weights of 0
+    // have to stay 0 in any.
+    const uint32_t least = DT == IN_BF16 ? (edge ? 0xFFFFFFFFu : 0x08000800u) : edge ? 0u : 0x00010001u;
     u32x4_t p[NQ], rest[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -646,7 +652,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& g, int req, int split, 
       for (int j = 0; j < 4; ++j) {
         p[n][j] = chop2<DT>(e[2 * j], e[2 * j + 1]);
         const uint32_t lost = pack2<DT>(e[2 * j] - unpack<DT, false>(p[n][j]), e[2 * j + 1] - unpack<DT, true>(p[n][j]));
-        rest[n][j] = max2(lost, DT == IN_F16 ? min2(p[n][j], least) : least);
+        rest[n][j] = max2(lost, DT == IN_BF16 ? less2(p[n][j], least) : min2(p[n][j], least));
       }
     }
     // ---- O^T

@@ -106,3 +106,23 @@ def test_nan_values_under_vanishing_weights(q_len, dtype):
     page, at = p.slot(0, 70)
     p.cache[2][page, 1, at, 11] = 0x7F
     p.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("form", ["one row tile, four waves", "one row tile, eight waves", "two row tiles", "tiles of four waves"])
+def test_large_values_under_vanishing_weights(form, dtype):
+    """Values near the type's largest whose weight is 2^-369 of the others': nothing of them is in the sum."""
+    heads, hk, reqs = FORMS[form]
+    p = Problem(reqs, heads, hk, 64, dtype=dtype, seed=12)
+    for r, (m, n) in enumerate(reqs):
+        low = np.arange(5, n - m, 9)
+        k = np.full((n, hk, 64), 4.0, np.float32)
+        k[low] = -4.0
+        v = np.random.default_rng(r).standard_normal((n, hk, 64)).astype(np.float32)
+        p.put(k, v, p.table[r, np.arange(n) // 16].astype(np.int64) * 16 + np.arange(n) % 16)
+        for key in low:
+            page, at = p.slot(r, int(key))
+            p.cache[2][page, :, at, ::2] = 0x7E          # 448 x 2^119, 448 x 2^7
+            p.cache[3][page, :, at] = 246 if dtype == "bf16" else 134
+    p.q.fill_(4.0)
+    check_sample(p)
