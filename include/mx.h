@@ -470,6 +470,123 @@ mx_status_t mx_paged_attention(const void* q, mx_dtype_t dtype, int64_t tokens, 
 mx_status_t mx_paged_attention_workspace(int64_t tokens, int heads, int kv_heads, int dim, int64_t requests,
                                          int64_t max_q, int64_t max_kv, int64_t window, int64_t* bytes);
 
+/* ---------------------------------------------------------------------------
+ * Beam search over the paged cache, and the cache's pages between two steps
+ *
+ * A pool of pages has an int32 count for every page: how many sequences hold it (0: it
+ * is free).  A sequence is a row of a page table, int32 [rows][table_cols] with row stride
+ * table_stride, and a length: it holds the pages of the first ceil(length / page) entries.
+ * Entries outside [0, pages) stand for no page.  Lengths count as within 0 ..
+ * table_cols * page.  The calls read counts, tables and lengths on the device and wait for
+ * nothing; they can be captured.  Which pages a sequence gets depends on these alone: the
+ * lowest free ones, in the order of the sequences.
+ * `layers` caches are caches of one shape that share the pool's page numbers, one for each
+ * layer of a model.  pages <= 2^31 - 1, rows and children <= 2^20, table_cols * page <=
+ * 2^31 - 1, kv_heads * page * dim <= 2^30. */
+
+/* Copies pages of every layer: page dst_pages[i] of dst[l] becomes page src_pages[i] of
+ * src[l], i < count (device int32 arrays).  src and dst have one shape but for the number
+ * of pages, and may be the same caches.  A pair with a page outside its pool is skipped.
+ * No page may be written twice, or written and read, in one call.
+ * Errors: MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */
+mx_status_t mx_kv_copy(const mx_kv_cache_t* src, const mx_kv_cache_t* dst, int layers, const int32_t* src_pages,
+                       const int32_t* dst_pages, int64_t count, hipStream_t stream);
+
+/* The sequences of the next step from those of the last: child i continues row parents[i]
+ * (several children may continue one row; a row outside [0, rows) stands for an empty
+ * sequence) and gets room for its new tokens, number cu[i] .. cu[i + 1] - 1 of all (as
+ * mx_paged_attention's cu).  It shares its parent's pages.  A last page that is partly
+ * filled and is to be written to becomes its own: where others hold the page too, the
+ * child gets a copy (of the tokens up to the next multiple of 16, every layer), but the
+ * first of several children of one row, none of them without new tokens, keeps the page
+ * where only they hold it.  Pages behind it are new.
+ *   release    != 0: the rows end with this call (each page loses their holds), so that a
+ *              child replaces its parent; 0: they stay beside the children.
+ *   parents    int32 [children]; NULL: child i continues row i (children == rows).
+ *   cu         int32 [children + 1], non-decreasing, or NULL: no new tokens (tokens == 0).
+ *   refs_out   counts after the call; may be refs itself.
+ *   table_out  int32 [children][out_cols] contiguous, out_cols >= table_cols; entries
+ *              behind a child's pages are -1.  Must not overlap page_table.
+ *   lens_out   int32 [children]: parent's length and the new tokens.  Must not overlap lens.
+ *   slots      int64 [tokens]: where mx_kv_append stores each new token; -1 for tokens of no child.
+ * A child that needs more pages than are left after the children before it took theirs, or
+ * than out_cols, gets none and no new tokens: its slots are -1, its length its parent's,
+ * its pages shared; and pages that it asked for are not given to later ones.
+ * The counts must be right (every row's hold counted once for each of its pages, and every
+ * other sequence's).
+ * workspace  mx_kv_fork_workspace bytes, 16-byte aligned; nothing is kept in it between calls.
+ * Errors: MX_ERR_SHAPE (also a workspace too small), MX_ERR_ARG (table_out or lens_out an input), MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */
+mx_status_t mx_kv_fork(const mx_kv_cache_t* caches, int layers, const int32_t* refs, const int32_t* page_table,
+                       int64_t table_stride, int64_t table_cols, const int32_t* lens, int64_t rows,
+                       const int32_t* parents, int64_t children, const int32_t* cu, int64_t tokens, int release,
+                       int32_t* refs_out, int32_t* table_out, int64_t out_cols, int32_t* lens_out, int64_t* slots,
+                       void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that mx_kv_fork needs for these arguments, in *bytes.  Errors: those of the same arguments there. */
+mx_status_t mx_kv_fork_workspace(int64_t pages, int64_t rows, int64_t children, int64_t tokens, int page,
+                                 int64_t* bytes);
+
+/* Cuts sequences to keep[r] tokens (those not longer stay; NULL: all end): each page behind
+ * the last kept one loses a hold, and is free when none is left.
+ *   refs_out, lens_out  counts and lengths after the call; may be refs and lens.
+ * Errors: MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */
+mx_status_t mx_kv_free(const int32_t* refs, int64_t pages, int page, const int32_t* page_table, int64_t table_stride,
+                       int64_t table_cols, const int32_t* lens, int64_t rows, const int32_t* keep, int32_t* refs_out,
+                       int32_t* lens_out, hipStream_t stream);
+
+/* Moves the pages in use to the front of the pool: with U of them (counts other than 0), the
+ * nth free page below U takes content and count of the nth used page from the pool's end.
+ * The table must have every sequence that holds pages.
+ *   refs_out   counts after the call; may be refs itself.
+ *   table_out  int32 [rows][table_cols] contiguous: the pages' new numbers (entries behind a
+ *              sequence's pages as they were); may be page_table itself if that is contiguous
+ *              (MX_ERR_ARG if it is not).
+ *   used       device int32: U.
+ * workspace  mx_kv_compact_workspace bytes, 16-byte aligned; nothing is kept in it between calls.
+ * Errors: MX_ERR_SHAPE (also a workspace too small), MX_ERR_ARG, MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */
+mx_status_t mx_kv_compact(const mx_kv_cache_t* caches, int layers, const int32_t* refs, const int32_t* page_table,
+                          int64_t table_stride, int64_t table_cols, const int32_t* lens, int64_t rows,
+                          int32_t* refs_out, int32_t* table_out, int32_t* used, void* workspace,
+                          int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that mx_kv_compact needs for a pool of `pages` pages, in *bytes. */
+mx_status_t mx_kv_compact_workspace(int64_t pages, int64_t* bytes);
+
+/* Beam search's choice of the next beams.  A request has `beams` beams, beam b a running
+ * score S_b (a sum of log-probabilities), and logits x_b; its candidates are
+ *   (b, v) of score S_b + x_bv - ln sum_u exp x_bu   for every token v with a logit above -inf,
+ *   a beam that is finished: itself alone, with score S_b and token `pad`.
+ * The `width` candidates of the highest scores become the next beams, the best first; of
+ * equal scores the lower beam's first, within a beam the higher logit's, of equal logits the
+ * lower token's.  A beam whose S_b is not finite, or whose logits hold a NaN or +inf or no
+ * finite one, has no candidates.  Where a request has fewer than width, the rest are empty
+ * beams: score -inf, token `pad`, beam 0's history.
+ *   logits     [requests][beams][vocab] of type dtype, strides in elements, token stride 1.
+ *   scores     FP32 [requests][beams]; finished uint8 (0 or 1), the same shape, or NULL.
+ *   width      1 .. 64; beams 1 .. 64; vocab 1 .. 2^30; requests <= 2^24.
+ *   eos        the token that finishes a beam (one outside the vocabulary: none does).
+ *   history    int32 [requests][beams][history_cols], lens int32 [requests][beams] (counted as
+ *              within 0 .. history_cols), or NULL both: the beams' tokens.
+ *   scores_out FP32, parents int32 (request * beams + beam, as mx_kv_fork takes them), tokens
+ *              int32, finished_out uint8, all [requests][width]; history_out int32
+ *              [requests][width][history_cols]: the parents' rows, each with its token behind
+ *              its last one (not for beams that were finished, are empty or are full);
+ *              lens_out int32 [requests][width].  None may overlap an input.
+ * Exponentials are FP32 and summed in FP32 over 64 logits and FP64 from there on; scores are
+ * compared in FP64 and rounded once to FP32.
+ * workspace  mx_beam_select_workspace bytes, 16-byte aligned; nothing is kept in it between calls.
+ * Errors: MX_ERR_UNSUPPORTED (dtype), MX_ERR_SHAPE (also a workspace too small), MX_ERR_ARG (eos or pad past 32
+ * bits), MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */
+mx_status_t mx_beam_select(const void* logits, mx_dtype_t dtype, int64_t requests, int64_t beams, int64_t vocab,
+                           int64_t request_stride, int64_t beam_stride, const float* scores, const uint8_t* finished,
+                           int64_t width, int64_t eos, int64_t pad, const int32_t* history, const int32_t* lens,
+                           int64_t history_cols, float* scores_out, int32_t* parents, int32_t* tokens,
+                           uint8_t* finished_out, int32_t* history_out, int32_t* lens_out, void* workspace,
+                           int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that mx_beam_select needs for these arguments, in *bytes. */
+mx_status_t mx_beam_select_workspace(int64_t requests, int64_t beams, int64_t vocab, int64_t width, int64_t* bytes);
+
 /* Human-readable name of a status code (static storage). */
 const char* mx_status_str(mx_status_t status);
 

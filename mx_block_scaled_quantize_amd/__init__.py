@@ -1,7 +1,7 @@
 """Python binding of libmx: OCP MX block quantization and block-scaled GEMM on
 AMD Instinct MI355X (gfx950).
 
-Argument marshalling only (of the rotary and cache operators by ``_bind.so``, from
+Argument marshalling only (of the rotary, cache and beam operators by ``_bind.so``, from
 ``csrc/bind.cpp``, which costs a call less time than ctypes).  Every step of the computation runs in the HIP
 kernels of ``libmx.so`` (built from ``csrc/`` by ``_build.py``); PyTorch only
 provides device memory and the current HIP stream.  There is no CPU fallback:
@@ -23,8 +23,14 @@ The functions carry the names of the C entry points declared in
     mx_rope(x, pos, table, layout, inverse, out)
     mx_kv_append(k, v, cache, slots, pos, table, layout, q, q_out)
     mx_paged_attention(q, cache, page_table, cu, lens, window, scale, lse, max_q, max_kv)
+    mx_beam_select(logits, scores, width, finished, eos, pad, history, lens)
+    mx_kv_fork(caches, refs, page_table, lens, cu, parents, release, tokens, cols, out)
+    mx_kv_free(refs, page_table, lens, page, keep, out)
+    mx_kv_compact(caches, refs, page_table, lens, out)
+    mx_kv_copy(src, src_pages, dst, dst_pages)
 
-KVCache (from new_kv_cache) is the paged MXFP8 key/value cache of the last two.
+KVCache (from new_kv_cache) is the paged MXFP8 key/value cache of mx_kv_append, mx_paged_attention and
+the mx_kv operators, which hold the pages of a pool by their counts (from new_page_refs).
 
 scale_layout "row" stores E8M0 scales row-major [lines][K/32]; "gemm" stores them
 in the GEMM layout [K/512][lines][16] (returned as a 3-D tensor of that shape).
@@ -32,7 +38,7 @@ in the GEMM layout [K/512][lines][16] (returned as a 3-D tensor of that shape).
 
 import ctypes
 import os
-from typing import NamedTuple
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -114,10 +120,23 @@ lib.mx_kv_append.argtypes = [_p, _p, _i32, _i64, _i64, _i64, _i64, _i64, _cache_
                              _i64, _i64, _p, _p]
 lib.mx_paged_attention.argtypes = [_p, _i32, _i64, _i32, _i64, _i64, _cache_p, _p, _i64, _i64, _p, _p, _i64, _i64, _i64,
                                    _i64, _f32, _p, _p, _p, _i64, _p]
+_layers_p = _cache_p
+lib.mx_kv_copy.argtypes = [_layers_p, _layers_p, _i32, _p, _p, _i64, _p]
+lib.mx_kv_fork.argtypes = [_layers_p, _i32, _p, _p, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i32, _p, _p, _i64, _p, _p, _p,
+                           _i64, _p]
+lib.mx_kv_fork_workspace.argtypes = [_i64, _i64, _i64, _i64, _i32, ctypes.POINTER(_i64)]
+lib.mx_kv_free.argtypes = [_p, _i64, _i32, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p]
+lib.mx_kv_compact.argtypes = [_layers_p, _i32, _p, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p]
+lib.mx_kv_compact_workspace.argtypes = [_i64, ctypes.POINTER(_i64)]
+lib.mx_beam_select.argtypes = [_p, _i32, _i64, _i64, _i64, _i64, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _i64, _p, _p, _p, _p,
+                               _p, _p, _p, _i64, _p]
+lib.mx_beam_select_workspace.argtypes = [_i64, _i64, _i64, _i64, ctypes.POINTER(_i64)]
 lib.mx_paged_attention_workspace.argtypes = [_i64, _i32, _i32, _i32, _i64, _i64, _i64, _i64, ctypes.POINTER(_i64)]
 for _f in (lib.mx_quantize, lib.mx_quantize_dual, lib.fp8_quantize_delayed, lib.mx_dequantize, lib.mx_gemm,
            lib.mx_quantize_sr, lib.mm_fp8, lib.mx_gemm_requant, lib.fp8_quantize_delayed_static, lib.mx_rope_table,
-           lib.mx_rope, lib.mx_kv_append, lib.mx_paged_attention, lib.mx_paged_attention_workspace):
+           lib.mx_rope, lib.mx_kv_append, lib.mx_paged_attention, lib.mx_paged_attention_workspace, lib.mx_kv_copy,
+           lib.mx_kv_fork, lib.mx_kv_fork_workspace, lib.mx_kv_free, lib.mx_kv_compact, lib.mx_kv_compact_workspace,
+           lib.mx_beam_select, lib.mx_beam_select_workspace):
     _f.restype = ctypes.c_int
 lib.mx_status_str.argtypes = [ctypes.c_int]
 lib.mx_status_str.restype = ctypes.c_char_p
@@ -125,7 +144,9 @@ lib.mx_abi_version.restype = ctypes.c_int
 
 ENTRY_POINTS = ("mx_quantize", "mx_quantize_dual", "fp8_quantize_delayed", "mx_dequantize", "mx_gemm",
                 "mx_quantize_sr", "mm_fp8", "mx_gemm_requant", "fp8_quantize_delayed_static", "mx_rope_table",
-                "mx_rope", "mx_kv_append", "mx_paged_attention", "mx_paged_attention_workspace", "mx_status_str",
+                "mx_rope", "mx_kv_append", "mx_paged_attention", "mx_paged_attention_workspace", "mx_kv_copy",
+                "mx_kv_fork", "mx_kv_fork_workspace", "mx_kv_free", "mx_kv_compact", "mx_kv_compact_workspace",
+                "mx_beam_select", "mx_beam_select_workspace", "mx_status_str",
                 "mx_abi_version")
 
 
@@ -508,3 +529,83 @@ def mx_paged_attention(q, cache, page_table, cu, lens, window=0, scale=None, lse
     if max_kv is None:
         max_kv = int(lens.max()) if lens.numel() else 0
     return _bind.paged_attention(q, *cache, page_table, cu, lens, window, scale, lse, max_q, max_kv, out)
+
+
+# ---------------------------------------------------------------- beams, and the pages between two steps
+def new_page_refs(pages: int, device="cuda") -> torch.Tensor:
+    """Counts of holders of a pool's pages, all free: int32 [pages]."""
+    return torch.zeros(pages, dtype=torch.int32, device=device)
+
+
+class Fork(NamedTuple):
+    """What mx_kv_fork gives: the pool's counts, and the children's page table, lengths and new tokens' slots."""
+    refs: torch.Tensor
+    page_table: torch.Tensor
+    lens: torch.Tensor
+    slots: torch.Tensor
+
+
+class BeamStep(NamedTuple):
+    """What mx_beam_select gives, each [requests][width] (history [requests][width][tokens])."""
+    scores: torch.Tensor
+    parents: torch.Tensor
+    tokens: torch.Tensor
+    finished: torch.Tensor
+    history: Optional[torch.Tensor]
+    lens: Optional[torch.Tensor]
+
+
+def mx_beam_select(logits, scores, width=None, finished=None, eos=-1, pad=0, history=None, lens=None) -> BeamStep:
+    """The best ``width`` (the number of beams by default, at most 64) continuations of each request's beams.
+
+    logits      [requests][beams][vocab] float32, bfloat16 or float16, any strides but the tokens'
+    scores      float32 [requests][beams]: sums of log-probabilities.  A first step, with the same prompt in
+                every beam, has 0 in beam 0 and -inf (no beam) in the others.
+    finished    bool [requests][beams]: beams that continue as they are, with token ``pad``
+    eos         the token that finishes a beam
+    history, lens  int32 [requests][beams][tokens] and [requests][beams]: the beams' tokens, reordered by
+                parent, each with its new token behind
+    parents of the result number the beams of all requests in a row, as mx_kv_fork takes them.  Fewer
+    candidates than width (logits of -inf are none) leave empty beams of score -inf."""
+    return BeamStep(*_bind.beam_select(logits, scores, width, finished, eos, pad, history, lens))
+
+
+def mx_kv_fork(caches, refs, page_table, lens, cu=None, parents=None, release=True, tokens=None, cols=None,
+               out=None) -> Fork:
+    """The sequences of the next step, with pages and slots for their new tokens.
+
+    caches      a KVCache, or one for each layer of a model (they share the pool's page numbers)
+    refs        int32 [pages] counts of holders (new_page_refs)
+    page_table, lens  int32 [rows][pages a row may have] and [rows]: the sequences so far
+    cu          int32 [children + 1]: child i has the new tokens cu[i] .. cu[i + 1] - 1; None: none
+    parents     int32 [children]: the row that a child continues (-1: an empty sequence); None: its own
+    release     the rows end, children replace them; False: they stay beside the children
+    tokens      cu's last entry.  Left out, it is read, which waits for the GPU: give it in serving loops.
+    cols        width of the new table, the old one's by default
+    out         (refs, page_table, lens, slots) to write to; refs may be the counts given
+    Children share their parent's pages.  One that writes behind a partly filled page others hold gets
+    a copy of it, in every layer.  A child for which pages lack gets no new tokens (its slots are -1,
+    its length stays)."""
+    if tokens is None:
+        tokens = int(cu[-1]) if cu is not None else 0
+    return Fork(*_bind.kv_fork(caches, refs, page_table, lens, cu, parents, release, tokens, cols, out))
+
+
+def mx_kv_free(refs, page_table, lens, page, keep=None, out=None):
+    """Cuts sequences to ``keep`` tokens (int32 [rows]; None: all end) and gives back their pages of
+    ``page`` tokens.  Returns (refs, lens), new tensors or those of out, which may be the ones given."""
+    return _bind.kv_free(refs, page_table, lens, page, keep, out)
+
+
+def mx_kv_compact(caches, refs, page_table, lens, out=None):
+    """Moves the pages in use to the front of the pool, in every layer.  Returns (refs, page_table, used),
+    used int32 [1]: how many are in use.  out may hold the refs and the table given.  The table must have
+    every sequence that holds pages."""
+    return _bind.kv_compact(caches, refs, page_table, lens, out)
+
+
+def mx_kv_copy(src, src_pages, dst, dst_pages):
+    """Copies pages src_pages (int32) of the caches src to pages dst_pages of dst, which may be the same
+    caches: a KVCache each, or one for each layer.  Pairs with a page outside its pool are skipped; no page
+    may be written twice, or written and read, in one call."""
+    _bind.kv_copy(src, src_pages, dst, dst_pages)

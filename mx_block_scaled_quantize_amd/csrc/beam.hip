@@ -1,0 +1,449 @@
+// Beam search's selection over beams and vocabulary on gfx950.
+//
+// A candidate (b, v) of a request has score S_b + x_bv - ln sum_u exp x_bu.  Within a beam the order of scores is
+// the order of logits, so one read of the logits gives both things that are needed: the sum, kept with its running
+// maximum, and the beam's best `width` logits.  A wave reads a segment of one beam's logits; a second launch joins the
+// segments of a request's beams, scores their candidates in 64 bits and takes the best, reorders the token
+// histories and appends the tokens.
+//
+// It is bound by the read of the logits where there are many, by the two launches and their latency where there are few.
+
+#include "mx_launch.hpp"
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <type_traits>
+
+namespace mxk {
+
+constexpr int kMostBeams = 64;              // a lane for each when they are merged
+constexpr int kMostWidth = 64;              // a lane for each of a beam's candidates
+constexpr int kMostSplits = 64;             // a lane for each segment of a beam's logits
+constexpr int kLoads = 8;                   // 16-byte loads of a lane in flight
+constexpr int kBuffer = 512;                // candidates a wave sets aside before it sorts them in
+
+// Sum and maximum of a segment: sum exp(x - m).
+struct Part {
+  double s;
+  float m;
+  uint32_t pad;
+};
+
+struct BeamArgs {
+  const void* x;
+  const float* scores;
+  const uint8_t* finished;
+  const int32_t *history, *lens;
+  float* scores_out;
+  int32_t *parents, *tokens, *history_out, *lens_out;
+  uint8_t* finished_out;
+  Part* parts;                              // [rows][splits]
+  uint64_t* best;                           // [rows][splits][keep]
+  int64_t request_stride, beam_stride, rows, segment;
+  int requests, beams, vocab, width, keep, splits, eos, pad, cols;
+};
+
+// Whole numbers in the order of floats (-0 below +0: callers add 0 first).
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+// The higher the better: the logit, of equal ones the lower token.  0 stands for none.
+__device__ __forceinline__ uint64_t candidate(float x, uint32_t token) {
+  return uint64_t(ordered(x + 0.0f)) << 32 | uint32_t(~token);
+}
+
+__device__ __forceinline__ uint64_t shuffle_xor(uint64_t x, int d) {
+  const uint32_t lo = __shfl_xor(int(uint32_t(x)), d), hi = __shfl_xor(int(uint32_t(x >> 32)), d);
+  return uint64_t(hi) << 32 | lo;
+}
+
+__device__ __forceinline__ uint64_t shuffle(uint64_t x, int lane) {
+  const uint32_t lo = __shfl(int(uint32_t(x)), lane), hi = __shfl(int(uint32_t(x >> 32)), lane);
+  return uint64_t(hi) << 32 | lo;
+}
+
+// list: 64 candidates, the best in lane 0; takes in 64 more in any order: these are sorted the other way round, so
+// that lane by lane the better of the two are the best 64 of all, up and down once, which six steps put in order.
+__device__ __forceinline__ uint64_t absorb(uint64_t list, uint64_t x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int size = 2; size <= 64; size *= 2)
+#pragma unroll
+    for (int d = size / 2; d >= 1; d /= 2) {
+      const uint64_t y = shuffle_xor(x, d);
+      const bool small = ((lane & size) == 0) == ((lane & d) == 0);
+      x = (x < y) == small ? x : y;
+    }
+  x = x > list ? x : list;
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) {
+    const uint64_t y = shuffle_xor(x, d);
+    x = (x < y) == ((lane & d) != 0) ? x : y;
+  }
+  return x;
+}
+
+// A wave's best `keep` candidates of what it has seen.
+struct Best {
+  uint64_t list = 0;                        // a lane each, the best in lane 0
+  uint64_t least = 0;                       // the keep-th of the list
+  float floor = -FLT_MAX;                   // no logit below it can enter
+  int waiting = 0;                          // candidates set aside in the buffer
+
+  __device__ __forceinline__ void take_in(uint64_t* buffer, int keep) {
+    const int lane = threadIdx.x & 63;
+    while (waiting > 0) {
+      const int n = min(waiting, 64);
+      waiting -= n;
+      list = absorb(list, lane < n ? buffer[waiting + lane] : 0);
+    }
+    least = shuffle(list, keep - 1);
+    if (least) floor = unordered(uint32_t(least >> 32));
+  }
+};
+
+template <int DT>
+struct Elements;
+template <>
+struct Elements<MX_F32> {
+  static constexpr int kVec = 4;
+  using Type = float;
+  static __device__ __forceinline__ float at(const uint4& v, int j) {
+    return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
+  }
+  static __device__ __forceinline__ float one(float x) { return x; }
+  static constexpr uint32_t kNone = 0xFF800000u;
+};
+template <>
+struct Elements<MX_BF16> {
+  static constexpr int kVec = 8;
+  using Type = uint16_t;
+  static __device__ __forceinline__ float at(const uint4& v, int j) {
+    const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
+    return __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
+  }
+  static __device__ __forceinline__ float one(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
+  static constexpr uint32_t kNone = 0xFF80FF80u;
+};
+template <>
+struct Elements<MX_F16> {
+  static constexpr int kVec = 8;
+  using Type = uint16_t;
+  static __device__ __forceinline__ float one(uint16_t x) {
+    return float(__builtin_bit_cast(_Float16, x));
+  }
+  static __device__ __forceinline__ float at(const uint4& v, int j) {
+    const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
+    return one(uint16_t(j & 1 ? w >> 16 : w & 0xFFFFu));
+  }
+  static constexpr uint32_t kNone = 0xFC00FC00u;
+};
+
+// A beam that can be continued.
+__device__ __forceinline__ bool live(const BeamArgs& g, int64_t row) {
+  return !(g.finished && g.finished[row]) && isfinite(g.scores[row]);
+}
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// A wave for each segment of each beam's logits.  Eight loads of 16 bytes a lane are in flight; a chunk's maximum
+// moves each lane's own reference before its exponentials are added (in 32 bits within a chunk, in 64 across chunks).
+// The first chunk's keep-th largest lane maximum is a bound that at least keep logits reach: those that reach it,
+// some more than keep, are set aside and sorted.
+template <int DT>
+__global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
+  using E = Elements<DT>;
+  using T = typename E::Type;
+  constexpr int kVec = E::kVec, kChunk = 64 * kVec * kLoads;
+  __shared__ uint64_t buffers[4][kBuffer];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint64_t* buffer = buffers[wave];
+  const int64_t id = int64_t(blockIdx.x) * 4 + wave;
+  const int64_t row = id / g.splits;
+  const int split = int(id - row * g.splits);
+  if (row >= g.rows || !live(g, row)) return;
+  const int64_t request = row / g.beams;
+  const T* x = static_cast<const T*>(g.x) + request * g.request_stride + (row - request * g.beams) * g.beam_stride;
+  const int begin = int(split * g.segment), end = int(min(int64_t(g.vocab), (split + 1) * g.segment));
+  Best best;
+  float m = -FLT_MAX;
+  double s = 0.0;
+  for (int at = begin; at < end; at += kChunk) {
+    uint4 v[kLoads];
+    float odd = -INFINITY;                  // of the elements behind the last whole 16 bytes, a lane has one
+    const int whole = end - (end - begin) % kVec;          // only a row's last segment has others
+    if (at + kChunk <= whole) {
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) __builtin_memcpy(&v[u], x + at + (u * 64 + lane) * kVec, 16);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        v[u] = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+        const int i = at + (u * 64 + lane) * kVec;
+        if (i < whole) __builtin_memcpy(&v[u], x + i, 16);
+      }
+      if (whole + lane < end && at + kChunk >= whole) odd = E::one(x[whole + lane]);
+    }
+    float top = odd;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) top = fmaxf(top, E::at(v[u], j));
+    if (top > m) {
+      s *= double(__builtin_amdgcn_exp2f((m - top) * kLog2e));
+      m = top;
+    }
+    float sum = __builtin_amdgcn_exp2f((odd - m) * kLog2e);
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      float part = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) part += __builtin_amdgcn_exp2f((E::at(v[u], j) - m) * kLog2e);
+      sum += part;
+    }
+    s += double(sum);
+    if (at == begin) {
+      // a bound that keep lanes' maxima reach, to 20 bits: the sign, the exponent and eleven more
+      const uint32_t key = ordered(top + 0.0f);
+      uint32_t bound = 0;
+#pragma unroll
+      for (int bit = 31; bit >= 12; --bit)
+        if (__popcll(__ballot(key >= (bound | 1u << bit))) >= g.keep) bound |= 1u << bit;
+      best.floor = bound ? fmaxf(unordered(bound), -FLT_MAX) : -FLT_MAX;
+      // bit patterns of NaN order above all numbers; the row is then passed over whatever is kept
+      if (!(best.floor <= FLT_MAX)) best.floor = FLT_MAX;
+    }
+    if (__ballot(top >= best.floor) == 0) continue;
+    const int before = best.waiting;
+    {
+      auto set_aside = [&](float y, uint32_t token) {
+        const bool hit = y >= best.floor;
+        const uint64_t mask = __ballot(hit);
+        if (mask == 0) return;
+        const int to = best.waiting + __popcll(mask & ((uint64_t(1) << lane) - 1));
+        if (hit && to < kBuffer) buffer[to] = candidate(y, token);
+        best.waiting += __popcll(mask);
+      };
+      set_aside(odd, uint32_t(whole + lane));
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) set_aside(E::at(v[u], j), uint32_t(at + (u * 64 + lane) * kVec + j));
+    }
+    if (best.waiting > kBuffer) {
+      // very many equal logits: 64 at a time in the order of the tokens, so that the list soon holds the lowest
+      best.waiting = before;
+      best.take_in(buffer, g.keep);
+      for (int i = at; i < min(end, at + kChunk); i += 64) {
+        const uint64_t c = i + lane < end && i + lane < at + kChunk ? candidate(E::one(x[i + lane]), uint32_t(i + lane)) : 0;
+        const bool hit = c > best.least && c >= uint64_t(ordered(-FLT_MAX)) << 32;
+        const uint64_t mask = __ballot(hit);
+        if (mask == 0) continue;
+        if (hit) buffer[best.waiting + __popcll(mask & ((uint64_t(1) << lane) - 1))] = c;
+        best.waiting += __popcll(mask);
+        if (best.waiting >= 64) best.take_in(buffer, g.keep);
+      }
+    } else if (best.waiting >= 64) {
+      best.take_in(buffer, g.keep);
+    }
+  }
+  best.take_in(buffer, g.keep);
+  float all = m;
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) all = fmaxf(all, __shfl_xor(all, d));
+  s *= double(__builtin_amdgcn_exp2f((m - all) * kLog2e));
+#pragma unroll
+  for (int d = 32; d >= 1; d /= 2) s += __shfl_xor(s, d);
+  if (lane == 0) g.parts[id] = {s, all, 0};
+  if (lane < g.keep) g.best[id * g.keep + lane] = best.list;
+}
+
+// A workgroup for each request, several where long histories are copied (each takes the same decision and copies
+// some of the columns).
+__global__ __launch_bounds__(256) void beam_merge_kernel(const BeamArgs g) {
+  extern __shared__ double score[];         // [beams][keep], and the tokens behind them
+  uint32_t* token = reinterpret_cast<uint32_t*>(score + g.beams * g.keep);
+  __shared__ int chosen_beam[kMostWidth];
+  __shared__ int chosen_token[kMostWidth];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int request = blockIdx.x;
+  const int64_t row0 = int64_t(request) * g.beams;
+  for (int b = wave; b < g.beams; b += 4) {
+    const int64_t row = row0 + b;
+    double mine = -INFINITY;
+    uint32_t v = 0;
+    if (live(g, row)) {
+      Part p = {0.0, -FLT_MAX, 0};
+      if (lane < g.splits) p = g.parts[row * g.splits + lane];
+      float all = p.m;
+#pragma unroll
+      for (int d = 32; d >= 1; d /= 2) all = fmaxf(all, __shfl_xor(all, d));
+      double s = p.s * exp(double(p.m) - double(all));
+#pragma unroll
+      for (int d = 32; d >= 1; d /= 2) s += __shfl_xor(s, d);
+      const double log_s = log(s);            // apart from the maximum, beside which it could vanish
+      uint64_t list = 0;
+      const int count = g.splits * g.keep;
+      const uint64_t* from = g.best + row * count;
+      for (int i = 0; i < count; i += 64) {
+        const uint64_t c = i + lane < count ? from[i + lane] : 0;
+        if (__ballot(c > shuffle(list, g.keep - 1))) list = absorb(list, c);
+      }
+      // a row with NaN or +inf, or without a finite logit, has no candidates
+      if (list && isfinite(log_s) && isfinite(all)) {
+        mine = double(g.scores[row]) + ((double(unordered(uint32_t(list >> 32))) - double(all)) - log_s);
+        v = ~uint32_t(list);
+      }
+    } else if (isfinite(g.scores[row]) && lane == 0) {
+      mine = g.scores[row];                 // finished: itself
+      v = uint32_t(g.pad);
+    }
+    if (lane < g.keep) {
+      score[b * g.keep + lane] = mine;
+      token[b * g.keep + lane] = v;
+    }
+  }
+  __syncthreads();
+  if (wave == 0) {
+    // lane b holds the best candidate of beam b that is left
+    int at = 0;
+    double head = lane < g.beams ? score[lane * g.keep] : -INFINITY;
+    for (int j = 0; j < g.width; ++j) {
+      double top = head;
+      int from = lane;
+#pragma unroll
+      for (int d = 1; d <= 32; d *= 2) {
+        const double y = __shfl_xor(top, d);
+        const int f = __shfl_xor(from, d);
+        if (y > top || (y == top && f < from)) {
+          top = y;
+          from = f;
+        }
+      }
+      const bool real = top > -INFINITY;
+      if (lane == from) {
+        if (blockIdx.y == 0) g.scores_out[int64_t(request) * g.width + j] = real ? float(top) : -INFINITY;
+        chosen_beam[j] = real ? lane : -1;
+        chosen_token[j] = real ? int(token[lane * g.keep + at]) : g.pad;
+        if (real) {
+          ++at;
+          head = at < g.keep ? score[lane * g.keep + at] : -INFINITY;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (blockIdx.y == 0 && int(threadIdx.x) < g.width) {
+    const int j = threadIdx.x, b = chosen_beam[j], v = chosen_token[j];
+    const int64_t row = row0 + max(b, 0), o = int64_t(request) * g.width + j;
+    const bool was = b >= 0 && g.finished && g.finished[row];
+    g.parents[o] = int32_t(row);
+    g.tokens[o] = v;
+    g.finished_out[o] = was || (b >= 0 && v == g.eos);
+    if (g.lens) {
+      const int n = min(max(g.lens[row], 0), g.cols);
+      g.lens_out[o] = b >= 0 && !was && n < g.cols ? n + 1 : n;
+    }
+  }
+  if (!g.history || g.cols == 0) return;
+  for (int j = wave; j < g.width; j += 4) {
+    const int b = chosen_beam[j];
+    const int64_t row = row0 + max(b, 0);
+    const int32_t* from = g.history + row * g.cols;
+    int32_t* to = g.history_out + (int64_t(request) * g.width + j) * g.cols;
+    const bool grows = b >= 0 && !(g.finished && g.finished[row]);
+    const int n = min(max(g.lens[row], 0), g.cols);
+    for (int i = blockIdx.y * 64 + lane; i < g.cols; i += gridDim.y * 64) to[i] = grows && i == n ? chosen_token[j] : from[i];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+// Segments of a beam's logits: enough waves for eight on every SIMD, but at least 1024 logits each (shorter ones cost
+// the second launch more than they save the first).
+mx_status_t plan(BeamArgs& g, mx_dtype_t dtype, int64_t requests, int64_t beams, int64_t vocab, int64_t width) {
+  if (dtype != MX_F32 && dtype != MX_BF16 && dtype != MX_F16) return MX_ERR_UNSUPPORTED;
+  if (requests < 0 || requests > (int64_t(1) << 24) || beams < 1 || beams > kMostBeams || width < 1 || width > kMostWidth ||
+      vocab < 1 || vocab > (int64_t(1) << 30))
+    return MX_ERR_SHAPE;
+  g.requests = int(requests);
+  g.beams = int(beams);
+  g.rows = requests * beams;
+  g.vocab = int(vocab);
+  g.width = int(width);
+  g.keep = int(std::min(width, vocab));
+  const int64_t waves = 32 * std::max<int64_t>(device_cus(), 1);
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kMostSplits, waves / std::max<int64_t>(g.rows, 1)));
+  const int64_t least = std::max<int64_t>(1024, (vocab + want - 1) / want);
+  g.segment = (least + 511) / 512 * 512;
+  g.splits = int((vocab + g.segment - 1) / g.segment);
+  return MX_OK;
+}
+
+inline int64_t parts_bytes(const BeamArgs& g) { return g.rows * g.splits * int64_t(sizeof(Part)); }
+inline int64_t best_bytes(const BeamArgs& g) { return g.rows * g.splits * g.keep * int64_t(sizeof(uint64_t)); }
+
+}  // namespace mxk
+
+using namespace mxk;
+
+extern "C" mx_status_t mx_beam_select_workspace(int64_t requests, int64_t beams, int64_t vocab, int64_t width,
+                                                int64_t* bytes) {
+  if (!bytes) return MX_ERR_NULL;
+  BeamArgs g = {};
+  const mx_status_t st = plan(g, MX_F32, requests, beams, vocab, width);
+  if (st != MX_OK) return st;
+  *bytes = parts_bytes(g) + best_bytes(g);
+  return MX_OK;
+}
+
+extern "C" mx_status_t mx_beam_select(const void* logits, mx_dtype_t dtype, int64_t requests, int64_t beams,
+                                      int64_t vocab, int64_t request_stride, int64_t beam_stride, const float* scores,
+                                      const uint8_t* finished, int64_t width, int64_t eos, int64_t pad,
+                                      const int32_t* history, const int32_t* lens, int64_t history_cols,
+                                      float* scores_out, int32_t* parents, int32_t* tokens, uint8_t* finished_out,
+                                      int32_t* history_out, int32_t* lens_out, void* workspace,
+                                      int64_t workspace_bytes, hipStream_t stream) {
+  BeamArgs g = {};
+  const mx_status_t st = plan(g, dtype, requests, beams, vocab, width);
+  if (st != MX_OK) return st;
+  if (history_cols < 0 || history_cols > INT32_MAX) return MX_ERR_SHAPE;
+  if (eos < INT32_MIN || eos > INT32_MAX || pad < INT32_MIN || pad > INT32_MAX) return MX_ERR_ARG;
+  if (requests == 0) return MX_OK;
+  if (!logits || !scores || !scores_out || !parents || !tokens || !finished_out) return MX_ERR_NULL;
+  const bool with_history = history || lens || history_out || lens_out;
+  if (with_history && (!lens || !lens_out || (history_cols && (!history || !history_out)))) return MX_ERR_NULL;
+  auto off4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+  if (reinterpret_cast<uintptr_t>(logits) % (dtype == MX_F32 ? 4 : 2)) return MX_ERR_ALIGN;
+  if (off4(scores) || off4(scores_out) || off4(parents) || off4(tokens) || off4(history) || off4(lens) ||
+      off4(history_out) || off4(lens_out))
+    return MX_ERR_ALIGN;
+  if (workspace_bytes < parts_bytes(g) + best_bytes(g)) return MX_ERR_SHAPE;
+  if (!workspace) return MX_ERR_NULL;
+  if (misaligned(workspace)) return MX_ERR_ALIGN;
+  g.x = logits; g.scores = scores; g.finished = finished; g.history = history; g.lens = lens;
+  g.scores_out = scores_out; g.parents = parents; g.tokens = tokens; g.finished_out = finished_out;
+  g.history_out = history_out; g.lens_out = lens_out;
+  g.parts = static_cast<Part*>(workspace);
+  g.best = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + parts_bytes(g));
+  g.request_stride = request_stride; g.beam_stride = beam_stride;
+  g.eos = int(eos); g.pad = int(pad); g.cols = int(history_cols);
+  const unsigned blocks = unsigned((g.rows * g.splits + 3) / 4);
+  if (dtype == MX_F32) beam_scan_kernel<MX_F32><<<blocks, 256, 0, stream>>>(g);
+  else if (dtype == MX_BF16) beam_scan_kernel<MX_BF16><<<blocks, 256, 0, stream>>>(g);
+  else beam_scan_kernel<MX_F16><<<blocks, 256, 0, stream>>>(g);
+  // 64 KiB of history a workgroup where there are few requests
+  const int64_t wide = with_history ? g.width * int64_t(g.cols) * 4 / 65536 : 0;
+  const int64_t most = std::max<int64_t>(1, 2 * std::max<int64_t>(device_cus(), 1) / requests);
+  const unsigned y = unsigned(std::max<int64_t>(1, std::min(wide, most)));
+  beam_merge_kernel<<<dim3(unsigned(requests), y), 256, size_t(g.beams) * g.keep * 12, stream>>>(g);
+  return hipGetLastError() == hipSuccess ? MX_OK : MX_ERR_LAUNCH;
+}

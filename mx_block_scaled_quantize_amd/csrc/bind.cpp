@@ -1,5 +1,5 @@
 // Python binding of the serving entry points (rotary tables, rotation, cache
-// append, paged attention) with the interpreter's own C interface.
+// append, paged attention, the cache's pages, beam selection) with the interpreter's own C interface.
 //
 // A decoding step makes a few of these calls per layer, each on kernels of a few
 // microseconds, so what a call costs before its launch counts: a call among others takes 4.3
@@ -16,6 +16,7 @@
 #include <c10/hip/HIPStream.h>
 
 #include <cmath>
+#include <vector>
 
 #include "../../include/mx.h"
 
@@ -290,6 +291,263 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// One cache (four tensors) or a sequence of them, one for each layer.
+std::vector<mx_kv_cache_t> layers_of(PyObject* o, const char* name, at::Device& dev) {
+  THPObjectPtr seq(PySequence_Fast(o, "expected a KVCache or a sequence of KVCaches"));
+  if (!seq) throw python_error();
+  const Py_ssize_t n = PySequence_Fast_GET_SIZE(seq.get());
+  PyObject** items = PySequence_Fast_ITEMS(seq.get());
+  TORCH_CHECK_VALUE(n > 0, name, " must have a layer");
+  std::vector<mx_kv_cache_t> caches;
+  if (THPVariable_Check(items[0])) {
+    TORCH_CHECK_VALUE(n == 4, name, " must be a KVCache or a sequence of KVCaches");
+    dev = THPVariable_Unpack(items[0]).device();
+    caches.push_back(cache_of(items, dev));
+    return caches;
+  }
+  for (Py_ssize_t l = 0; l < n; ++l) {
+    THPObjectPtr one(PySequence_Fast(items[l], "expected a KVCache or a sequence of KVCaches"));
+    if (!one) throw python_error();
+    TORCH_CHECK_VALUE(PySequence_Fast_GET_SIZE(one.get()) == 4, name, " must be a KVCache or a sequence of KVCaches");
+    PyObject** four = PySequence_Fast_ITEMS(one.get());
+    if (l == 0) dev = tensor(four[0], name).device();
+    caches.push_back(cache_of(four, dev));
+  }
+  return caches;
+}
+
+int layer_count(const std::vector<mx_kv_cache_t>& c) { return narrow_int(int64_t(c.size()), "layers"); }
+
+const int32_t* ints(const at::Tensor& t) { return static_cast<const int32_t*>(t.data_ptr()); }
+int32_t* ints_out(const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
+
+void check_page_table(const at::Tensor& t, int64_t rows, const at::Device& dev) {
+  TORCH_CHECK_VALUE(t.scalar_type() == at::kInt && t.dim() == 2 && t.size(0) == rows &&
+                        (t.stride(1) == 1 || t.size(1) <= 1) && t.device() == dev,
+                    "page_table must be an int32 tensor [rows][pages] with contiguous rows, a row for each length");
+}
+
+// Rows that do not overlap: a table expanded from one row is no table to write or to count twice.
+int64_t row_stride(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+
+int64_t vector_size(const at::Tensor& t, const char* name) {
+  TORCH_CHECK_VALUE(t.dim() == 1, name, " must be a vector");
+  return t.size(0);
+}
+
+// The n-th of the tensors to write to, or a new one.
+at::Tensor out_or_new(PyObject* out, Py_ssize_t n, const char* name, at::IntArrayRef shape, at::ScalarType dt,
+                      const at::TensorOptions& like) {
+  if (out == Py_None) return at::empty(shape, like.dtype(dt));
+  const at::Tensor& t = tensor(PyTuple_GET_ITEM(out, n), name);
+  TORCH_CHECK_VALUE(t.sizes() == shape && t.scalar_type() == dt && t.is_contiguous() && t.device() == like.device(), name,
+                    " must be a contiguous ", dt, " tensor of shape ", shape, " on the device of the other arguments");
+  return t;
+}
+
+void check_out_tuple(PyObject* out, Py_ssize_t n) {
+  TORCH_CHECK_VALUE(out == Py_None || (PyTuple_Check(out) && PyTuple_GET_SIZE(out) == n), "out must be a tuple of ", n,
+                    " tensors");
+}
+
+PyObject* wrapped(std::initializer_list<at::Tensor> tensors) {
+  THPObjectPtr r(PyTuple_New(Py_ssize_t(tensors.size())));
+  if (!r) throw python_error();
+  Py_ssize_t i = 0;
+  for (const at::Tensor& t : tensors) {
+    PyObject* o = Py_None;
+    if (t.defined()) {
+      o = THPVariable_Wrap(t);
+      if (!o) throw python_error();
+    } else {
+      Py_INCREF(o);
+    }
+    PyTuple_SET_ITEM(r.get(), i++, o);
+  }
+  return r.release();
+}
+
+// kv_copy(src, src_pages, dst, dst_pages)
+PyObject* kv_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_args(n, 4);
+  at::Device dev(at::kCPU), other(at::kCPU);
+  const std::vector<mx_kv_cache_t> src = layers_of(a[0], "src", dev), dst = layers_of(a[2], "dst", other);
+  TORCH_CHECK_VALUE(dev == other, "src and dst must be on one device");
+  TORCH_CHECK_VALUE(src.size() == dst.size(), "src and dst must have the same layers");
+  const at::Tensor &from = tensor(a[1], "src_pages"), &to = tensor(a[3], "dst_pages");
+  const int64_t count = vector_size(from, "src_pages");
+  check_vector(from, "src_pages", at::kInt, count, dev);
+  check_vector(to, "dst_pages", at::kInt, count, dev);
+  OnDevice on(dev);
+  check_status(mx_kv_copy(src.data(), dst.data(), layer_count(src), ints(from), ints(to), count, on.stream));
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
+// kv_fork(caches, refs, page_table, lens, cu or None, parents or None, release, tokens, cols or None, out or None)
+PyObject* kv_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_args(n, 10);
+  at::Device dev(at::kCPU);
+  const std::vector<mx_kv_cache_t> caches = layers_of(a[0], "caches", dev);
+  const at::Tensor &refs = tensor(a[1], "refs"), &table = tensor(a[2], "page_table"), &lens = tensor(a[3], "lens");
+  const int64_t rows = vector_size(lens, "lens"), pages = caches[0].pages;
+  check_vector(refs, "refs", at::kInt, pages, dev);
+  check_vector(lens, "lens", at::kInt, rows, dev);
+  check_page_table(table, rows, dev);
+  int64_t children = rows;
+  const int32_t *parents = nullptr, *cu = nullptr;
+  if (a[5] != Py_None) {
+    const at::Tensor& t = tensor(a[5], "parents");
+    TORCH_CHECK_VALUE(t.scalar_type() == at::kInt && t.is_contiguous() && t.device() == dev,
+                      "parents must be a contiguous int32 tensor on the device of the other arguments");
+    children = t.numel();
+    parents = ints(t);
+  }
+  const int64_t tokens = integer(a[7]);
+  TORCH_CHECK_VALUE(tokens >= 0, "tokens must not be negative");
+  if (a[4] != Py_None) {
+    const at::Tensor& t = tensor(a[4], "cu");
+    check_vector(t, "cu", at::kInt, children + 1, dev);
+    cu = ints(t);
+  }
+  const bool release = truth(a[6]);
+  PyObject* out = a[9];
+  check_out_tuple(out, 4);
+  int64_t cols = a[8] == Py_None ? table.size(1) : integer(a[8]);
+  if (out != Py_None && a[8] == Py_None) {
+    const at::Tensor& t = tensor(PyTuple_GET_ITEM(out, 1), "out's page_table");
+    if (t.dim() == 2) cols = t.size(1);
+  }
+  TORCH_CHECK_VALUE(cols >= table.size(1), "the new table must not be narrower than the old one");
+  OnDevice on(dev);
+  int64_t need = 0;
+  check_status(mx_kv_fork_workspace(pages, rows, children, tokens, caches[0].page, &need));
+  const at::TensorOptions like = refs.options();
+  at::Tensor r = out_or_new(out, 0, "out's refs", {pages}, at::kInt, like),
+             t = out_or_new(out, 1, "out's page_table", {children, cols}, at::kInt, like),
+             l = out_or_new(out, 2, "out's lens", {children}, at::kInt, like),
+             s = out_or_new(out, 3, "out's slots", {tokens}, at::kLong, like),
+             space = at::empty({need}, like.dtype(at::kByte));
+  // a parents tensor without elements has no address, which would stand for children that continue their own rows
+  if (a[5] != Py_None && children == 0) parents = ints(refs);
+  check_status(mx_kv_fork(caches.data(), layer_count(caches), ints(refs), ints(table), row_stride(table), table.size(1),
+                          ints(lens), rows, parents, children, cu, tokens, release, ints_out(r), ints_out(t), cols,
+                          ints_out(l), static_cast<int64_t*>(s.data_ptr()), space.data_ptr(), need, on.stream));
+  return wrapped({r, t, l, s});
+  END_HANDLE_TH_ERRORS
+}
+
+// kv_free(refs, page_table, lens, page, keep or None, out or None)
+PyObject* kv_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_args(n, 6);
+  const at::Tensor &refs = tensor(a[0], "refs"), &table = tensor(a[1], "page_table"), &lens = tensor(a[2], "lens");
+  const at::Device dev = refs.device();
+  const int64_t rows = vector_size(lens, "lens"), pages = vector_size(refs, "refs");
+  check_vector(refs, "refs", at::kInt, pages, dev);
+  check_vector(lens, "lens", at::kInt, rows, dev);
+  check_page_table(table, rows, dev);
+  const int32_t* keep = nullptr;
+  if (a[4] != Py_None) {
+    const at::Tensor& t = tensor(a[4], "keep");
+    check_vector(t, "keep", at::kInt, rows, dev);
+    keep = ints(t);
+  }
+  check_out_tuple(a[5], 2);
+  OnDevice on(dev);
+  at::Tensor r = out_or_new(a[5], 0, "out's refs", {pages}, at::kInt, refs.options()),
+             l = out_or_new(a[5], 1, "out's lens", {rows}, at::kInt, refs.options());
+  check_status(mx_kv_free(ints(refs), pages, narrow_int(integer(a[3]), "page"), ints(table), row_stride(table),
+                          table.size(1), ints(lens), rows, keep, ints_out(r), ints_out(l), on.stream));
+  return wrapped({r, l});
+  END_HANDLE_TH_ERRORS
+}
+
+// kv_compact(caches, refs, page_table, lens, out or None)
+PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_args(n, 5);
+  at::Device dev(at::kCPU);
+  const std::vector<mx_kv_cache_t> caches = layers_of(a[0], "caches", dev);
+  const at::Tensor &refs = tensor(a[1], "refs"), &table = tensor(a[2], "page_table"), &lens = tensor(a[3], "lens");
+  const int64_t rows = vector_size(lens, "lens"), pages = caches[0].pages;
+  check_vector(refs, "refs", at::kInt, pages, dev);
+  check_vector(lens, "lens", at::kInt, rows, dev);
+  check_page_table(table, rows, dev);
+  check_out_tuple(a[4], 3);
+  OnDevice on(dev);
+  int64_t need = 0;
+  check_status(mx_kv_compact_workspace(pages, &need));
+  const at::TensorOptions like = refs.options();
+  at::Tensor r = out_or_new(a[4], 0, "out's refs", {pages}, at::kInt, like),
+             t = out_or_new(a[4], 1, "out's page_table", table.sizes(), at::kInt, like),
+             u = out_or_new(a[4], 2, "out's count", {1}, at::kInt, like), space = at::empty({need}, like.dtype(at::kByte));
+  check_status(mx_kv_compact(caches.data(), layer_count(caches), ints(refs), ints(table), row_stride(table), table.size(1),
+                             ints(lens), rows, ints_out(r), ints_out(t), ints_out(u), space.data_ptr(), need, on.stream));
+  return wrapped({r, t, u});
+  END_HANDLE_TH_ERRORS
+}
+
+// beam_select(logits, scores, width or None, finished or None, eos, pad, history or None, lens or None)
+PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  check_args(n, 8);
+  const at::Tensor &x = tensor(a[0], "logits"), &scores = tensor(a[1], "scores");
+  const mx_dtype_t dt = dtype_of(x);
+  const at::Device dev = x.device();
+  TORCH_CHECK_VALUE(x.dim() == 3 && (x.stride(2) == 1 || x.size(2) <= 1),
+                    "logits must be [requests][beams][vocab] with contiguous tokens");
+  const int64_t requests = x.size(0), beams = x.size(1);
+  const int64_t one[2] = {requests, beams};
+  auto check_beams = [&](const at::Tensor& t, const char* name, bool ok) {
+    TORCH_CHECK_VALUE(ok && t.sizes() == at::IntArrayRef(one, 2) && t.is_contiguous() && t.device() == dev, name,
+                      " must be a contiguous tensor [requests][beams] on the device of the other arguments"
+                      " (scores float32, finished bool or uint8, lens int32)");
+  };
+  check_beams(scores, "scores", scores.scalar_type() == at::kFloat);
+  const int64_t width = a[2] == Py_None ? beams : integer(a[2]);
+  const uint8_t* finished = nullptr;
+  if (a[3] != Py_None) {
+    const at::Tensor& t = tensor(a[3], "finished");
+    check_beams(t, "finished", t.scalar_type() == at::kBool || t.scalar_type() == at::kByte);
+    finished = static_cast<const uint8_t*>(t.data_ptr());
+  }
+  const int64_t eos = integer(a[4]), pad = integer(a[5]);
+  const int32_t *history = nullptr, *lens = nullptr;
+  int64_t cols = 0;
+  TORCH_CHECK_VALUE((a[6] == Py_None) == (a[7] == Py_None), "history and lens are given together");
+  if (a[6] != Py_None) {
+    const at::Tensor &h = tensor(a[6], "history"), &l = tensor(a[7], "lens");
+    check_beams(l, "lens", l.scalar_type() == at::kInt);
+    TORCH_CHECK_VALUE(h.scalar_type() == at::kInt && h.dim() == 3 && h.size(0) == requests && h.size(1) == beams &&
+                          h.is_contiguous() && h.device() == dev,
+                      "history must be a contiguous int32 tensor [requests][beams][tokens]");
+    history = ints(h);
+    lens = ints(l);
+    cols = h.size(2);
+  }
+  OnDevice on(dev);
+  int64_t need = 0;
+  check_status(mx_beam_select_workspace(requests, beams, x.size(2), width, &need));
+  const at::TensorOptions like = scores.options(), whole = like.dtype(at::kInt);
+  at::Tensor s = at::empty({requests, width}, like), p = at::empty({requests, width}, whole),
+             t = at::empty({requests, width}, whole), f = at::empty({requests, width}, like.dtype(at::kBool)), h, l,
+             space = at::empty({need}, like.dtype(at::kByte));
+  if (a[6] != Py_None) {
+    h = at::empty({requests, width, cols}, whole);
+    l = at::empty({requests, width}, whole);
+  }
+  check_status(mx_beam_select(x.data_ptr(), dt, requests, beams, x.size(2), stride_of(x, 0), stride_of(x, 1),
+                              static_cast<const float*>(scores.data_ptr()), finished, width, eos, pad, history, lens, cols,
+                              static_cast<float*>(s.data_ptr()), ints_out(p), ints_out(t),
+                              static_cast<uint8_t*>(f.data_ptr()), h.defined() ? ints_out(h) : nullptr,
+                              l.defined() ? ints_out(l) : nullptr, space.data_ptr(), need, on.stream));
+  return wrapped({s, p, t, f, h, l});
+  END_HANDLE_TH_ERRORS
+}
+
 // set_check(callable): what raises for a status
 PyObject* set_check(PyObject*, PyObject* f) {
   Py_INCREF(f);
@@ -306,6 +564,11 @@ PyMethodDef g_methods[] = {fast<rope_table>("rope_table"),
                            fast<rope>("rope"),
                            fast<kv_append>("kv_append"),
                            fast<paged_attention>("paged_attention"),
+                           fast<kv_copy>("kv_copy"),
+                           fast<kv_fork>("kv_fork"),
+                           fast<kv_free>("kv_free"),
+                           fast<kv_compact>("kv_compact"),
+                           fast<beam_select>("beam_select"),
                            {"set_check", set_check, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 

@@ -1,0 +1,875 @@
+// Pages of the paged MXFP8 key/value cache on gfx950: copied, forked, freed and moved together.
+//
+// A pool of pages has a count of holders for every page (0: free).  All plans are made on the
+// device from the counts and the page table: which pages a sequence keeps, which it gets, and
+// what has to be copied.  Pages are dealt by rank (the nth page needed is the nth free one), found
+// by counting in blocks and summing the blocks before, so nothing depends on the order in which
+// workgroups run; atomics are used for counts only, which any order adds up to the same.
+//
+// What bounds them: the copies are bound by memory (one read and one write of each page); the plans
+// read the counts and the tables once, which takes a few microseconds, and so are bound by the
+// chain of launches that their dependent steps need.
+
+#include "mx_launch.hpp"
+
+#include <algorithm>
+
+namespace mxk {
+
+constexpr int kLayersPerLaunch = 32;        // 4 pointers each: 1 KiB of a launch's arguments
+constexpr int kPartGranules = 256;          // 16-byte granules that a wave copies at once: four a lane
+constexpr int kPerThread = 16;              // counts that a thread of a counting block reads
+constexpr int kCountBlock = 256 * kPerThread;
+constexpr int kMostCountBlocks = 4096;      // every block sums the blocks before it: 16 loads a thread
+
+struct Layers {
+  uint8_t* p[kLayersPerLaunch][4];          // k, k_scales, v, v_scales
+};
+
+typedef uint32_t Granule __attribute__((ext_vector_type(4)));
+
+struct PageShape {
+  int kv_heads, page, dim;
+};
+
+// n / d for quotients below 2^51, with inv = 1.0 / d: the product is off by less than one, which one step mends.
+__device__ __forceinline__ int64_t divide(int64_t n, int64_t d, double inv, int64_t& rest) {
+  int64_t q = int64_t(double(n) * inv);
+  rest = n - q * d;
+  if (rest < 0) { --q; rest += d; }
+  if (rest >= d) { ++q; rest -= d; }
+  return q;
+}
+
+// ---------------------------------------------------------------------------
+// Copies
+// ---------------------------------------------------------------------------
+// A wave copies part `part` of the first `tokens` tokens (a multiple of 16) of page src to page dst: 4 KiB of the
+// keys, the values, the key scales and the value scales in a row.  Four loads of 16 bytes a lane are in flight
+// before the first store.  A whole page is one run of bytes in each array; of a part of one, each head is a run.
+__device__ __forceinline__ void copy_part(uint8_t* const (&from)[4], uint8_t* const (&to)[4], const PageShape& s,
+                                          int64_t src, int64_t dst, int tokens, uint32_t part) {
+  const bool whole = tokens == s.page;
+  const uint32_t heads = whole ? 1u : uint32_t(s.kv_heads);
+  const uint32_t head_codes = (whole ? uint32_t(s.kv_heads) * uint32_t(s.page) : uint32_t(tokens)) * uint32_t(s.dim) / 16u;
+  const uint32_t head_scales = head_codes / 32u, codes = heads * head_codes, scales = heads * head_scales;
+  const int64_t page_codes = int64_t(s.kv_heads) * s.page * s.dim;
+  const uint32_t lane = threadIdx.x & 63u;
+  Granule v[4];
+  uint8_t* at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t g = part * kPartGranules + i * 64 + lane;
+    const bool is_scale = g >= 2u * codes;
+    uint32_t o = is_scale ? g - 2u * codes : g;
+    const uint32_t n = is_scale ? scales : codes, run = is_scale ? head_scales : head_codes;
+    const bool is_value = o >= n;
+    o -= is_value ? n : 0u;
+    const int64_t page_bytes = is_scale ? page_codes / 32 : page_codes;
+    int64_t off = int64_t(o) * 16;
+    if (!whole) {
+      const uint32_t head = o / run;
+      off = int64_t(head) * (int64_t(s.page) * s.dim / (is_scale ? 32 : 1)) + int64_t(o - head * run) * 16;
+    }
+    const uint8_t* f = is_scale ? (is_value ? from[3] : from[1]) : (is_value ? from[2] : from[0]);
+    uint8_t* t = is_scale ? (is_value ? to[3] : to[1]) : (is_value ? to[2] : to[0]);
+    const bool real = g < 2u * (codes + scales);
+    v[i] = Granule{};
+    if (real) v[i] = *reinterpret_cast<const Granule*>(f + src * page_bytes + off);
+    at[i] = real ? t + dst * page_bytes + off : nullptr;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (at[i]) *reinterpret_cast<Granule*>(at[i]) = v[i];
+}
+
+struct Item {
+  int64_t copy;
+  int layer;
+  uint32_t part;
+};
+
+// Items of work of a launch: (copy, layer, part), the parts of a page in a row.
+struct Items {
+  int layers, parts;
+  double inv_layers, inv_parts;
+  __device__ __forceinline__ Item at(int64_t i) const {
+    int64_t part, layer;
+    const int64_t unit = divide(i, parts, inv_parts, part);
+    const int64_t copy = divide(unit, layers, inv_layers, layer);
+    return {copy, int(layer), uint32_t(part)};
+  }
+};
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+struct CopyArgs {
+  Layers from, to;
+  const int32_t *src, *dst;
+  int64_t count, src_pages, dst_pages;
+  PageShape shape;
+  Items items;
+};
+
+__global__ __launch_bounds__(256) void page_copy_kernel(const CopyArgs g) {
+  const int64_t waves = int64_t(gridDim.x) * 4;
+  const int64_t total = g.count * g.items.layers * g.items.parts;
+  for (int64_t i = int64_t(blockIdx.x) * 4 + uniform(threadIdx.x >> 6); i < total; i += waves) {
+    const Item it = g.items.at(i);
+    const int32_t src = g.src[it.copy], dst = g.dst[it.copy];
+    if (src < 0 || src >= g.src_pages || dst < 0 || dst >= g.dst_pages) continue;
+    const int layer = uniform(it.layer);
+    copy_part(g.from.p[layer], g.to.p[layer], g.shape, src, dst, g.shape.page, it.part);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Sums over a workgroup of 256 threads
+// ---------------------------------------------------------------------------
+template <class T>
+__device__ __forceinline__ T wave_scan(T x) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const T y = __shfl_up(x, d);
+    if (int(threadIdx.x & 63u) >= d) x += y;
+  }
+  return x;
+}
+
+// Sum of x over the threads before this one, and over all of them.
+template <class T>
+__device__ __forceinline__ T block_scan(T x, T& total) {
+  __shared__ T part[4];
+  const T mine = wave_scan(x);
+  const int w = threadIdx.x >> 6;
+  __syncthreads();                          // the last call's sums are read
+  if ((threadIdx.x & 63u) == 63u) part[w] = mine;
+  __syncthreads();
+  T before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < w) before += part[i];
+    total += part[i];
+  }
+  return before + mine - x;
+}
+
+// Sum of the first `before` and of all `count` entries.
+template <class T, class U>
+__device__ __forceinline__ T sum_before(const U* a, int count, int before, T& total) {
+  T x = 0, y = 0;
+  for (int i = threadIdx.x; i < count; i += 256) {
+    const T v = T(a[i]);
+    y += v;
+    if (i < before) x += v;
+  }
+  T sum;
+  block_scan(x, sum);
+  block_scan(y, total);
+  return sum;
+}
+
+// Counting blocks: block b has the pages [b, b + 1) * per_block.
+struct Blocks {
+  int64_t pages, per_block;                 // per_block a multiple of kCountBlock
+  int count;
+};
+
+// Calls f(page, ref) for this thread's pages of block b, 16 consecutive ones of each 4096.
+template <class F>
+__device__ __forceinline__ void each_run(const Blocks& k, const int32_t* refs, int b, F f) {
+  for (int64_t at = int64_t(b) * k.per_block; at < std::min(k.pages, int64_t(b + 1) * k.per_block); at += kCountBlock) {
+    const int64_t p = at + threadIdx.x * kPerThread;
+    int32_t r[kPerThread];
+    if (p + kPerThread <= k.pages) {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) r[i] = refs[p + i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) r[i] = p + i < k.pages ? refs[p + i] : 0;
+    }
+    f(p, r);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Forking
+// ---------------------------------------------------------------------------
+struct ForkArgs {
+  Layers caches;
+  const int32_t *refs, *table, *lens, *parents, *cu;
+  int32_t *refs_out, *table_out, *lens_out;
+  int64_t* slots;
+  int64_t pages, stride, rows, children, tokens, capacity;
+  int cols, out_cols, release;
+  PageShape shape;
+  Items items;
+  Blocks blocks;
+  int child_blocks;
+  // workspace
+  int64_t *start, *child_sum;               // first new page of a child (-1: it gets none); pages that a block of children needs
+  int32_t *kids, *writers, *first;          // of each row: children, those that write into its last page, the first of these
+  int32_t *info;                            // of each child: 2 * new pages + whether the first is a copy; -1: too many for a row
+  int32_t *child_copies, *block_free, *list, *copies;
+  int4* copy;                               // source page (-1: none), place of the new page in the list, tokens
+};
+
+struct Child {
+  int64_t row;                              // -1: starts empty
+  int had, fresh, from;                     // cached tokens, new tokens, the first one's number
+  int held, partly;                         // pages, and tokens in the last one if it is partly filled
+};
+
+__device__ __forceinline__ int row_length(const ForkArgs& g, int64_t row) {
+  return min(max(g.lens[row], 0), g.cols * g.shape.page);
+}
+
+__device__ __forceinline__ Child child_of(const ForkArgs& g, int64_t i) {
+  Child c;
+  c.row = g.parents ? int64_t(g.parents[i]) : i;
+  if (c.row < 0 || c.row >= g.rows) c.row = -1;
+  c.had = c.row < 0 ? 0 : row_length(g, c.row);
+  c.from = c.fresh = 0;
+  if (g.cu) {
+    const int64_t lo = min(max(int64_t(g.cu[i]), int64_t(0)), g.tokens);
+    const int64_t hi = min(max(int64_t(g.cu[i + 1]), lo), g.tokens);
+    c.from = int(lo);
+    c.fresh = int(hi - lo);
+  }
+  c.held = (c.had + g.shape.page - 1) / g.shape.page;
+  c.partly = c.had % g.shape.page;
+  return c;
+}
+
+__device__ __forceinline__ bool in_pool(const ForkArgs& g, int32_t page) { return page >= 0 && page < g.pages; }
+
+__global__ __launch_bounds__(256) void fork_init_kernel(const ForkArgs g) {
+  const int64_t step = int64_t(gridDim.x) * 256;
+  const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (g.refs_out != g.refs)
+    for (int64_t i = at; i < g.pages; i += step) g.refs_out[i] = g.refs[i];
+  for (int64_t i = at; i < g.rows; i += step) {
+    g.kids[i] = g.writers[i] = 0;
+    g.first[i] = INT32_MAX;
+  }
+}
+
+__global__ __launch_bounds__(256) void fork_kids_kernel(const ForkArgs g) {
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= g.children) return;
+  const Child c = child_of(g, i);
+  if (c.row < 0) return;
+  atomicAdd(&g.kids[c.row], 1);
+  if (c.fresh && c.partly) {
+    atomicAdd(&g.writers[c.row], 1);
+    atomicMin(&g.first[c.row], int32_t(i));
+  }
+}
+
+// Every page of a row gains the row's children and loses the row itself if it is released.
+__global__ __launch_bounds__(256) void fork_counts_kernel(const ForkArgs g) {
+  for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
+    const int d = g.kids[row] - g.release;
+    if (d == 0) continue;
+    const int held = (row_length(g, row) + g.shape.page - 1) / g.shape.page;
+    for (int j = blockIdx.y * 256 + threadIdx.x; j < held; j += gridDim.y * 256) {
+      const int32_t page = g.table[row * g.stride + j];
+      if (in_pool(g, page)) atomicAdd(&g.refs_out[page], d);
+    }
+  }
+}
+
+// Blocks of children: the pages that each needs; blocks of pages: how many are free.
+__global__ __launch_bounds__(256) void fork_needs_kernel(const ForkArgs g) {
+  if (int(blockIdx.x) >= g.child_blocks) {
+    const int b = blockIdx.x - g.child_blocks;
+    int n = 0;
+    // without parents and with the rows released the counts stay, and are copied here
+    const bool copy = !g.parents && g.release && g.refs_out != g.refs;
+    each_run(g.blocks, copy ? g.refs : g.refs_out, b, [&](int64_t p, const int32_t(&r)[kPerThread]) {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i)
+        if (p + i < g.pages) {
+          n += r[i] == 0;
+          if (copy) g.refs_out[p + i] = r[i];
+        }
+    });
+    int total;
+    block_scan(n, total);
+    if (threadIdx.x == 0) g.block_free[b] = total;
+    return;
+  }
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  int need = 0, info = 0;
+  bool copy = false;
+  if (i < g.children) {
+    const Child c = child_of(g, i);
+    const int64_t after = (int64_t(c.had) + c.fresh + g.shape.page - 1) / g.shape.page;
+    if (c.fresh && c.partly) {
+      const int32_t tail = g.table[c.row * g.stride + c.held - 1];
+      if (in_pool(g, tail)) {
+        const bool alone = !g.parents && g.release;
+        const int32_t count = (alone ? g.refs : g.refs_out)[tail];
+        const int32_t writers = alone ? 1 : g.writers[c.row];
+        copy = !(count == writers && (alone || g.first[c.row] == i));
+      }
+    }
+    need = int(after) - c.held + copy;
+    info = 2 * need + copy;
+    if (after > g.out_cols) need = 0, info = -1, copy = false;
+    g.info[i] = info;
+  }
+  int64_t total;
+  const int64_t before = block_scan(int64_t(need), total);
+  int copies;
+  block_scan(int(copy), copies);
+  if (i < g.children) g.start[i] = before;
+  if (threadIdx.x == 0) {
+    g.child_sum[blockIdx.x] = total;
+    g.child_copies[blockIdx.x] = copies;
+  }
+}
+
+// Blocks of children: where each one's new pages begin in the list, or that there are too few, and the copies;
+// blocks of pages: the free ones into the list, as many as can be needed.
+__global__ __launch_bounds__(256) void fork_list_kernel(const ForkArgs g) {
+  if (int(blockIdx.x) >= g.child_blocks) {
+    const int b = blockIdx.x - g.child_blocks;
+    int64_t all, rank = sum_before<int64_t>(g.block_free, g.blocks.count, b, all);
+    if (rank >= g.capacity) return;
+    each_run(g.blocks, g.refs_out, b, [&](int64_t p, const int32_t(&r)[kPerThread]) {
+      int n = 0, total;
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) n += p + i < g.pages && r[i] == 0;
+      int64_t at = rank + block_scan(n, total);
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i)
+        if (p + i < g.pages && r[i] == 0) {
+          if (at < g.capacity) g.list[at] = int32_t(p + i);
+          ++at;
+        }
+      rank += total;
+    });
+    return;
+  }
+  int64_t all_free, all_needed;
+  sum_before<int64_t>(g.block_free, g.blocks.count, 0, all_free);
+  const int64_t base = sum_before<int64_t>(g.child_sum, g.child_blocks, blockIdx.x, all_needed);
+  int all_copies;
+  const int copies = sum_before<int>(g.child_copies, g.child_blocks, blockIdx.x, all_copies);
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int info = i < g.children ? g.info[i] : 0;
+  const bool copy = info > 0 && (info & 1);
+  int total;
+  const int nth = copies + block_scan(int(copy), total);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *g.copies = all_copies;
+  if (i >= g.children) return;
+  const Child c = child_of(g, i);
+  const int64_t start = base + g.start[i];
+  const int need = info >> 1;
+  const bool fits = c.fresh && info >= 0 && (need == 0 || start + need <= min(all_free, g.capacity));
+  g.start[i] = fits ? start : -1;
+  if (copy) {
+    const int32_t tail = g.table[c.row * g.stride + c.held - 1];
+    g.copy[nth] = make_int4(fits ? tail : -1, fits ? int(start) : 0, (c.partly + 15) / 16 * 16, 0);
+  }
+}
+
+// A workgroup for each child writes its row of the table, its slots and the counts of its pages; the workgroups
+// behind them copy the partly filled pages, 4 KiB a wave at a time.
+__global__ __launch_bounds__(256) void fork_rows_kernel(const ForkArgs g) {
+  if (int64_t(blockIdx.x) >= g.children) {
+    const int64_t waves = (int64_t(gridDim.x) - g.children) * 4;
+    const int64_t total = int64_t(*g.copies) * g.items.layers * g.items.parts;
+    for (int64_t i = (int64_t(blockIdx.x) - g.children) * 4 + uniform(threadIdx.x >> 6); i < total; i += waves) {
+      const Item it = g.items.at(i);
+      const int4 c = g.copy[it.copy];
+      if (c.x < 0) continue;
+      const int layer = uniform(it.layer);
+      copy_part(g.caches.p[layer], g.caches.p[layer], g.shape, c.x, g.list[c.y], uniform(c.z), it.part);
+    }
+    return;
+  }
+  const int64_t i = blockIdx.x;
+  if (i == 0 && g.tokens) {                 // tokens before the first child and behind the last are padding
+    const int64_t lo = g.cu ? min(max(int64_t(g.cu[0]), int64_t(0)), g.tokens) : g.tokens;
+    const int64_t hi = g.cu ? min(max(int64_t(g.cu[g.children]), int64_t(0)), g.tokens) : g.tokens;
+    for (int64_t t = threadIdx.x; t < lo; t += 256) g.slots[t] = -1;
+    for (int64_t t = hi + threadIdx.x; t < g.tokens; t += 256) g.slots[t] = -1;
+  }
+  const Child c = child_of(g, i);
+  const int64_t start = g.start[i];
+  const bool fits = start >= 0;
+  const int copy = fits ? g.info[i] & 1 : 0;
+  const int after = fits ? int((int64_t(c.had) + c.fresh + g.shape.page - 1) / g.shape.page) : c.held;
+  const int32_t* row = g.table + c.row * g.stride;        // read up to held, which is 0 without a row
+  const int kept = c.held - copy;                          // pages that stay
+  int32_t* out = g.table_out + i * g.out_cols;
+  for (int j = threadIdx.x; j < g.out_cols; j += 256) {
+    int32_t page = -1;
+    if (j < kept) {
+      page = row[j];
+    } else if (j < after) {
+      page = g.list[start + j - kept];
+      g.refs_out[page] = 1;
+    }
+    out[j] = page;
+  }
+  if (threadIdx.x == 0) {
+    g.lens_out[i] = c.had + (fits ? c.fresh : 0);
+    if (copy) atomicSub(&g.refs_out[row[c.held - 1]], 1);
+  }
+  for (int t = threadIdx.x; t < c.fresh; t += 256) {
+    int64_t slot = -1;
+    if (fits) {
+      const int at = c.had + t, j = at / g.shape.page;
+      const int32_t page = j < kept ? row[j] : g.list[start + j - kept];
+      if (in_pool(g, page)) slot = int64_t(page) * g.shape.page + at % g.shape.page;
+    }
+    g.slots[c.from + t] = slot;
+  }
+}
+
+// Copies of further layers than those of one launch.
+__global__ __launch_bounds__(256) void fork_copy_kernel(const ForkArgs g) {
+  const int64_t waves = int64_t(gridDim.x) * 4;
+  const int64_t total = int64_t(*g.copies) * g.items.layers * g.items.parts;
+  for (int64_t i = int64_t(blockIdx.x) * 4 + uniform(threadIdx.x >> 6); i < total; i += waves) {
+    const Item it = g.items.at(i);
+    const int4 c = g.copy[it.copy];
+    if (c.x < 0) continue;
+    const int layer = uniform(it.layer);
+    copy_part(g.caches.p[layer], g.caches.p[layer], g.shape, c.x, g.list[c.y], uniform(c.z), it.part);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Freeing
+// ---------------------------------------------------------------------------
+struct FreeArgs {
+  const int32_t *refs, *table, *lens, *keep;
+  int32_t *refs_out, *lens_out;
+  int64_t pages, stride, rows;
+  int cols, page;
+};
+
+__global__ __launch_bounds__(256) void refs_copy_kernel(const int32_t* from, int32_t* to, int64_t n) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256) to[i] = from[i];
+}
+
+__device__ __forceinline__ int kept_tokens(const FreeArgs& g, int64_t row, int had) {
+  return min(had, g.keep ? max(g.keep[row], 0) : 0);
+}
+
+__global__ __launch_bounds__(256) void free_pages_kernel(const FreeArgs g) {
+  for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
+    const int had = min(max(g.lens[row], 0), g.cols * g.page), left = kept_tokens(g, row, had);
+    const int end = (had + g.page - 1) / g.page;
+    for (int j = (left + g.page - 1) / g.page + blockIdx.y * 256 + threadIdx.x; j < end; j += gridDim.y * 256) {
+      const int32_t page = g.table[row * g.stride + j];
+      if (page >= 0 && page < g.pages) atomicSub(&g.refs_out[page], 1);
+    }
+    if (g.lens_out != g.lens && blockIdx.y == 0 && threadIdx.x == 0) g.lens_out[row] = left;
+  }
+}
+
+// Lengths changed in place change after every workgroup has read them.
+__global__ __launch_bounds__(256) void free_lens_kernel(const FreeArgs g) {
+  const int64_t row = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (row < g.rows) g.lens_out[row] = kept_tokens(g, row, min(max(g.lens[row], 0), g.cols * g.page));
+}
+
+// ---------------------------------------------------------------------------
+// Moving pages together
+// ---------------------------------------------------------------------------
+// With U pages in use, those at or above U move into the free ones below: the nth free page takes the nth used one
+// from the top.  A page p has n used ones before it, so a free one is number p - n of the free, and a used one is
+// number U - 1 - n from the top; both follow from one running count, and no source is a target.
+struct CompactArgs {
+  Layers caches;
+  const int32_t *refs, *table, *lens;
+  int32_t *refs_out, *table_out, *used;
+  int64_t pages, stride, rows;
+  int cols;
+  PageShape shape;
+  Items items;
+  Blocks blocks;
+  int64_t table_blocks;
+  // workspace
+  int32_t *block_used, *hole, *mover, *mover_refs, *nth, *moves;
+};
+
+__global__ __launch_bounds__(256) void compact_count_kernel(const CompactArgs g) {
+  int n = 0, total;
+  each_run(g.blocks, g.refs, blockIdx.x, [&](int64_t, const int32_t(&r)[kPerThread]) {
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) n += r[i] != 0;
+  });
+  block_scan(n, total);
+  if (threadIdx.x == 0) g.block_used[blockIdx.x] = total;
+}
+
+__global__ __launch_bounds__(256) void compact_plan_kernel(const CompactArgs g) {
+  int64_t used, before = sum_before<int64_t>(g.block_used, g.blocks.count, blockIdx.x, used);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *g.used = int32_t(used);
+    if (used == 0) *g.moves = 0;
+  }
+  each_run(g.blocks, g.refs, blockIdx.x, [&](int64_t p, const int32_t(&r)[kPerThread]) {
+    int n = 0, total;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) n += r[i] != 0;
+    int64_t u = before + block_scan(n, total);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int64_t page = p + i;
+      if (page < g.pages) {
+        const bool live = r[i] != 0;
+        if (page < used) {
+          if (!live) g.hole[page - u] = int32_t(page);
+          else g.refs_out[page] = r[i];                    // a hole's count comes with its page
+        } else {
+          g.nth[page] = live ? int32_t(used - 1 - u) : -1;
+          if (live) {
+            g.mover[used - 1 - u] = int32_t(page);
+            g.mover_refs[used - 1 - u] = r[i];
+          }
+          g.refs_out[page] = 0;
+        }
+        if (page == used - 1) *g.moves = int32_t(used - u - live);
+        u += live;
+      }
+    }
+    before += total;
+  });
+}
+
+__global__ __launch_bounds__(256) void compact_move_kernel(const CompactArgs g) {
+  const int64_t moves = *g.moves, used = *g.used;
+  if (int64_t(blockIdx.x) < g.table_blocks) {
+    const int64_t step = g.table_blocks * 256, at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    for (int64_t i = at; i < moves; i += step) g.refs_out[g.hole[i]] = g.mover_refs[i];
+    for (int64_t row = blockIdx.x; row < g.rows; row += g.table_blocks) {
+      const int held = (min(max(g.lens[row], 0), g.cols * g.shape.page) + g.shape.page - 1) / g.shape.page;
+      for (int j = threadIdx.x; j < g.cols; j += 256) {
+        int32_t page = g.table[row * g.stride + j];
+        if (j < held && page >= used && page < g.pages) {
+          const int32_t n = g.nth[page];
+          if (n >= 0) page = g.hole[n];
+        }
+        g.table_out[row * g.cols + j] = page;
+      }
+    }
+    return;
+  }
+  const int64_t waves = (int64_t(gridDim.x) - g.table_blocks) * 4;
+  const int64_t total = moves * g.items.layers * g.items.parts;
+  for (int64_t i = (int64_t(blockIdx.x) - g.table_blocks) * 4 + uniform(threadIdx.x >> 6); i < total; i += waves) {
+    const Item it = g.items.at(i);
+    const int layer = uniform(it.layer);
+    copy_part(g.caches.p[layer], g.caches.p[layer], g.shape, g.mover[it.copy], g.hole[it.copy], g.shape.page, it.part);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+inline mx_status_t launched() { return hipGetLastError() == hipSuccess ? MX_OK : MX_ERR_LAUNCH; }
+
+inline bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+inline bool off8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) != 0; }
+
+// Caches of all layers: alike, with all their pointers, pages of at most 2^30 bytes of codes.
+mx_status_t check_layers(const mx_kv_cache_t* c, int layers) {
+  if (layers < 1 || layers > 65536) return MX_ERR_SHAPE;
+  if (!c) return MX_ERR_NULL;
+  for (int l = 0; l < layers; ++l) {
+    const mx_status_t st = check_kv_cache(c[l]);
+    if (st != MX_OK) return st;
+    if (c[l].pages != c[0].pages || c[l].kv_heads != c[0].kv_heads || c[l].page != c[0].page || c[l].dim != c[0].dim)
+      return MX_ERR_SHAPE;
+  }
+  if (int64_t(c->kv_heads) * c->page > (int64_t(1) << 30) / c->dim) return MX_ERR_SHAPE;
+  if (c->pages > INT32_MAX) return MX_ERR_SHAPE;
+  if (c->pages == 0) return MX_OK;
+  for (int l = 0; l < layers; ++l) {
+    if (!c[l].k || !c[l].k_scales || !c[l].v || !c[l].v_scales) return MX_ERR_NULL;
+    if (misaligned(c[l].k) || misaligned(c[l].k_scales) || misaligned(c[l].v) || misaligned(c[l].v_scales))
+      return MX_ERR_ALIGN;
+  }
+  return MX_OK;
+}
+
+PageShape shape_of(const mx_kv_cache_t& c) { return {c.kv_heads, c.page, c.dim}; }
+
+void fill_layers(Layers& to, const mx_kv_cache_t* c, int n) {
+  for (int l = 0; l < n; ++l) {
+    uint8_t* p[4] = {c[l].k, c[l].k_scales, c[l].v, c[l].v_scales};
+    std::copy(p, p + 4, to.p[l]);
+  }
+}
+
+// 4 KiB parts of a page, the last one short.
+Items items_of(const mx_kv_cache_t& c, int layers) {
+  const int64_t codes = int64_t(c.kv_heads) * c.page * c.dim / 16;
+  Items it;
+  it.layers = layers;
+  it.parts = int((2 * (codes + codes / 32) + kPartGranules - 1) / kPartGranules);
+  it.inv_layers = 1.0 / it.layers;
+  it.inv_parts = 1.0 / it.parts;
+  return it;
+}
+
+// Workgroups of four waves for `copies` copies: at most eight for each CU, which walk the work.
+unsigned copy_grid(int64_t copies, const Items& it) {
+  const int64_t cus = std::max<int64_t>(device_cus(), 1);
+  const double waves = double(copies) * it.layers * it.parts;
+  return unsigned(std::max(1.0, std::min(double(8 * cus), std::ceil(waves / 4.0))));
+}
+
+Blocks blocks_of(int64_t pages) {
+  Blocks b;
+  b.pages = pages;
+  const int64_t runs = (pages + kCountBlock - 1) / kCountBlock;
+  b.per_block = std::max<int64_t>(1, (runs + kMostCountBlocks - 1) / kMostCountBlocks) * kCountBlock;
+  b.count = int((pages + b.per_block - 1) / b.per_block);
+  return b;
+}
+
+// Hands out parts of a workspace, each on a 16-byte border.
+struct Space {
+  uint8_t* base;
+  int64_t used = 0;
+  template <class T>
+  T* take(int64_t n) {
+    T* p = reinterpret_cast<T*>(base + used);
+    used += (n * int64_t(sizeof(T)) + 15) / 16 * 16;
+    return p;
+  }
+};
+
+constexpr int64_t kMostRows = int64_t(1) << 20;
+
+// Pages that all children together can need: a copy and a started page each, and one a page's worth of new tokens.
+int64_t fork_capacity(int64_t pages, int64_t children, int64_t tokens, int page) {
+  return std::min(pages, 2 * children + tokens / page);
+}
+
+int64_t fork_space(ForkArgs& g, uint8_t* base) {
+  Space s{base};
+  g.start = s.take<int64_t>(g.children);
+  g.child_sum = s.take<int64_t>(g.child_blocks);
+  g.copy = s.take<int4>(g.children);
+  g.kids = s.take<int32_t>(g.rows);
+  g.writers = s.take<int32_t>(g.rows);
+  g.first = s.take<int32_t>(g.rows);
+  g.info = s.take<int32_t>(g.children);
+  g.child_copies = s.take<int32_t>(g.child_blocks);
+  g.block_free = s.take<int32_t>(g.blocks.count);
+  g.list = s.take<int32_t>(g.capacity);
+  g.copies = s.take<int32_t>(1);
+  return s.used;
+}
+
+mx_status_t fork_sizes(ForkArgs& g, int64_t pages, int64_t rows, int64_t children, int64_t tokens, int page) {
+  if (pages < 0 || pages > INT32_MAX || rows < 0 || rows > kMostRows || children < 0 || children > kMostRows || tokens < 0 ||
+      tokens > INT32_MAX || page < 16 || page > 65536 || page % 16)
+    return MX_ERR_SHAPE;
+  g.pages = pages;
+  g.rows = rows;
+  g.children = children;
+  g.tokens = tokens;
+  g.blocks = blocks_of(pages);
+  g.child_blocks = int((children + 255) / 256);
+  g.capacity = fork_capacity(pages, children, tokens, page);
+  return MX_OK;
+}
+
+int64_t compact_space(CompactArgs& g, uint8_t* base) {
+  Space s{base};
+  g.block_used = s.take<int32_t>(g.blocks.count);
+  g.hole = s.take<int32_t>(g.pages / 2);
+  g.mover = s.take<int32_t>(g.pages / 2);
+  g.mover_refs = s.take<int32_t>(g.pages / 2);
+  g.nth = s.take<int32_t>(g.pages);
+  g.moves = s.take<int32_t>(1);
+  return s.used;
+}
+
+}  // namespace mxk
+
+using namespace mxk;
+
+extern "C" mx_status_t mx_kv_copy(const mx_kv_cache_t* src, const mx_kv_cache_t* dst, int layers,
+                                  const int32_t* src_pages, const int32_t* dst_pages, int64_t count,
+                                  hipStream_t stream) {
+  mx_status_t st = check_layers(src, layers);
+  if (st != MX_OK) return st;
+  st = check_layers(dst, layers);
+  if (st != MX_OK) return st;
+  if (src->kv_heads != dst->kv_heads || src->page != dst->page || src->dim != dst->dim) return MX_ERR_SHAPE;
+  if (count < 0 || count > INT32_MAX) return MX_ERR_SHAPE;
+  if (count == 0 || src->pages == 0 || dst->pages == 0) return MX_OK;
+  if (!src_pages || !dst_pages) return MX_ERR_NULL;
+  if (off4(src_pages) || off4(dst_pages)) return MX_ERR_ALIGN;
+  for (int l = 0; l < layers; l += kLayersPerLaunch) {
+    const int n = std::min(kLayersPerLaunch, layers - l);
+    CopyArgs g = {};
+    fill_layers(g.from, src + l, n);
+    fill_layers(g.to, dst + l, n);
+    g.src = src_pages;
+    g.dst = dst_pages;
+    g.count = count;
+    g.src_pages = src->pages;
+    g.dst_pages = dst->pages;
+    g.shape = shape_of(*src);
+    g.items = items_of(*src, n);
+    page_copy_kernel<<<copy_grid(count, g.items), 256, 0, stream>>>(g);
+  }
+  return launched();
+}
+
+extern "C" mx_status_t mx_kv_fork_workspace(int64_t pages, int64_t rows, int64_t children, int64_t tokens, int page,
+                                            int64_t* bytes) {
+  if (!bytes) return MX_ERR_NULL;
+  ForkArgs g = {};
+  const mx_status_t st = fork_sizes(g, pages, rows, children, tokens, page);
+  if (st != MX_OK) return st;
+  *bytes = fork_space(g, nullptr);
+  return MX_OK;
+}
+
+extern "C" mx_status_t mx_kv_fork(const mx_kv_cache_t* caches, int layers, const int32_t* refs,
+                                  const int32_t* page_table, int64_t table_stride, int64_t table_cols,
+                                  const int32_t* lens, int64_t rows, const int32_t* parents, int64_t children,
+                                  const int32_t* cu, int64_t tokens, int release, int32_t* refs_out,
+                                  int32_t* table_out, int64_t out_cols, int32_t* lens_out, int64_t* slots,
+                                  void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  mx_status_t st = check_layers(caches, layers);
+  if (st != MX_OK) return st;
+  ForkArgs g = {};
+  const int page = caches->page;
+  st = fork_sizes(g, caches->pages, rows, children, tokens, page);
+  if (st != MX_OK) return st;
+  if (table_cols < 0 || out_cols < table_cols || out_cols > INT32_MAX / page || (table_stride < table_cols && rows > 1))
+    return MX_ERR_SHAPE;
+  if (!parents && children != rows) return MX_ERR_SHAPE;
+  if (!cu && tokens) return MX_ERR_NULL;
+  if (g.pages && (!refs || !refs_out)) return MX_ERR_NULL;
+  if (rows && (!lens || (table_cols && !page_table))) return MX_ERR_NULL;
+  if (children && (!lens_out || (out_cols && !table_out))) return MX_ERR_NULL;
+  if (tokens && !slots) return MX_ERR_NULL;
+  if (off4(refs) || off4(refs_out) || off4(lens) || off4(lens_out) || off4(page_table) || off4(table_out) ||
+      off4(parents) || off4(cu) || off8(slots))
+    return MX_ERR_ALIGN;
+  if (children && ((table_out && table_out == page_table) || lens_out == lens)) return MX_ERR_ARG;
+  const int64_t need = fork_space(g, nullptr);
+  if (workspace_bytes < need) return MX_ERR_SHAPE;
+  if (!workspace) return MX_ERR_NULL;
+  if (misaligned(workspace)) return MX_ERR_ALIGN;
+  fork_space(g, static_cast<uint8_t*>(workspace));
+  g.refs = refs; g.table = page_table; g.lens = lens; g.parents = parents; g.cu = cu;
+  g.refs_out = refs_out; g.table_out = table_out; g.lens_out = lens_out; g.slots = slots;
+  g.stride = table_stride;
+  g.cols = int(table_cols); g.out_cols = int(out_cols); g.release = release != 0;
+  g.shape = shape_of(*caches);
+  const int64_t cus = std::max<int64_t>(device_cus(), 1);
+  if (parents || !release) {
+    const int64_t n = std::max(rows, refs_out != refs ? g.pages : 0);
+    if (n) fork_init_kernel<<<unsigned(std::min(8 * cus, (n + 255) / 256)), 256, 0, stream>>>(g);
+    if (children) fork_kids_kernel<<<unsigned(g.child_blocks), 256, 0, stream>>>(g);
+    if (rows && table_cols) {
+      // a workgroup a row, several where there are few rows
+      const int64_t x = std::min(rows, 8 * cus), y = std::min((table_cols + 255) / 256, std::max<int64_t>(1, 8 * cus / x));
+      fork_counts_kernel<<<dim3(unsigned(x), unsigned(y)), 256, 0, stream>>>(g);
+    }
+  }
+  const unsigned both = unsigned(g.child_blocks + g.blocks.count);
+  if (both) fork_needs_kernel<<<both, 256, 0, stream>>>(g);
+  if (children == 0) return launched();
+  fork_list_kernel<<<both, 256, 0, stream>>>(g);
+  for (int l = 0; l < layers; l += kLayersPerLaunch) {
+    const int n = std::min(kLayersPerLaunch, layers - l);
+    fill_layers(g.caches, caches + l, n);
+    g.items = items_of(*caches, n);
+    const unsigned copiers = tokens && g.pages ? copy_grid(children, g.items) : 0;
+    if (l == 0) fork_rows_kernel<<<unsigned(children) + copiers, 256, 0, stream>>>(g);
+    else if (copiers) fork_copy_kernel<<<copiers, 256, 0, stream>>>(g);
+  }
+  return launched();
+}
+
+extern "C" mx_status_t mx_kv_free(const int32_t* refs, int64_t pages, int page, const int32_t* page_table,
+                                  int64_t table_stride, int64_t table_cols, const int32_t* lens, int64_t rows,
+                                  const int32_t* keep, int32_t* refs_out, int32_t* lens_out, hipStream_t stream) {
+  if (pages < 0 || pages > INT32_MAX || rows < 0 || rows > kMostRows || page < 16 || page > 65536 || page % 16)
+    return MX_ERR_SHAPE;
+  if (table_cols < 0 || table_cols > INT32_MAX / page || (table_stride < table_cols && rows > 1)) return MX_ERR_SHAPE;
+  if (pages && (!refs || !refs_out)) return MX_ERR_NULL;
+  if (rows && (!lens || !lens_out || (table_cols && !page_table))) return MX_ERR_NULL;
+  if (off4(refs) || off4(refs_out) || off4(lens) || off4(lens_out) || off4(page_table) || off4(keep)) return MX_ERR_ALIGN;
+  if (rows == 0 && (pages == 0 || refs_out == refs)) return MX_OK;
+  FreeArgs g = {refs, page_table, lens, keep, refs_out, lens_out, pages, table_stride, rows, int(table_cols), page};
+  const int64_t cus = std::max<int64_t>(device_cus(), 1);
+  if (refs_out != refs && pages)
+    refs_copy_kernel<<<unsigned(std::min(8 * cus, (pages + 255) / 256)), 256, 0, stream>>>(refs, refs_out, pages);
+  if (rows) {
+    const int64_t x = std::min(rows, 8 * cus);
+    const int64_t y = std::min(std::max<int64_t>(1, (table_cols + 255) / 256), std::max<int64_t>(1, 8 * cus / x));
+    free_pages_kernel<<<dim3(unsigned(x), unsigned(y)), 256, 0, stream>>>(g);
+    if (lens_out == lens) free_lens_kernel<<<unsigned((rows + 255) / 256), 256, 0, stream>>>(g);
+  }
+  return launched();
+}
+
+extern "C" mx_status_t mx_kv_compact_workspace(int64_t pages, int64_t* bytes) {
+  if (!bytes) return MX_ERR_NULL;
+  if (pages < 0 || pages > INT32_MAX) return MX_ERR_SHAPE;
+  CompactArgs g = {};
+  g.pages = pages;
+  g.blocks = blocks_of(pages);
+  *bytes = compact_space(g, nullptr);
+  return MX_OK;
+}
+
+extern "C" mx_status_t mx_kv_compact(const mx_kv_cache_t* caches, int layers, const int32_t* refs,
+                                     const int32_t* page_table, int64_t table_stride, int64_t table_cols,
+                                     const int32_t* lens, int64_t rows, int32_t* refs_out, int32_t* table_out,
+                                     int32_t* used, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  const mx_status_t st = check_layers(caches, layers);
+  if (st != MX_OK) return st;
+  const int page = caches->page;
+  if (rows < 0 || rows > kMostRows || table_cols < 0 || table_cols > INT32_MAX / page ||
+      (table_stride < table_cols && rows > 1))
+    return MX_ERR_SHAPE;
+  CompactArgs g = {};
+  g.pages = caches->pages;
+  g.blocks = blocks_of(g.pages);
+  if (!used || (g.pages && (!refs || !refs_out))) return MX_ERR_NULL;
+  if (rows && (!lens || (table_cols && (!page_table || !table_out)))) return MX_ERR_NULL;
+  if (off4(refs) || off4(refs_out) || off4(lens) || off4(page_table) || off4(table_out) || off4(used)) return MX_ERR_ALIGN;
+  // a table changed in place has the same rows
+  if (table_out == page_table && table_stride != table_cols && rows > 1) return MX_ERR_ARG;
+  const int64_t need = compact_space(g, nullptr);
+  if (workspace_bytes < need) return MX_ERR_SHAPE;
+  if (!workspace) return MX_ERR_NULL;
+  if (misaligned(workspace)) return MX_ERR_ALIGN;
+  compact_space(g, static_cast<uint8_t*>(workspace));
+  g.refs = refs; g.table = page_table; g.lens = lens;
+  g.refs_out = refs_out; g.table_out = table_out; g.used = used;
+  g.stride = table_stride; g.rows = rows; g.cols = int(table_cols);
+  g.shape = shape_of(*caches);
+  const int64_t cus = std::max<int64_t>(device_cus(), 1);
+  if (g.blocks.count) compact_count_kernel<<<unsigned(g.blocks.count), 256, 0, stream>>>(g);
+  compact_plan_kernel<<<unsigned(std::max(1, g.blocks.count)), 256, 0, stream>>>(g);
+  for (int l = 0; l < layers; l += kLayersPerLaunch) {
+    const int n = std::min(kLayersPerLaunch, layers - l);
+    fill_layers(g.caches, caches + l, n);
+    g.items = items_of(*caches, n);
+    const unsigned copiers = g.pages > 1 ? copy_grid(g.pages / 2, g.items) : 0;
+    g.table_blocks = l == 0 ? std::max<int64_t>(1, std::min(4 * cus, std::max(rows, g.pages / 2048))) : 0;
+    if (g.table_blocks + copiers) compact_move_kernel<<<unsigned(g.table_blocks) + copiers, 256, 0, stream>>>(g);
+  }
+  return launched();
+}
