@@ -20,7 +20,7 @@ namespace mxk {
 constexpr int kMostBeams = 64;              // a lane for each when they are merged
 constexpr int kMostWidth = 64;              // a lane for each of a beam's candidates
 constexpr int kMostSplits = 64;             // a lane for each segment of a beam's logits
-constexpr int kLoads = 8;                   // 16-byte loads of a lane in flight
+constexpr int kMergeWaves = 8;
 constexpr int kBuffer = 512;                // candidates a wave sets aside before it sorts them in
 
 // Sum and maximum of a segment: sum exp(x - m).
@@ -41,7 +41,7 @@ struct BeamArgs {
   Part* parts;                              // [rows][splits]
   uint64_t* best;                           // [rows][splits][keep]
   int64_t request_stride, beam_stride, rows, segment;
-  int requests, beams, vocab, width, keep, splits, eos, pad, cols;
+  int requests, beams, vocab, width, keep, splits, eos, pad, cols, vector;
 };
 
 // Whole numbers in the order of floats (-0 below +0: callers add 0 first).
@@ -59,35 +59,82 @@ __device__ __forceinline__ uint64_t candidate(float x, uint32_t token) {
   return uint64_t(ordered(x + 0.0f)) << 32 | uint32_t(~token);
 }
 
-__device__ __forceinline__ uint64_t shuffle_xor(uint64_t x, int d) {
-  const uint32_t lo = __shfl_xor(int(uint32_t(x)), d), hi = __shfl_xor(int(uint32_t(x >> 32)), d);
+// The value of lane ^ D, by moves inside the vector unit: a shuffle through LDS takes some 60 clocks more, and a sort
+// is 27 of them one behind the other.
+template <int D>
+__device__ __forceinline__ uint32_t across(uint32_t x) {
+  if constexpr (D == 1) return __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, false);             // quads 1 0 3 2
+  else if constexpr (D == 2) return __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, false);        // quads 2 3 0 1
+  else if constexpr (D == 4) {
+    const uint32_t y = __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, false);                    // mirrored eights: lane ^ 7
+    return __builtin_amdgcn_mov_dpp(y, 0x1B, 0xF, 0xF, false);                                 // mirrored quads: lane ^ 3
+  } else if constexpr (D == 8) return __builtin_amdgcn_mov_dpp(x, 0x128, 0xF, 0xF, false);     // sixteens turned by 8
+  else if constexpr (D == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return threadIdx.x & 16u ? r[0] : r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return threadIdx.x & 32u ? r[0] : r[1];
+  }
+}
+
+template <int D>
+__device__ __forceinline__ uint64_t across(uint64_t x) {
+  return uint64_t(across<D>(uint32_t(x >> 32))) << 32 | across<D>(uint32_t(x));
+}
+template <int D>
+__device__ __forceinline__ float across(float x) { return __uint_as_float(across<D>(__float_as_uint(x))); }
+template <int D>
+__device__ __forceinline__ double across(double x) {
+  return __longlong_as_double(int64_t(across<D>(uint64_t(__double_as_longlong(x)))));
+}
+
+// f(x of this lane, x of lane ^ D) for D = From, From / 2 .. 1.
+template <int From, class T, class F>
+__device__ __forceinline__ T fold(T x, F f) {
+  x = f(x, across<From>(x), std::integral_constant<int, From>{});
+  if constexpr (From > 1) return fold<From / 2>(x, f);
+  else return x;
+}
+
+template <class T>
+__device__ __forceinline__ T wave_sum(T x) {
+  return fold<32>(x, [](T a, T b, auto) { return a + b; });
+}
+__device__ __forceinline__ float wave_max(float x) {
+  return fold<32>(x, [](float a, float b, auto) { return fmaxf(a, b); });
+}
+
+__device__ __forceinline__ uint64_t lane_value(uint64_t x, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(x), lane), hi = __builtin_amdgcn_readlane(uint32_t(x >> 32), lane);
   return uint64_t(hi) << 32 | lo;
 }
 
-__device__ __forceinline__ uint64_t shuffle(uint64_t x, int lane) {
-  const uint32_t lo = __shfl(int(uint32_t(x)), lane), hi = __shfl(int(uint32_t(x >> 32)), lane);
-  return uint64_t(hi) << 32 | lo;
+template <int Size>
+__device__ __forceinline__ uint64_t sorted(uint64_t x) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (Size > 2) x = sorted<Size / 2>(x);
+  return fold<Size / 2>(x, [&](uint64_t a, uint64_t b, auto d) {
+    const bool small = ((lane & Size) == 0) == ((lane & decltype(d)::value) == 0);
+    return (a < b) == small ? a : b;
+  });
 }
 
 // list: 64 candidates, the best in lane 0; takes in 64 more in any order: these are sorted the other way round, so
 // that lane by lane the better of the two are the best 64 of all, up and down once, which six steps put in order.
 __device__ __forceinline__ uint64_t absorb(uint64_t list, uint64_t x) {
   const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int size = 2; size <= 64; size *= 2)
-#pragma unroll
-    for (int d = size / 2; d >= 1; d /= 2) {
-      const uint64_t y = shuffle_xor(x, d);
-      const bool small = ((lane & size) == 0) == ((lane & d) == 0);
-      x = (x < y) == small ? x : y;
-    }
+  x = sorted<64>(x);
   x = x > list ? x : list;
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) {
-    const uint64_t y = shuffle_xor(x, d);
-    x = (x < y) == ((lane & d) != 0) ? x : y;
-  }
-  return x;
+  return fold<32>(x, [&](uint64_t a, uint64_t b, auto d) {
+    return (a < b) == ((lane & decltype(d)::value) != 0) ? a : b;
+  });
+}
+
+// Lanes of a wave hand candidates to each other through LDS: what was written before is read after.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 // A wave's best `keep` candidates of what it has seen.
@@ -99,15 +146,42 @@ struct Best {
 
   __device__ __forceinline__ void take_in(uint64_t* buffer, int keep) {
     const int lane = threadIdx.x & 63;
+    wave_fence();
+    const int all = waiting + __popcll(__ballot(list != 0));
+    if (all <= 64) {
+      // few, as almost always: each one's place is the number of better ones (no two are alike).  20 clocks a
+      // candidate, where the sort of 64 takes 3000 with its code fetched
+      if (list) buffer[waiting + lane] = list;
+      wave_fence();
+      const uint64_t x = lane < all ? buffer[lane] : 0;
+      int place = 0;
+      for (int i = 0; i < all; ++i) place += lane_value(x, i) > x;
+      if (lane < all) buffer[place] = x;
+      wave_fence();
+      list = lane < min(all, keep) ? buffer[lane] : 0;
+      waiting = 0;
+    }
     while (waiting > 0) {
       const int n = min(waiting, 64);
       waiting -= n;
       list = absorb(list, lane < n ? buffer[waiting + lane] : 0);
+      if (lane >= keep) list = 0;
     }
-    least = shuffle(list, keep - 1);
+    least = lane_value(list, keep - 1);
     if (least) floor = unordered(uint32_t(least >> 32));
+    wave_fence();                           // read before the next ones are written
   }
 };
+
+// A bound that the keys of at least `keep` lanes reach (0 where not so many have one): the keep-th largest of them to
+// 16 bits, a float's sign, exponent and seven more.
+__device__ __forceinline__ uint32_t bound_of(uint32_t key, int keep) {
+  uint32_t bound = 0;
+#pragma unroll
+  for (int bit = 31; bit >= 16; --bit)
+    if (__popcll(__ballot(key >= (bound | 1u << bit))) >= keep) bound |= 1u << bit;
+  return bound;
+}
 
 template <int DT>
 struct Elements;
@@ -157,7 +231,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // moves each lane's own reference before its exponentials are added (in 32 bits within a chunk, in 64 across chunks).
 // The first chunk's keep-th largest lane maximum is a bound that at least keep logits reach: those that reach it,
 // some more than keep, are set aside and sorted.
-template <int DT>
+template <int DT, int kLoads>
 __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
   using E = Elements<DT>;
   using T = typename E::Type;
@@ -210,12 +284,7 @@ __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
     }
     s += double(sum);
     if (at == begin) {
-      // a bound that keep lanes' maxima reach, to 20 bits: the sign, the exponent and eleven more
-      const uint32_t key = ordered(top + 0.0f);
-      uint32_t bound = 0;
-#pragma unroll
-      for (int bit = 31; bit >= 12; --bit)
-        if (__popcll(__ballot(key >= (bound | 1u << bit))) >= g.keep) bound |= 1u << bit;
+      const uint32_t bound = bound_of(ordered(top + 0.0f), g.keep);
       best.floor = bound ? fmaxf(unordered(bound), -FLT_MAX) : -FLT_MAX;
       // bit patterns of NaN order above all numbers; the row is then passed over whatever is kept
       if (!(best.floor <= FLT_MAX)) best.floor = FLT_MAX;
@@ -255,19 +324,16 @@ __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
     }
   }
   best.take_in(buffer, g.keep);
-  float all = m;
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) all = fmaxf(all, __shfl_xor(all, d));
-  s *= double(__builtin_amdgcn_exp2f((m - all) * kLog2e));
-#pragma unroll
-  for (int d = 32; d >= 1; d /= 2) s += __shfl_xor(s, d);
+  const float all = wave_max(m);
+  s = wave_sum(s * double(__builtin_amdgcn_exp2f((m - all) * kLog2e)));
   if (lane == 0) g.parts[id] = {s, all, 0};
   if (lane < g.keep) g.best[id * g.keep + lane] = best.list;
 }
 
 // A workgroup for each request, several where long histories are copied (each takes the same decision and copies
 // some of the columns).
-__global__ __launch_bounds__(256) void beam_merge_kernel(const BeamArgs g) {
+__global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const BeamArgs g) {
+  __shared__ uint64_t buffers[kMergeWaves][kBuffer];
   extern __shared__ double score[];         // [beams][keep], and the tokens behind them
   uint32_t* token = reinterpret_cast<uint32_t*>(score + g.beams * g.keep);
   __shared__ int chosen_beam[kMostWidth];
@@ -275,34 +341,62 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(const BeamArgs g) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int request = blockIdx.x;
   const int64_t row0 = int64_t(request) * g.beams;
-  for (int b = wave; b < g.beams; b += 4) {
+  __shared__ int length[kMostBeams];
+  __shared__ bool was[kMostBeams];
+  // all that does not depend on the choice is read before it
+  if (int(threadIdx.x) < g.beams) {
+    was[threadIdx.x] = g.finished && g.finished[row0 + threadIdx.x];
+    length[threadIdx.x] = g.lens ? min(max(g.lens[row0 + threadIdx.x], 0), g.cols) : 0;
+  }
+  for (int b = wave; b < g.beams; b += kMergeWaves) {
     const int64_t row = row0 + b;
+    const float before = g.scores[row];
+    const bool done = g.finished && g.finished[row];
+    // (of a beam without a scan, what the workspace holds is read and not used)
+    const int count = g.splits * g.keep;
+    const uint64_t* from = g.best + row * count;
+    uint64_t c[kBuffer / 64];
+    auto load = [&](int i) {
+#pragma unroll
+      for (int u = 0; u < kBuffer / 64; ++u) c[u] = i + u * 64 + lane < count ? from[i + u * 64 + lane] : 0;
+    };
+    load(0);
+    Part p = {0.0, -FLT_MAX, 0};
+    if (lane < g.splits) p = g.parts[row * g.splits + lane];
     double mine = -INFINITY;
     uint32_t v = 0;
-    if (live(g, row)) {
-      Part p = {0.0, -FLT_MAX, 0};
-      if (lane < g.splits) p = g.parts[row * g.splits + lane];
-      float all = p.m;
-#pragma unroll
-      for (int d = 32; d >= 1; d /= 2) all = fmaxf(all, __shfl_xor(all, d));
-      double s = p.s * exp(double(p.m) - double(all));
-#pragma unroll
-      for (int d = 32; d >= 1; d /= 2) s += __shfl_xor(s, d);
+    if (isfinite(before) && !done) {
+      Best best;
+      const float all = wave_max(p.m);
+      const double s = wave_sum(p.s * double(__builtin_amdgcn_exp2f((p.m - all) * kLog2e)));
       const double log_s = log(s);            // apart from the maximum, beside which it could vanish
-      uint64_t list = 0;
-      const int count = g.splits * g.keep;
-      const uint64_t* from = g.best + row * count;
-      for (int i = 0; i < count; i += 64) {
-        const uint64_t c = i + lane < count ? from[i + lane] : 0;
-        if (__ballot(c > shuffle(list, g.keep - 1))) list = absorb(list, c);
+      for (int i = 0; i < count; i += kBuffer) {
+        if (i) load(i);
+        if (i == 0 && count > 64) {
+          // as in the scan, a bound that keep lanes reach
+          uint32_t key = 0;
+#pragma unroll
+          for (int u = 0; u < kBuffer / 64; ++u) key = max(key, uint32_t(c[u] >> 32));
+          best.least = uint64_t(bound_of(key, g.keep)) << 32;
+        }
+#pragma unroll
+        for (int u = 0; u < kBuffer / 64; ++u) {
+          if (i + u * 64 >= count) break;
+          const bool hit = c[u] && c[u] >= best.least;
+          const uint64_t mask = __ballot(hit);
+          if (hit) buffers[wave][best.waiting + __popcll(mask & ((uint64_t(1) << lane) - 1))] = c[u];
+          best.waiting += __popcll(mask);
+        }
+        best.take_in(buffers[wave], g.keep);
       }
+      const uint64_t list = best.list;
       // a row with NaN or +inf, or without a finite logit, has no candidates
       if (list && isfinite(log_s) && isfinite(all)) {
-        mine = double(g.scores[row]) + ((double(unordered(uint32_t(list >> 32))) - double(all)) - log_s);
+        mine = double(before) + ((double(unordered(uint32_t(list >> 32))) - double(all)) - log_s);
         v = ~uint32_t(list);
       }
-    } else if (isfinite(g.scores[row]) && lane == 0) {
-      mine = g.scores[row];                 // finished: itself
+    } else if (isfinite(before) && lane == 0) {
+      mine = before;                        // finished: itself
       v = uint32_t(g.pad);
     }
     if (lane < g.keep) {
@@ -311,31 +405,42 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(const BeamArgs g) {
     }
   }
   __syncthreads();
-  if (wave == 0) {
-    // lane b holds the best candidate of beam b that is left
+  auto choose = [&](int place, int beam, double z, int t) {
+    chosen_beam[place] = beam;
+    chosen_token[place] = t;
+    if (blockIdx.y == 0) g.scores_out[int64_t(request) * g.width + place] = float(z);
+  };
+  const int candidates = g.beams * g.keep;
+  if (candidates <= 64 * kMergeWaves) {
+    // a candidate's place is the number of better ones: those before it (lower beams, better logits) that are not
+    // worse, and those behind it that are better
+    const int me = threadIdx.x;
+    const double mine = me < candidates ? score[me] : -INFINITY;
+    int place = 0;
+    if (wave * 64 < candidates) {
+#pragma unroll 8
+      for (int i = 0; i < candidates; ++i) {
+        const double other = score[i];
+        place += other > mine || (other == mine && i < me);
+      }
+    }
+    if (mine > -INFINITY && place < g.width) choose(place, me / g.keep, mine, int(token[me]));
+    const int real = __syncthreads_count(mine > -INFINITY);
+    if (me >= real && me < g.width) choose(me, -1, -INFINITY, g.pad);
+  } else if (wave == 0) {
+    // one after the other: lane b holds the best candidate of beam b that is left
     int at = 0;
     double head = lane < g.beams ? score[lane * g.keep] : -INFINITY;
     for (int j = 0; j < g.width; ++j) {
-      double top = head;
-      int from = lane;
-#pragma unroll
-      for (int d = 1; d <= 32; d *= 2) {
-        const double y = __shfl_xor(top, d);
-        const int f = __shfl_xor(from, d);
-        if (y > top || (y == top && f < from)) {
-          top = y;
-          from = f;
-        }
-      }
-      const bool real = top > -INFINITY;
-      if (lane == from) {
-        if (blockIdx.y == 0) g.scores_out[int64_t(request) * g.width + j] = real ? float(top) : -INFINITY;
-        chosen_beam[j] = real ? lane : -1;
-        chosen_token[j] = real ? int(token[lane * g.keep + at]) : g.pad;
-        if (real) {
-          ++at;
-          head = at < g.keep ? score[lane * g.keep + at] : -INFINITY;
-        }
+      const double top = fold<32>(head, [](double a, double b, auto) { return fmax(a, b); });
+      const int from = __ffsll(__ballot(head == top)) - 1;          // of equal ones the lower beam
+      if (lane != from) continue;
+      if (top > -INFINITY) {
+        choose(j, lane, top, int(token[lane * g.keep + at]));
+        ++at;
+        head = at < g.keep ? score[lane * g.keep + at] : -INFINITY;
+      } else {
+        choose(j, -1, top, g.pad);
       }
     }
   }
@@ -343,31 +448,51 @@ __global__ __launch_bounds__(256) void beam_merge_kernel(const BeamArgs g) {
   if (blockIdx.y == 0 && int(threadIdx.x) < g.width) {
     const int j = threadIdx.x, b = chosen_beam[j], v = chosen_token[j];
     const int64_t row = row0 + max(b, 0), o = int64_t(request) * g.width + j;
-    const bool was = b >= 0 && g.finished && g.finished[row];
+    const bool stays = b < 0 || was[b];
     g.parents[o] = int32_t(row);
     g.tokens[o] = v;
-    g.finished_out[o] = was || (b >= 0 && v == g.eos);
+    g.finished_out[o] = b >= 0 && (was[b] || v == g.eos);
     if (g.lens) {
-      const int n = min(max(g.lens[row], 0), g.cols);
-      g.lens_out[o] = b >= 0 && !was && n < g.cols ? n + 1 : n;
+      const int n = length[max(b, 0)];
+      g.lens_out[o] = stays || n == g.cols ? n : n + 1;
     }
   }
   if (!g.history || g.cols == 0) return;
-  for (int j = wave; j < g.width; j += 4) {
+  for (int j = wave; j < g.width; j += kMergeWaves) {
     const int b = chosen_beam[j];
     const int64_t row = row0 + max(b, 0);
     const int32_t* from = g.history + row * g.cols;
     int32_t* to = g.history_out + (int64_t(request) * g.width + j) * g.cols;
-    const bool grows = b >= 0 && !(g.finished && g.finished[row]);
-    const int n = min(max(g.lens[row], 0), g.cols);
-    for (int i = blockIdx.y * 64 + lane; i < g.cols; i += gridDim.y * 64) to[i] = grows && i == n ? chosen_token[j] : from[i];
+    const bool grows = b >= 0 && !was[b];
+    const int n = length[max(b, 0)], t = chosen_token[j];
+    // 16 bytes at once where rows start on such borders, eight of them in flight
+    const int vectors = g.vector ? g.cols / 4 : 0;
+    for (int i = blockIdx.y * 512; i < vectors; i += gridDim.y * 512) {
+      int4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i + u * 64 + lane < vectors) v[u] = reinterpret_cast<const int4*>(from)[i + u * 64 + lane];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int at = i + u * 64 + lane;
+        if (at >= vectors) continue;
+        if (grows && n / 4 == at) {
+          if (n % 4 == 0) v[u].x = t;
+          else if (n % 4 == 1) v[u].y = t;
+          else if (n % 4 == 2) v[u].z = t;
+          else v[u].w = t;
+        }
+        reinterpret_cast<int4*>(to)[at] = v[u];
+      }
+    }
+    for (int i = vectors * 4 + blockIdx.y * 64 + lane; i < g.cols; i += gridDim.y * 64) to[i] = grows && i == n ? t : from[i];
   }
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-// Segments of a beam's logits: enough waves for eight on every SIMD, but at least 1024 logits each (shorter ones cost
+// Segments of a beam's logits: enough waves for four on every SIMD, but at least 1024 logits each (shorter ones cost
 // the second launch more than they save the first).
 mx_status_t plan(BeamArgs& g, mx_dtype_t dtype, int64_t requests, int64_t beams, int64_t vocab, int64_t width) {
   if (dtype != MX_F32 && dtype != MX_BF16 && dtype != MX_F16) return MX_ERR_UNSUPPORTED;
@@ -380,10 +505,10 @@ mx_status_t plan(BeamArgs& g, mx_dtype_t dtype, int64_t requests, int64_t beams,
   g.vocab = int(vocab);
   g.width = int(width);
   g.keep = int(std::min(width, vocab));
-  const int64_t waves = 32 * std::max<int64_t>(device_cus(), 1);
+  const int64_t waves = 16 * std::max<int64_t>(device_cus(), 1);
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kMostSplits, waves / std::max<int64_t>(g.rows, 1)));
   const int64_t least = std::max<int64_t>(1024, (vocab + want - 1) / want);
-  g.segment = (least + 511) / 512 * 512;
+  g.segment = least <= 1024 ? 1024 : least <= 2048 ? 2048 : (least + 4095) / 4096 * 4096;
   g.splits = int((vocab + g.segment - 1) / g.segment);
   return MX_OK;
 }
@@ -437,13 +562,21 @@ extern "C" mx_status_t mx_beam_select(const void* logits, mx_dtype_t dtype, int6
   g.request_stride = request_stride; g.beam_stride = beam_stride;
   g.eos = int(eos); g.pad = int(pad); g.cols = int(history_cols);
   const unsigned blocks = unsigned((g.rows * g.splits + 3) / 4);
-  if (dtype == MX_F32) beam_scan_kernel<MX_F32><<<blocks, 256, 0, stream>>>(g);
-  else if (dtype == MX_BF16) beam_scan_kernel<MX_BF16><<<blocks, 256, 0, stream>>>(g);
-  else beam_scan_kernel<MX_F16><<<blocks, 256, 0, stream>>>(g);
-  // 64 KiB of history a workgroup where there are few requests
-  const int64_t wide = with_history ? g.width * int64_t(g.cols) * 4 / 65536 : 0;
+  auto scan = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    const int64_t loads = (g.segment + 64 * Elements<DT>::kVec - 1) / (64 * Elements<DT>::kVec);
+    if (loads <= 2) beam_scan_kernel<DT, 2><<<blocks, 256, 0, stream>>>(g);
+    else if (loads <= 4) beam_scan_kernel<DT, 4><<<blocks, 256, 0, stream>>>(g);
+    else beam_scan_kernel<DT, 8><<<blocks, 256, 0, stream>>>(g);
+  };
+  if (dtype == MX_F32) scan(std::integral_constant<int, MX_F32>{});
+  else if (dtype == MX_BF16) scan(std::integral_constant<int, MX_BF16>{});
+  else scan(std::integral_constant<int, MX_F16>{});
+  g.vector = g.cols % 4 == 0 && !misaligned(history) && !misaligned(history_out);
+  // 32 KiB of history a workgroup, up to two of them on a CU
+  const int64_t wide = with_history ? g.width * int64_t(g.cols) * 4 / 32768 : 0;
   const int64_t most = std::max<int64_t>(1, 2 * std::max<int64_t>(device_cus(), 1) / requests);
   const unsigned y = unsigned(std::max<int64_t>(1, std::min(wide, most)));
-  beam_merge_kernel<<<dim3(unsigned(requests), y), 256, size_t(g.beams) * g.keep * 12, stream>>>(g);
+  beam_merge_kernel<<<dim3(unsigned(requests), y), 64 * kMergeWaves, size_t(g.beams) * g.keep * 12, stream>>>(g);
   return hipGetLastError() == hipSuccess ? MX_OK : MX_ERR_LAUNCH;
 }
