@@ -23,6 +23,9 @@ constexpr int kMostSplits = 64;             // a lane for each segment of a beam
 constexpr int kMergeWaves = 8;
 constexpr int kBuffer = 512;                // candidates a wave sets aside before it sorts them in
 
+typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));      // of logits, at any place of their type
+typedef int32_t Vector __attribute__((ext_vector_type(4)));
+
 // Sum and maximum of a segment: sum exp(x - m).
 struct Part {
   double s;
@@ -189,8 +192,8 @@ template <>
 struct Elements<MX_F32> {
   static constexpr int kVec = 4;
   using Type = float;
-  static __device__ __forceinline__ float at(const uint4& v, int j) {
-    return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
+  static __device__ __forceinline__ float at(const Words& v, int j) {
+    return __uint_as_float(v[j]);
   }
   static __device__ __forceinline__ float one(float x) { return x; }
   static constexpr uint32_t kNone = 0xFF800000u;
@@ -199,8 +202,8 @@ template <>
 struct Elements<MX_BF16> {
   static constexpr int kVec = 8;
   using Type = uint16_t;
-  static __device__ __forceinline__ float at(const uint4& v, int j) {
-    const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
+  static __device__ __forceinline__ float at(const Words& v, int j) {
+    const uint32_t w = v[j / 2];
     return __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16);
   }
   static __device__ __forceinline__ float one(uint16_t x) { return __uint_as_float(uint32_t(x) << 16); }
@@ -213,8 +216,8 @@ struct Elements<MX_F16> {
   static __device__ __forceinline__ float one(uint16_t x) {
     return float(__builtin_bit_cast(_Float16, x));
   }
-  static __device__ __forceinline__ float at(const uint4& v, int j) {
-    const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
+  static __device__ __forceinline__ float at(const Words& v, int j) {
+    const uint32_t w = v[j / 2];
     return one(uint16_t(j & 1 ? w >> 16 : w & 0xFFFFu));
   }
   static constexpr uint32_t kNone = 0xFC00FC00u;
@@ -227,10 +230,12 @@ __device__ __forceinline__ bool live(const BeamArgs& g, int64_t row) {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// A wave for each segment of each beam's logits.  Eight loads of 16 bytes a lane are in flight; a chunk's maximum
-// moves each lane's own reference before its exponentials are added (in 32 bits within a chunk, in 64 across chunks).
-// The first chunk's keep-th largest lane maximum is a bound that at least keep logits reach: those that reach it,
-// some more than keep, are set aside and sorted.
+// A wave for each segment of each beam's logits.  Eight loads of 16 bytes a lane are in flight, past the caches (which
+// spares 8%); a chunk's maximum moves each lane's own reference before its exponentials are added, in 32 bits within a
+// chunk and in 64 across chunks.  The first chunk's keep-th largest lane maximum is a bound that at least keep logits
+// reach: those that reach it, some more than keep, are set aside and sorted.  2048 rows of 131072 BF16 logits take 109
+// us, 4.9 TB/s, as a copy does, with the vector unit busy half of the time.  Tried: each granule's registers reloaded
+// for the next chunk as soon as it is worked off, 128 us: the compiler waits for all of them at the loop's head.
 template <int DT, int kLoads>
 __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
   using E = Elements<DT>;
@@ -250,18 +255,18 @@ __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
   float m = -FLT_MAX;
   double s = 0.0;
   for (int at = begin; at < end; at += kChunk) {
-    uint4 v[kLoads];
+    Words v[kLoads];
     float odd = -INFINITY;                  // of the elements behind the last whole 16 bytes, a lane has one
     const int whole = end - (end - begin) % kVec;          // only a row's last segment has others
     if (at + kChunk <= whole) {
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) __builtin_memcpy(&v[u], x + at + (u * 64 + lane) * kVec, 16);
+      for (int u = 0; u < kLoads; ++u) v[u] = __builtin_nontemporal_load(reinterpret_cast<const Words*>(x + at + (u * 64 + lane) * kVec));
     } else {
 #pragma unroll
       for (int u = 0; u < kLoads; ++u) {
-        v[u] = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+        v[u] = Words{E::kNone, E::kNone, E::kNone, E::kNone};
         const int i = at + (u * 64 + lane) * kVec;
-        if (i < whole) __builtin_memcpy(&v[u], x + i, 16);
+        if (i < whole) v[u] = __builtin_nontemporal_load(reinterpret_cast<const Words*>(x + i));
       }
       if (whole + lane < end && at + kChunk >= whole) odd = E::one(x[whole + lane]);
     }
@@ -345,8 +350,9 @@ __global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const Beam
   __shared__ bool was[kMostBeams];
   // all that does not depend on the choice is read before it
   if (int(threadIdx.x) < g.beams) {
+    const int n = g.lens ? g.lens[row0 + threadIdx.x] : 0;
     was[threadIdx.x] = g.finished && g.finished[row0 + threadIdx.x];
-    length[threadIdx.x] = g.lens ? min(max(g.lens[row0 + threadIdx.x], 0), g.cols) : 0;
+    length[threadIdx.x] = min(max(n, 0), g.cols);
   }
   for (int b = wave; b < g.beams; b += kMergeWaves) {
     const int64_t row = row0 + b;
@@ -358,11 +364,16 @@ __global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const Beam
     uint64_t c[kBuffer / 64];
     auto load = [&](int i) {
 #pragma unroll
-      for (int u = 0; u < kBuffer / 64; ++u) c[u] = i + u * 64 + lane < count ? from[i + u * 64 + lane] : 0;
+      for (int u = 0; u < kBuffer / 64; ++u) c[u] = from[min(i + u * 64 + lane, count - 1)];
+#pragma unroll
+      for (int u = 0; u < kBuffer / 64; ++u) c[u] = i + u * 64 + lane < count ? c[u] : 0;
     };
     load(0);
-    Part p = {0.0, -FLT_MAX, 0};
-    if (lane < g.splits) p = g.parts[row * g.splits + lane];
+    Part p = g.parts[row * g.splits + min(lane, g.splits - 1)];
+    // without this the loads move down to where each value is needed, one behind the other
+#pragma unroll
+    for (int u = 0; u < kBuffer / 64; ++u) asm volatile("" : "+v"(c[u]));
+    if (lane >= g.splits) p = {0.0, -FLT_MAX, 0};
     double mine = -INFINITY;
     uint32_t v = 0;
     if (isfinite(before) && !done) {
@@ -468,21 +479,21 @@ __global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const Beam
     // 16 bytes at once where rows start on such borders, eight of them in flight
     const int vectors = g.vector ? g.cols / 4 : 0;
     for (int i = blockIdx.y * 512; i < vectors; i += gridDim.y * 512) {
-      int4 v[8];
+      Vector v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (i + u * 64 + lane < vectors) v[u] = reinterpret_cast<const int4*>(from)[i + u * 64 + lane];
+        v[u] = reinterpret_cast<const Vector*>(from)[min(i + u * 64 + lane, vectors - 1)];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int at = i + u * 64 + lane;
         if (at >= vectors) continue;
         if (grows && n / 4 == at) {
-          if (n % 4 == 0) v[u].x = t;
-          else if (n % 4 == 1) v[u].y = t;
-          else if (n % 4 == 2) v[u].z = t;
-          else v[u].w = t;
+          v[u].x = n % 4 == 0 ? t : v[u].x;
+          v[u].y = n % 4 == 1 ? t : v[u].y;
+          v[u].z = n % 4 == 2 ? t : v[u].z;
+          v[u].w = n % 4 == 3 ? t : v[u].w;
         }
-        reinterpret_cast<int4*>(to)[at] = v[u];
+        reinterpret_cast<Vector*>(to)[at] = v[u];
       }
     }
     for (int i = vectors * 4 + blockIdx.y * 64 + lane; i < g.cols; i += gridDim.y * 64) to[i] = grows && i == n ? t : from[i];
@@ -492,8 +503,11 @@ __global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const Beam
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-// Segments of a beam's logits: enough waves for four on every SIMD, but at least 1024 logits each (shorter ones cost
-// the second launch more than they save the first).
+// Segments of a beam's logits: enough waves for eight on every SIMD, but of at least 4096 logits where that leaves one
+// for every SIMD, else of 1024: the bound, the sorts and the sums at the end of a segment cost a wave as much as some
+// thousand logits, and the second launch reads what each leaves.  (32 x 4 beams of 50001 F16 logits, both launches: 9.7 +
+// 6.8 us with segments of 4096, 9.0 + 7.4 with 2048, 11.3 + 9.8 with 1024; 2048 rows of 131072 BF16 logits, the first
+// launch: 108 us with eight waves on a SIMD, 111 with four.)
 mx_status_t plan(BeamArgs& g, mx_dtype_t dtype, int64_t requests, int64_t beams, int64_t vocab, int64_t width) {
   if (dtype != MX_F32 && dtype != MX_BF16 && dtype != MX_F16) return MX_ERR_UNSUPPORTED;
   if (requests < 0 || requests > (int64_t(1) << 24) || beams < 1 || beams > kMostBeams || width < 1 || width > kMostWidth ||
@@ -505,9 +519,10 @@ mx_status_t plan(BeamArgs& g, mx_dtype_t dtype, int64_t requests, int64_t beams,
   g.vocab = int(vocab);
   g.width = int(width);
   g.keep = int(std::min(width, vocab));
-  const int64_t waves = 16 * std::max<int64_t>(device_cus(), 1);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kMostSplits, waves / std::max<int64_t>(g.rows, 1)));
-  const int64_t least = std::max<int64_t>(1024, (vocab + want - 1) / want);
+  const int64_t cus = std::max<int64_t>(device_cus(), 1), rows = std::max<int64_t>(g.rows, 1);
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kMostSplits, 32 * cus / rows));
+  const int64_t shortest = rows * ((vocab + 4095) / 4096) >= 4 * cus ? 4096 : 1024;
+  const int64_t least = std::max<int64_t>(shortest, (vocab + want - 1) / want);
   g.segment = least <= 1024 ? 1024 : least <= 2048 ? 2048 : (least + 4095) / 4096 * 4096;
   g.splits = int((vocab + g.segment - 1) / g.segment);
   return MX_OK;

@@ -42,14 +42,16 @@ __device__ __forceinline__ int64_t divide(int64_t n, int64_t d, double inv, int6
   return q;
 }
 
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 // ---------------------------------------------------------------------------
 // Copies
 // ---------------------------------------------------------------------------
 // A wave copies part `part` of the first `tokens` tokens (a multiple of 16) of page src to page dst: 8 KiB of the
 // keys, the values, the key scales and the value scales in a row.  Eight loads of 16 bytes a lane are in flight
 // before the first store, past the caches, as no part is read twice.  A whole page is one run of bytes in each array;
-// of a part of one, each head is a run.  Measured on 1.1 GB read and written: 205 us (5.4 TB/s); with four loads 213,
-// through the caches 227, with 2048 instead of up to 16384 workgroups 216; 300 with an address worked out for each
+// of a part of one, each head is a run.  Measured on 1.1 GB read and written: 205 to 213 us (5.2 to 5.4 TB/s); with four loads
+// 213, through the caches 227, with 2048 instead of up to 16384 workgroups 216; 300 with an address worked out for each
 // 16 bytes, as now only in parts that are not of one array.
 __device__ __forceinline__ void copy_part(uint8_t* const (&from)[4], uint8_t* const (&to)[4], const PageShape& s,
                                           int64_t src, int64_t dst, int tokens, uint32_t part) {
@@ -72,31 +74,43 @@ __device__ __forceinline__ void copy_part(uint8_t* const (&from)[4], uint8_t* co
     for (int i = 0; i < kPartLoads; ++i) __builtin_nontemporal_store(v[i], t + i * 64);
     return;
   }
-  uint8_t* at[kPartLoads];
+  // four at a time: 256 registers for eight of them and their addresses
+  uint8_t* const from0 = from[0];
+  uint8_t* const from1 = from[1];
+  uint8_t* const from2 = from[2];
+  uint8_t* const from3 = from[3];
+  uint8_t* const to0 = to[0];
+  uint8_t* const to1 = to[1];
+  uint8_t* const to2 = to[2];
+  uint8_t* const to3 = to[3];
+#pragma unroll 1
+  for (int half = 0; half < kPartLoads; half += 4) {
+    uint8_t* at[4];
 #pragma unroll
-  for (int i = 0; i < kPartLoads; ++i) {
-    const uint32_t g = first + i * 64 + lane;
-    const bool is_scale = g >= 2u * codes;
-    uint32_t o = is_scale ? g - 2u * codes : g;
-    const uint32_t n = is_scale ? scales : codes, run = is_scale ? head_scales : head_codes;
-    const bool is_value = o >= n;
-    o -= is_value ? n : 0u;
-    const int64_t page_bytes = is_scale ? page_codes / 32 : page_codes;
-    int64_t off = int64_t(o) * 16;
-    if (!whole) {
-      const uint32_t head = o / run;
-      off = int64_t(head) * (int64_t(s.page) * s.dim / (is_scale ? 32 : 1)) + int64_t(o - head * run) * 16;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t g = first + (half + i) * 64 + lane;
+      const bool is_scale = g >= 2u * codes;
+      uint32_t o = is_scale ? g - 2u * codes : g;
+      const uint32_t n = is_scale ? scales : codes, run = is_scale ? head_scales : head_codes;
+      const bool is_value = o >= n;
+      o -= is_value ? n : 0u;
+      const int64_t page_bytes = is_scale ? page_codes / 32 : page_codes;
+      int64_t off = int64_t(o) * 16;
+      if (!whole) {
+        const uint32_t head = o / run;
+        off = int64_t(head) * (int64_t(s.page) * s.dim / (is_scale ? 32 : 1)) + int64_t(o - head * run) * 16;
+      }
+      const uint8_t* f = is_scale ? (is_value ? from3 : from1) : (is_value ? from2 : from0);
+      uint8_t* t = is_scale ? (is_value ? to3 : to1) : (is_value ? to2 : to0);
+      const bool real = g < 2u * (codes + scales);
+      v[i] = Granule{};
+      if (real) v[i] = __builtin_nontemporal_load(reinterpret_cast<const Granule*>(f + src * page_bytes + off));
+      at[i] = real ? t + dst * page_bytes + off : nullptr;
     }
-    const uint8_t* f = is_scale ? (is_value ? from[3] : from[1]) : (is_value ? from[2] : from[0]);
-    uint8_t* t = is_scale ? (is_value ? to[3] : to[1]) : (is_value ? to[2] : to[0]);
-    const bool real = g < 2u * (codes + scales);
-    v[i] = Granule{};
-    if (real) v[i] = __builtin_nontemporal_load(reinterpret_cast<const Granule*>(f + src * page_bytes + off));
-    at[i] = real ? t + dst * page_bytes + off : nullptr;
-  }
 #pragma unroll
-  for (int i = 0; i < kPartLoads; ++i)
-    if (at[i]) __builtin_nontemporal_store(v[i], reinterpret_cast<Granule*>(at[i]));
+    for (int i = 0; i < 4; ++i)
+      if (at[i]) __builtin_nontemporal_store(v[i], reinterpret_cast<Granule*>(at[i]));
+  }
 }
 
 struct Item {
@@ -116,8 +130,6 @@ struct Items {
     return {copy, int(layer), uint32_t(part)};
   }
 };
-
-__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 struct CopyArgs {
   Layers from, to;
@@ -140,22 +152,33 @@ __global__ __launch_bounds__(256) void page_copy_kernel(const CopyArgs g) {
 }
 
 // ---------------------------------------------------------------------------
-// Sums over a workgroup of 256 threads
+// Sums over a workgroup
 // ---------------------------------------------------------------------------
+// x of a lane some way before this one, 0 where there is none: by moves inside the vector unit.
+template <int Ctrl, int Rows>
+__device__ __forceinline__ int32_t before_lane(int32_t x) { return __builtin_amdgcn_update_dpp(0, x, Ctrl, Rows, 0xF, false); }
+template <int Ctrl, int Rows>
+__device__ __forceinline__ int64_t before_lane(int64_t x) {
+  const uint32_t lo = before_lane<Ctrl, Rows>(int32_t(x)), hi = before_lane<Ctrl, Rows>(int32_t(x >> 32));
+  return int64_t(uint64_t(hi) << 32 | lo);
+}
+
+// Sum of x over the lanes up to this one: within each sixteen lanes, then the last lanes of sixteens, of halves.
 template <class T>
 __device__ __forceinline__ T wave_scan(T x) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const T y = __shfl_up(x, d);
-    if (int(threadIdx.x & 63u) >= d) x += y;
-  }
+  x += before_lane<0x111, 0xF>(x);
+  x += before_lane<0x112, 0xF>(x);
+  x += before_lane<0x114, 0xF>(x);
+  x += before_lane<0x118, 0xF>(x);
+  x += before_lane<0x142, 0xA>(x);
+  x += before_lane<0x143, 0xC>(x);
   return x;
 }
 
-// Sum of x over the threads before this one, and over all of them.
-template <class T>
+// Sum of x over the threads before this one, and over all of them, in a workgroup of W waves.
+template <int W = 4, class T>
 __device__ __forceinline__ T block_scan(T x, T& total) {
-  __shared__ T part[4];
+  __shared__ T part[W];
   const T mine = wave_scan(x);
   const int w = threadIdx.x >> 6;
   __syncthreads();                          // the last call's sums are read
@@ -164,7 +187,7 @@ __device__ __forceinline__ T block_scan(T x, T& total) {
   T before = 0;
   total = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < W; ++i) {
     if (i < w) before += part[i];
     total += part[i];
   }
@@ -190,23 +213,79 @@ __device__ __forceinline__ T sum_before(const U* a, int count, int before, T& to
 struct Blocks {
   int64_t pages, per_block;                 // per_block a multiple of kCountBlock
   int count;
+  __device__ __forceinline__ int64_t begin(int b) const { return int64_t(b) * per_block; }
+  __device__ __forceinline__ int64_t end(int b) const { return min(pages, int64_t(b + 1) * per_block); }
 };
 
-// Calls f(page, ref) for this thread's pages of block b, 16 consecutive ones of each 4096.
-template <class F>
-__device__ __forceinline__ void each_run(const Blocks& k, const int32_t* refs, int b, F f) {
-  for (int64_t at = int64_t(b) * k.per_block; at < std::min(k.pages, int64_t(b + 1) * k.per_block); at += kCountBlock) {
-    const int64_t p = at + threadIdx.x * kPerThread;
-    int32_t r[kPerThread];
-    if (p + kPerThread <= k.pages) {
+// Keeps loads where they are asked for: without it they move down to where each value is first needed, and each waits.
+template <int N>
+__device__ __forceinline__ void hold(int32_t (&r)[N]) {
 #pragma unroll
-      for (int i = 0; i < kPerThread; ++i) r[i] = refs[p + i];
-    } else {
+  for (int k = 0; k < N; ++k) asm volatile("" : "+v"(r[k]));
+}
+
+// A run: 1024 pages in a row of a wave, lane l with those at 64 k + l (so that loads and stores are of whole lines, and
+// a ballot counts 64 pages).  Pages behind the pool read as `other`.
+struct Run {
+  uint32_t at;                              // below 2^31 + 2^14
+  int32_t r[kPerThread];
+  __device__ __forceinline__ void load(const int32_t* refs, int64_t first, int64_t pages, int32_t other) {
+    at = uint32_t(first) + (threadIdx.x >> 6) * (64 * kPerThread) + (threadIdx.x & 63u);
+    if (pages == 0) {
 #pragma unroll
-      for (int i = 0; i < kPerThread; ++i) r[i] = p + i < k.pages ? refs[p + i] : 0;
+      for (int k = 0; k < kPerThread; ++k) r[k] = other;
+      return;
     }
-    f(p, r);
+    // without a condition on a lane, so that all sixteen are in flight
+    const uint32_t wave_at = uint32_t(uniform(int(at)));
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      r[k] = other;
+      if (wave_at + 64 * k < pages) r[k] = refs[min(int64_t(at + 64 * k), pages - 1)];
+    }
+    hold(r);
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) r[k] = at + 64 * k < pages ? r[k] : other;
   }
+  template <class P>
+  __device__ __forceinline__ int count(P p) const {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) n += __popcll(__ballot(p(r[k])));
+    return n;
+  }
+  // Calls f(k, page, how many pages before it p holds for), with `before` of them before this wave's run.
+  template <class P, class F>
+  __device__ __forceinline__ void each(int before, P p, F f) const {
+    const uint64_t below = (uint64_t(1) << (threadIdx.x & 63u)) - 1;
+#pragma unroll
+    for (int k = 0; k < kPerThread; ++k) {
+      const uint64_t mask = __ballot(p(r[k]));
+      f(k, at + 64 * k, before + __popcll(mask & below));
+      before += __popcll(mask);
+    }
+  }
+};
+
+__device__ __forceinline__ bool is_free(int32_t n) { return n == 0; }
+__device__ __forceinline__ bool is_used(int32_t n) { return n != 0; }
+
+// Sum of the waves' counts before this wave's, and of all.
+template <int W>
+__device__ __forceinline__ int waves_before(int n, int& total) {
+  __shared__ int part[W];
+  const int w = threadIdx.x >> 6;
+  __syncthreads();
+  if ((threadIdx.x & 63u) == 0) part[w] = n;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (i < w) before += part[i];
+    total += part[i];
+  }
+  return before;
 }
 
 // ---------------------------------------------------------------------------
@@ -241,21 +320,23 @@ __device__ __forceinline__ int row_length(const ForkArgs& g, int64_t row) {
   return min(max(g.lens[row], 0), g.cols * g.shape.page);
 }
 
-__device__ __forceinline__ Child child_of(const ForkArgs& g, int64_t i) {
+// The child of row `row` (-1: none) of length `had`, with new tokens from lo up to hi.
+__device__ __forceinline__ Child child_of(const ForkArgs& g, int64_t row, int had, int64_t lo, int64_t hi) {
   Child c;
-  c.row = g.parents ? int64_t(g.parents[i]) : i;
-  if (c.row < 0 || c.row >= g.rows) c.row = -1;
-  c.had = c.row < 0 ? 0 : row_length(g, c.row);
-  c.from = c.fresh = 0;
-  if (g.cu) {
-    const int64_t lo = min(max(int64_t(g.cu[i]), int64_t(0)), g.tokens);
-    const int64_t hi = min(max(int64_t(g.cu[i + 1]), lo), g.tokens);
-    c.from = int(lo);
-    c.fresh = int(hi - lo);
-  }
+  c.row = row;
+  c.had = had;
+  lo = min(max(lo, int64_t(0)), g.tokens);
+  c.from = int(lo);
+  c.fresh = int(min(max(hi, lo), g.tokens) - lo);
   c.held = (c.had + g.shape.page - 1) / g.shape.page;
   c.partly = c.had % g.shape.page;
   return c;
+}
+
+__device__ __forceinline__ Child child_of(const ForkArgs& g, int64_t i) {
+  int64_t row = g.parents ? int64_t(g.parents[i]) : i;
+  if (row < 0 || row >= g.rows) row = -1;
+  return child_of(g, row, row < 0 ? 0 : row_length(g, row), g.cu ? g.cu[i] : 0, g.cu ? g.cu[i + 1] : 0);
 }
 
 __device__ __forceinline__ bool in_pool(const ForkArgs& g, int32_t page) { return page >= 0 && page < g.pages; }
@@ -300,19 +381,16 @@ __global__ __launch_bounds__(256) void fork_counts_kernel(const ForkArgs g) {
 __global__ __launch_bounds__(256) void fork_needs_kernel(const ForkArgs g) {
   if (int(blockIdx.x) >= g.child_blocks) {
     const int b = blockIdx.x - g.child_blocks;
-    int n = 0;
+    int n = 0, total;
     // without parents and with the rows released the counts stay, and are copied here
     const bool copy = !g.parents && g.release && g.refs_out != g.refs;
-    each_run(g.blocks, copy ? g.refs : g.refs_out, b, [&](int64_t p, const int32_t(&r)[kPerThread]) {
-#pragma unroll
-      for (int i = 0; i < kPerThread; ++i)
-        if (p + i < g.pages) {
-          n += r[i] == 0;
-          if (copy) g.refs_out[p + i] = r[i];
-        }
-    });
-    int total;
-    block_scan(n, total);
+    for (int64_t at = g.blocks.begin(b); at < g.blocks.end(b); at += kCountBlock) {
+      Run run;
+      run.load(copy ? g.refs : g.refs_out, at, g.pages, 1);
+      n += run.count(is_free);
+      if (copy) run.each(0, is_free, [&](int k, uint32_t page, int) { if (page < g.pages) g.refs_out[page] = run.r[k]; });
+    }
+    waves_before<4>(n, total);
     if (threadIdx.x == 0) g.block_free[b] = total;
     return;
   }
@@ -352,21 +430,18 @@ __global__ __launch_bounds__(256) void fork_needs_kernel(const ForkArgs g) {
 __global__ __launch_bounds__(256) void fork_list_kernel(const ForkArgs g) {
   if (int(blockIdx.x) >= g.child_blocks) {
     const int b = blockIdx.x - g.child_blocks;
-    int64_t all, rank = sum_before<int64_t>(g.block_free, g.blocks.count, b, all);
+    int all, rank = sum_before<int>(g.block_free, g.blocks.count, b, all);
     if (rank >= g.capacity) return;
-    each_run(g.blocks, g.refs_out, b, [&](int64_t p, const int32_t(&r)[kPerThread]) {
-      int n = 0, total;
-#pragma unroll
-      for (int i = 0; i < kPerThread; ++i) n += p + i < g.pages && r[i] == 0;
-      int64_t at = rank + block_scan(n, total);
-#pragma unroll
-      for (int i = 0; i < kPerThread; ++i)
-        if (p + i < g.pages && r[i] == 0) {
-          if (at < g.capacity) g.list[at] = int32_t(p + i);
-          ++at;
-        }
+    for (int64_t at = g.blocks.begin(b); at < g.blocks.end(b); at += kCountBlock) {
+      Run run;
+      run.load(g.refs_out, at, g.pages, 1);
+      int total;
+      const int before = waves_before<4>(run.count(is_free), total);
+      run.each(rank + before, is_free, [&](int k, uint32_t page, int nth) {
+        if (run.r[k] == 0 && nth < g.capacity) g.list[nth] = int32_t(page);
+      });
       rank += total;
-    });
+    }
     return;
   }
   int64_t all_free, all_needed;
@@ -390,6 +465,112 @@ __global__ __launch_bounds__(256) void fork_list_kernel(const ForkArgs g) {
     const int32_t tail = g.table[c.row * g.stride + c.held - 1];
     g.copy[nth] = make_int4(fits ? tail : -1, fits ? int(start) : 0, (c.partly + 15) / 16 * 16, 0);
   }
+}
+
+// Small pools: one workgroup of 16 waves plans alone, with the counts in LDS, instead of five launches behind each other.
+constexpr int kSmallPages = 16384, kSmallRows = 1024, kSmallEntries = 8192;
+
+// Entries of a table, eight of a thread at once; read before it is known which of them count.
+struct Entries {
+  int32_t page[8];
+  __device__ __forceinline__ static int row_of(int e, int cols, float inv) {
+    int row = int(float(e) * inv);          // off by one at most: e < 2^16
+    if (row * cols > e) --row;
+    if ((row + 1) * cols <= e) ++row;
+    return row;
+  }
+  __device__ __forceinline__ void load(const int32_t* table, int64_t stride, int base, int entries, int cols, float inv) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      page[u] = -1;
+      if (base + u * 1024 + uniform(int(threadIdx.x & ~63u)) >= entries) continue;
+      const int e = min(base + u * 1024 + int(threadIdx.x), entries - 1);
+      const int row = row_of(e, cols, inv);
+      page[u] = table[row * stride + e - row * cols];
+    }
+    hold(page);
+  }
+  // Adds weight[r] to the counts of the entries [from[r], to[r]) of every row r.
+  __device__ __forceinline__ void add(int32_t* count, int pages, int base, int entries, int cols, float inv,
+                                      const int32_t* weight, const int32_t* from, const int32_t* to) const {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int e = base + u * 1024 + int(threadIdx.x);
+      if (e >= entries || page[u] < 0 || page[u] >= pages) continue;
+      const int row = row_of(e, cols, inv), j = e - row * cols;
+      if (weight[row] != 0 && j >= from[row] && j < to[row]) atomicAdd(&count[page[u]], weight[row]);
+    }
+  }
+};
+
+__global__ __launch_bounds__(1024) void fork_small_kernel(const ForkArgs g) {
+  __shared__ int32_t count[kSmallPages];
+  __shared__ int32_t kids[kSmallRows], zero[kSmallRows], length[kSmallRows], held[kSmallRows], writers[kSmallRows],
+      first[kSmallRows];
+  const int t = threadIdx.x, pages = int(g.pages), entries = int(g.rows) * g.cols;
+  const float inv = g.cols ? 1.0f / float(g.cols) : 0.0f;
+  const bool alone = !g.parents && g.release;             // every row goes on: no count changes but by copies
+  // all that is read at places known beforehand
+  Run run;
+  run.load(g.refs, 0, pages, 1);
+  Entries some;
+  if (!alone && entries) some.load(g.table, g.stride, 0, entries, g.cols, inv);
+  const bool is_child = t < g.children;
+  int64_t parent = is_child ? g.parents ? int64_t(g.parents[t]) : t : -1;
+  if (parent < 0 || parent >= g.rows) parent = -1;
+  int64_t lo = 0, hi = 0;
+  if (is_child && g.cu) {
+    lo = g.cu[t];
+    hi = g.cu[t + 1];
+  }
+  const int mine = t < g.rows ? row_length(g, t) : 0;
+  run.each(0, is_free, [&](int k, uint32_t page, int) { count[page] = run.r[k]; });
+  kids[t] = g.release ? -1 : 0;
+  zero[t] = writers[t] = 0;
+  first[t] = INT32_MAX;
+  length[t] = mine;
+  held[t] = (mine + g.shape.page - 1) / g.shape.page;
+  __syncthreads();
+  const Child c = child_of(g, parent, parent < 0 ? 0 : length[parent], lo, hi);
+  int32_t tail = -1;
+  if (c.fresh && c.partly) tail = g.table[c.row * g.stride + c.held - 1];
+  if (c.row >= 0) {
+    atomicAdd(&kids[c.row], 1);
+    if (c.fresh && c.partly) {
+      atomicAdd(&writers[c.row], 1);
+      atomicMin(&first[c.row], t);
+    }
+  }
+  __syncthreads();
+  if (!alone) {
+    for (int base = 0; base < entries; base += 8 * 1024) {
+      if (base) some.load(g.table, g.stride, base, entries, g.cols, inv);
+      some.add(count, pages, base, entries, g.cols, inv, kids, zero, held);
+    }
+    __syncthreads();
+  }
+  // pages that each child needs
+  const int64_t after = (int64_t(c.had) + c.fresh + g.shape.page - 1) / g.shape.page;
+  const bool wide = after > g.out_cols;
+  const bool copy = !wide && in_pool(g, tail) && !(count[tail] == writers[c.row] && first[c.row] == t);
+  const int64_t need = wide ? 0 : after - c.held + copy;
+  int64_t sums;                             // of pages, and of copies in the lowest bits (1024 at most)
+  const int64_t both = block_scan<16>(need * 2048 + copy, sums);
+  const int64_t start = both >> 11;
+  const int nth = int(both & 2047), copies = int(sums & 2047);
+  int all_free;
+  run.each(0, is_free, [&](int k, uint32_t page, int) { run.r[k] = count[page]; });
+  const int before = waves_before<16>(run.count(is_free), all_free);
+  run.each(before, is_free, [&](int k, uint32_t page, int rank) {
+    if (run.r[k] == 0 && rank < g.capacity) g.list[rank] = int32_t(page);
+    if (page < pages && (g.refs_out != g.refs || !alone)) g.refs_out[page] = run.r[k];
+  });
+  if (t == 0) *g.copies = copies;
+  if (!is_child) return;
+  const bool fits = c.fresh && !wide && (need == 0 || start + need <= min(int64_t(all_free), g.capacity));
+  g.info[t] = int(2 * need + copy);
+  g.start[t] = fits ? start : -1;
+  if (copy) g.copy[nth] = make_int4(fits ? tail : -1, fits ? int(start) : 0, (c.partly + 15) / 16 * 16, 0);
 }
 
 // A workgroup for each child writes its row of the table, its slots and the counts of its pages; the workgroups
@@ -490,6 +671,35 @@ __global__ __launch_bounds__(256) void free_pages_kernel(const FreeArgs g) {
   }
 }
 
+// Small pools: one launch, with the counts in LDS.
+__global__ __launch_bounds__(1024) void free_small_kernel(const FreeArgs g) {
+  __shared__ int32_t count[kSmallPages];
+  __shared__ int32_t minus[kSmallRows], from[kSmallRows], to[kSmallRows];
+  const int t = threadIdx.x, pages = int(g.pages), entries = int(g.rows) * g.cols;
+  const float inv = g.cols ? 1.0f / float(g.cols) : 0.0f;
+  Run run;
+  run.load(g.refs, 0, pages, 1);
+  Entries some;
+  if (entries) some.load(g.table, g.stride, 0, entries, g.cols, inv);
+  int left = 0;
+  if (t < g.rows) {
+    const int had = min(max(g.lens[t], 0), g.cols * g.page);
+    left = kept_tokens(g, t, had);
+    minus[t] = -1;
+    from[t] = (left + g.page - 1) / g.page;
+    to[t] = (had + g.page - 1) / g.page;
+  }
+  run.each(0, is_free, [&](int k, uint32_t page, int) { count[page] = run.r[k]; });
+  __syncthreads();
+  for (int base = 0; base < entries; base += 8 * 1024) {
+    if (base) some.load(g.table, g.stride, base, entries, g.cols, inv);
+    some.add(count, pages, base, entries, g.cols, inv, minus, from, to);
+  }
+  __syncthreads();
+  run.each(0, is_free, [&](int, uint32_t page, int) { if (page < pages) g.refs_out[page] = count[page]; });
+  if (t < g.rows) g.lens_out[t] = left;
+}
+
 // Lengths changed in place change after every workgroup has read them.
 __global__ __launch_bounds__(256) void free_lens_kernel(const FreeArgs g) {
   const int64_t row = int64_t(blockIdx.x) * 256 + threadIdx.x;
@@ -518,47 +728,64 @@ struct CompactArgs {
 
 __global__ __launch_bounds__(256) void compact_count_kernel(const CompactArgs g) {
   int n = 0, total;
-  each_run(g.blocks, g.refs, blockIdx.x, [&](int64_t, const int32_t(&r)[kPerThread]) {
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) n += r[i] != 0;
-  });
-  block_scan(n, total);
+  for (int64_t at = g.blocks.begin(blockIdx.x); at < g.blocks.end(blockIdx.x); at += kCountBlock) {
+    Run run;
+    run.load(g.refs, at, g.pages, 0);
+    n += run.count(is_used);
+  }
+  waves_before<4>(n, total);
   if (threadIdx.x == 0) g.block_used[blockIdx.x] = total;
 }
 
+// What becomes of a page with count `count` and u used ones before it.
+__device__ __forceinline__ void compact_page(const CompactArgs& g, int page, int32_t count, int u, int used) {
+  const bool live = count != 0;
+  if (page < used) {
+    if (!live) g.hole[page - u] = int32_t(page);
+    else g.refs_out[page] = count;                         // a hole's count comes with its page
+  } else {
+    g.nth[page] = live ? int32_t(used - 1 - u) : -1;
+    if (live) {
+      g.mover[used - 1 - u] = int32_t(page);
+      g.mover_refs[used - 1 - u] = count;
+    }
+    g.refs_out[page] = 0;
+  }
+  if (page == used - 1) *g.moves = int32_t(used - u - live);
+}
+
 __global__ __launch_bounds__(256) void compact_plan_kernel(const CompactArgs g) {
-  int64_t used, before = sum_before<int64_t>(g.block_used, g.blocks.count, blockIdx.x, used);
+  int used, before = sum_before<int>(g.block_used, g.blocks.count, blockIdx.x, used);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *g.used = int32_t(used);
+    *g.used = used;
     if (used == 0) *g.moves = 0;
   }
-  each_run(g.blocks, g.refs, blockIdx.x, [&](int64_t p, const int32_t(&r)[kPerThread]) {
-    int n = 0, total;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) n += r[i] != 0;
-    int64_t u = before + block_scan(n, total);
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int64_t page = p + i;
-      if (page < g.pages) {
-        const bool live = r[i] != 0;
-        if (page < used) {
-          if (!live) g.hole[page - u] = int32_t(page);
-          else g.refs_out[page] = r[i];                    // a hole's count comes with its page
-        } else {
-          g.nth[page] = live ? int32_t(used - 1 - u) : -1;
-          if (live) {
-            g.mover[used - 1 - u] = int32_t(page);
-            g.mover_refs[used - 1 - u] = r[i];
-          }
-          g.refs_out[page] = 0;
-        }
-        if (page == used - 1) *g.moves = int32_t(used - u - live);
-        u += live;
-      }
-    }
+  for (int64_t at = g.blocks.begin(blockIdx.x); at < g.blocks.end(blockIdx.x); at += kCountBlock) {
+    Run run;
+    run.load(g.refs, at, g.pages, 0);
+    int total;
+    const int first = waves_before<4>(run.count(is_used), total);
+    run.each(before + first, is_used, [&](int k, uint32_t page, int u) {
+      if (page < g.pages) compact_page(g, page, run.r[k], u, used);
+    });
     before += total;
+  }
+}
+
+// Small pools: count and plan in one launch.
+__global__ __launch_bounds__(1024) void compact_small_kernel(const CompactArgs g) {
+  const int t = threadIdx.x;
+  Run run;
+  run.load(g.refs, 0, g.pages, 0);
+  int used;
+  const int before = waves_before<16>(run.count(is_used), used);
+  run.each(before, is_used, [&](int k, uint32_t page, int u) {
+    if (page < g.pages) compact_page(g, page, run.r[k], u, used);
   });
+  if (t == 0) {
+    *g.used = used;
+    if (used == 0) *g.moves = 0;
+  }
 }
 
 __global__ __launch_bounds__(256) void compact_move_kernel(const CompactArgs g) {
@@ -637,6 +864,10 @@ Items items_of(const mx_kv_cache_t& c, int layers) {
   return it;
 }
 
+// LDS that nothing uses: it keeps the copying workgroups to two on a CU, with which the memory does more (1.1 GB read and
+// written: 213 us, with eight 218; 1.0 GB moved in a pool: 178 and 188).
+constexpr size_t kTwoOnACu = 80000;
+
 // Workgroups of four waves for `copies` copies, which walk the work where there are more than 64 for each CU.
 unsigned copy_grid(int64_t copies, const Items& it) {
   const int64_t cus = std::max<int64_t>(device_cus(), 1);
@@ -666,6 +897,11 @@ struct Space {
 };
 
 constexpr int64_t kMostRows = int64_t(1) << 20;
+
+// Whether one workgroup holds the counts of a pool and reads a table in a few steps.
+bool is_small(int64_t pages, int64_t rows, int64_t cols) {
+  return pages <= kSmallPages && rows <= kSmallRows && rows * cols <= kSmallEntries;
+}
 
 // Pages that all children together can need: a copy and a started page each, and one a page's worth of new tokens.
 int64_t fork_capacity(int64_t pages, int64_t children, int64_t tokens, int page) {
@@ -741,7 +977,7 @@ extern "C" mx_status_t mx_kv_copy(const mx_kv_cache_t* src, const mx_kv_cache_t*
     g.dst_pages = dst->pages;
     g.shape = shape_of(*src);
     g.items = items_of(*src, n);
-    page_copy_kernel<<<copy_grid(count, g.items), 256, 0, stream>>>(g);
+    page_copy_kernel<<<copy_grid(count, g.items), 256, kTwoOnACu, stream>>>(g);
   }
   return launched();
 }
@@ -791,7 +1027,11 @@ extern "C" mx_status_t mx_kv_fork(const mx_kv_cache_t* caches, int layers, const
   g.cols = int(table_cols); g.out_cols = int(out_cols); g.release = release != 0;
   g.shape = shape_of(*caches);
   const int64_t cus = std::max<int64_t>(device_cus(), 1);
-  if (parents || !release) {
+  const bool small = is_small(g.pages, rows, table_cols) && children <= kSmallRows;
+  const unsigned both = unsigned(g.child_blocks + g.blocks.count);
+  if (small) {
+    fork_small_kernel<<<1, 1024, 0, stream>>>(g);
+  } else if (parents || !release) {
     const int64_t n = std::max(rows, refs_out != refs ? g.pages : 0);
     if (n) fork_init_kernel<<<unsigned(std::min(8 * cus, (n + 255) / 256)), 256, 0, stream>>>(g);
     if (children) fork_kids_kernel<<<unsigned(g.child_blocks), 256, 0, stream>>>(g);
@@ -801,10 +1041,9 @@ extern "C" mx_status_t mx_kv_fork(const mx_kv_cache_t* caches, int layers, const
       fork_counts_kernel<<<dim3(unsigned(x), unsigned(y)), 256, 0, stream>>>(g);
     }
   }
-  const unsigned both = unsigned(g.child_blocks + g.blocks.count);
-  if (both) fork_needs_kernel<<<both, 256, 0, stream>>>(g);
+  if (!small && both) fork_needs_kernel<<<both, 256, 0, stream>>>(g);
   if (children == 0) return launched();
-  fork_list_kernel<<<both, 256, 0, stream>>>(g);
+  if (!small) fork_list_kernel<<<both, 256, 0, stream>>>(g);
   for (int l = 0; l < layers; l += kLayersPerLaunch) {
     const int n = std::min(kLayersPerLaunch, layers - l);
     fill_layers(g.caches, caches + l, n);
@@ -827,6 +1066,10 @@ extern "C" mx_status_t mx_kv_free(const int32_t* refs, int64_t pages, int page, 
   if (off4(refs) || off4(refs_out) || off4(lens) || off4(lens_out) || off4(page_table) || off4(keep)) return MX_ERR_ALIGN;
   if (rows == 0 && (pages == 0 || refs_out == refs)) return MX_OK;
   FreeArgs g = {refs, page_table, lens, keep, refs_out, lens_out, pages, table_stride, rows, int(table_cols), page};
+  if (refs_out != refs && is_small(pages, rows, table_cols)) {
+    free_small_kernel<<<1, 1024, 0, stream>>>(g);
+    return launched();
+  }
   const int64_t cus = std::max<int64_t>(device_cus(), 1);
   if (refs_out != refs && pages)
     refs_copy_kernel<<<unsigned(std::min(8 * cus, (pages + 255) / 256)), 256, 0, stream>>>(refs, refs_out, pages);
@@ -877,15 +1120,19 @@ extern "C" mx_status_t mx_kv_compact(const mx_kv_cache_t* caches, int layers, co
   g.stride = table_stride; g.rows = rows; g.cols = int(table_cols);
   g.shape = shape_of(*caches);
   const int64_t cus = std::max<int64_t>(device_cus(), 1);
-  if (g.blocks.count) compact_count_kernel<<<unsigned(g.blocks.count), 256, 0, stream>>>(g);
-  compact_plan_kernel<<<unsigned(std::max(1, g.blocks.count)), 256, 0, stream>>>(g);
+  if (g.pages <= kSmallPages) {
+    compact_small_kernel<<<1, 1024, 0, stream>>>(g);
+  } else {
+    compact_count_kernel<<<unsigned(g.blocks.count), 256, 0, stream>>>(g);
+    compact_plan_kernel<<<unsigned(g.blocks.count), 256, 0, stream>>>(g);
+  }
   for (int l = 0; l < layers; l += kLayersPerLaunch) {
     const int n = std::min(kLayersPerLaunch, layers - l);
     fill_layers(g.caches, caches + l, n);
     g.items = items_of(*caches, n);
     const unsigned copiers = g.pages > 1 ? copy_grid(g.pages / 2, g.items) : 0;
     g.table_blocks = l == 0 ? std::max<int64_t>(1, std::min(4 * cus, std::max(rows, g.pages / 2048))) : 0;
-    if (g.table_blocks + copiers) compact_move_kernel<<<unsigned(g.table_blocks) + copiers, 256, 0, stream>>>(g);
+    if (g.table_blocks + copiers) compact_move_kernel<<<unsigned(g.table_blocks) + copiers, 256, kTwoOnACu, stream>>>(g);
   }
   return launched();
 }
