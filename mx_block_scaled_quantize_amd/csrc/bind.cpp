@@ -12,7 +12,9 @@
 #include <torch/csrc/utils/object_ptr.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/Allocator.h>
 #include <c10/hip/HIPStream.h>
 
 #include <cmath>
@@ -335,12 +337,19 @@ int64_t vector_size(const at::Tensor& t, const char* name) {
   return t.size(0);
 }
 
+// A new tensor on the current device, made without the dispatcher's way to the same allocator: these calls make up to
+// seven.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType dt) {
+  return at::detail::empty_generic(shape, c10::GetAllocator(at::kCUDA), c10::DispatchKeySet(c10::DispatchKey::CUDA), dt,
+                                   std::nullopt);
+}
+
 // The n-th of the tensors to write to, or a new one.
 at::Tensor out_or_new(PyObject* out, Py_ssize_t n, const char* name, at::IntArrayRef shape, at::ScalarType dt,
-                      const at::TensorOptions& like) {
-  if (out == Py_None) return at::empty(shape, like.dtype(dt));
+                      const at::Device& dev) {
+  if (out == Py_None) return fresh(shape, dt);
   const at::Tensor& t = tensor(PyTuple_GET_ITEM(out, n), name);
-  TORCH_CHECK_VALUE(t.sizes() == shape && t.scalar_type() == dt && t.is_contiguous() && t.device() == like.device(), name,
+  TORCH_CHECK_VALUE(t.sizes() == shape && t.scalar_type() == dt && t.is_contiguous() && t.device() == dev, name,
                     " must be a contiguous ", dt, " tensor of shape ", shape, " on the device of the other arguments");
   return t;
 }
@@ -424,12 +433,11 @@ PyObject* kv_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
   OnDevice on(dev);
   int64_t need = 0;
   check_status(mx_kv_fork_workspace(pages, rows, children, tokens, caches[0].page, &need));
-  const at::TensorOptions like = refs.options();
-  at::Tensor r = out_or_new(out, 0, "out's refs", {pages}, at::kInt, like),
-             t = out_or_new(out, 1, "out's page_table", {children, cols}, at::kInt, like),
-             l = out_or_new(out, 2, "out's lens", {children}, at::kInt, like),
-             s = out_or_new(out, 3, "out's slots", {tokens}, at::kLong, like),
-             space = at::empty({need}, like.dtype(at::kByte));
+  at::Tensor r = out_or_new(out, 0, "out's refs", {pages}, at::kInt, dev),
+             t = out_or_new(out, 1, "out's page_table", {children, cols}, at::kInt, dev),
+             l = out_or_new(out, 2, "out's lens", {children}, at::kInt, dev),
+             s = out_or_new(out, 3, "out's slots", {tokens}, at::kLong, dev),
+             space = fresh({need}, at::kByte);
   // a parents tensor without elements has no address, which would stand for children that continue their own rows
   if (a[5] != Py_None && children == 0) parents = ints(refs);
   check_status(mx_kv_fork(caches.data(), layer_count(caches), ints(refs), ints(table), row_stride(table), table.size(1),
@@ -457,8 +465,8 @@ PyObject* kv_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   check_out_tuple(a[5], 2);
   OnDevice on(dev);
-  at::Tensor r = out_or_new(a[5], 0, "out's refs", {pages}, at::kInt, refs.options()),
-             l = out_or_new(a[5], 1, "out's lens", {rows}, at::kInt, refs.options());
+  at::Tensor r = out_or_new(a[5], 0, "out's refs", {pages}, at::kInt, dev),
+             l = out_or_new(a[5], 1, "out's lens", {rows}, at::kInt, dev);
   check_status(mx_kv_free(ints(refs), pages, narrow_int(integer(a[3]), "page"), ints(table), row_stride(table),
                           table.size(1), ints(lens), rows, keep, ints_out(r), ints_out(l), on.stream));
   return wrapped({r, l});
@@ -480,10 +488,9 @@ PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   OnDevice on(dev);
   int64_t need = 0;
   check_status(mx_kv_compact_workspace(pages, &need));
-  const at::TensorOptions like = refs.options();
-  at::Tensor r = out_or_new(a[4], 0, "out's refs", {pages}, at::kInt, like),
-             t = out_or_new(a[4], 1, "out's page_table", table.sizes(), at::kInt, like),
-             u = out_or_new(a[4], 2, "out's count", {1}, at::kInt, like), space = at::empty({need}, like.dtype(at::kByte));
+  at::Tensor r = out_or_new(a[4], 0, "out's refs", {pages}, at::kInt, dev),
+             t = out_or_new(a[4], 1, "out's page_table", table.sizes(), at::kInt, dev),
+             u = out_or_new(a[4], 2, "out's count", {1}, at::kInt, dev), space = fresh({need}, at::kByte);
   check_status(mx_kv_compact(caches.data(), layer_count(caches), ints(refs), ints(table), row_stride(table), table.size(1),
                              ints(lens), rows, ints_out(r), ints_out(t), ints_out(u), space.data_ptr(), need, on.stream));
   return wrapped({r, t, u});
@@ -531,13 +538,12 @@ PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   OnDevice on(dev);
   int64_t need = 0;
   check_status(mx_beam_select_workspace(requests, beams, x.size(2), width, &need));
-  const at::TensorOptions like = scores.options(), whole = like.dtype(at::kInt);
-  at::Tensor s = at::empty({requests, width}, like), p = at::empty({requests, width}, whole),
-             t = at::empty({requests, width}, whole), f = at::empty({requests, width}, like.dtype(at::kBool)), h, l,
-             space = at::empty({need}, like.dtype(at::kByte));
+  at::Tensor s = fresh({requests, width}, at::kFloat), p = fresh({requests, width}, at::kInt),
+             t = fresh({requests, width}, at::kInt), f = fresh({requests, width}, at::kBool), h, l,
+             space = fresh({need}, at::kByte);
   if (a[6] != Py_None) {
-    h = at::empty({requests, width, cols}, whole);
-    l = at::empty({requests, width}, whole);
+    h = fresh({requests, width, cols}, at::kInt);
+    l = fresh({requests, width}, at::kInt);
   }
   check_status(mx_beam_select(x.data_ptr(), dt, requests, beams, x.size(2), stride_of(x, 0), stride_of(x, 1),
                               static_cast<const float*>(scores.data_ptr()), finished, width, eos, pad, history, lens, cols,

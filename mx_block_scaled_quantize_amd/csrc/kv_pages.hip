@@ -341,6 +341,39 @@ __device__ __forceinline__ Child child_of(const ForkArgs& g, int64_t i) {
 
 __device__ __forceinline__ bool in_pool(const ForkArgs& g, int32_t page) { return page >= 0 && page < g.pages; }
 
+// The rows' children, counted in LDS by the first workgroup, while the others copy the counts of pages.
+constexpr int kBeginRows = 4096, kBeginChildren = 16384;
+
+__global__ __launch_bounds__(1024) void fork_begin_kernel(const ForkArgs g) {
+  __shared__ int32_t kids[kBeginRows], writers[kBeginRows], first[kBeginRows];
+  if (blockIdx.x > 0) {
+    const int64_t step = int64_t(gridDim.x - 1) * 1024;
+    for (int64_t i = int64_t(blockIdx.x - 1) * 1024 + threadIdx.x; i < g.pages; i += step) g.refs_out[i] = g.refs[i];
+    return;
+  }
+  for (int i = threadIdx.x; i < g.rows; i += 1024) {
+    kids[i] = writers[i] = 0;
+    first[i] = INT32_MAX;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < g.children; i += 1024) {
+    const Child c = child_of(g, i);
+    if (c.row < 0) continue;
+    atomicAdd(&kids[c.row], 1);
+    if (c.fresh && c.partly) {
+      atomicAdd(&writers[c.row], 1);
+      atomicMin(&first[c.row], i);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < g.rows; i += 1024) {
+    g.kids[i] = kids[i];
+    g.writers[i] = writers[i];
+    g.first[i] = first[i];
+  }
+}
+
+// The same where there are more rows or children, in two launches.
 __global__ __launch_bounds__(256) void fork_init_kernel(const ForkArgs g) {
   const int64_t step = int64_t(gridDim.x) * 256;
   const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
@@ -1032,9 +1065,13 @@ extern "C" mx_status_t mx_kv_fork(const mx_kv_cache_t* caches, int layers, const
   if (small) {
     fork_small_kernel<<<1, 1024, 0, stream>>>(g);
   } else if (parents || !release) {
-    const int64_t n = std::max(rows, refs_out != refs ? g.pages : 0);
-    if (n) fork_init_kernel<<<unsigned(std::min(8 * cus, (n + 255) / 256)), 256, 0, stream>>>(g);
-    if (children) fork_kids_kernel<<<unsigned(g.child_blocks), 256, 0, stream>>>(g);
+    const int64_t copied = refs_out != refs ? g.pages : 0, n = std::max(rows, copied);
+    if (rows <= kBeginRows && children <= kBeginChildren) {
+      fork_begin_kernel<<<unsigned(1 + std::min(2 * cus, (copied + 1023) / 1024)), 1024, 0, stream>>>(g);
+    } else {
+      fork_init_kernel<<<unsigned(std::min(8 * cus, (n + 255) / 256)), 256, 0, stream>>>(g);
+      if (children) fork_kids_kernel<<<unsigned(g.child_blocks), 256, 0, stream>>>(g);
+    }
     if (rows && table_cols) {
       // a workgroup a row, several where there are few rows
       const int64_t x = std::min(rows, 8 * cus), y = std::min((table_cols + 255) / 256, std::max<int64_t>(1, 8 * cus / x));
