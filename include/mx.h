@@ -480,6 +480,8 @@ mx_status_t mx_paged_attention_workspace(int64_t tokens, int heads, int kv_heads
  * table_cols * page.  The calls read counts, tables and lengths on the device and wait for
  * nothing; they can be captured.  Which pages a sequence gets depends on these alone: the
  * lowest free ones, in the order of the sequences.
+ * Calls that read or change one pool's counts, tables or pages are ordered by the caller
+ * (one stream, or events).
  * `layers` caches are caches of one shape that share the pool's page numbers, one for each
  * layer of a model.  pages <= 2^31 - 1, rows and children <= 2^20, table_cols * page <=
  * 2^31 - 1, kv_heads * page * dim <= 2^30. */
@@ -528,8 +530,8 @@ mx_status_t mx_kv_fork_workspace(int64_t pages, int64_t rows, int64_t children, 
 
 /* Cuts sequences to keep[r] tokens (those not longer stay; NULL: all end): each page behind
  * the last kept one loses a hold, and is free when none is left.
- *   refs_out, lens_out  counts and lengths after the call; may be refs and lens.
- * Errors: MX_ERR_SHAPE, MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */
+ *   refs_out, lens_out  counts and lengths after the call; may be refs and lens (lens_out not keep).
+ * Errors: MX_ERR_SHAPE, MX_ERR_ARG (lens_out is keep), MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */
 mx_status_t mx_kv_free(const int32_t* refs, int64_t pages, int page, const int32_t* page_table, int64_t table_stride,
                        int64_t table_cols, const int32_t* lens, int64_t rows, const int32_t* keep, int32_t* refs_out,
                        int32_t* lens_out, hipStream_t stream);

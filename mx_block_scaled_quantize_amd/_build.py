@@ -82,8 +82,8 @@ def build(verbose=False):
     # lies beside it
     bind_obj, torch_lib = bind.result()
     tmp = BIND + ".tmp"
-    _run(["g++", "-shared", "-o", tmp, bind_obj, f"-L{PKG}", "-lmx", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu",
-          "-lc10", "-lc10_hip", "-lamdhip64", "-Wl,-rpath,$ORIGIN"], "link of _bind.so")
+    _run(["g++", "-shared", "-o", tmp, bind_obj, f"-L{PKG}", "-lmx", f"-L{torch_lib}", "-ltorch_python", "-ltorch_hip",
+          "-ltorch_cpu", "-lc10", "-lc10_hip", "-lamdhip64", "-Wl,-rpath,$ORIGIN"], "link of _bind.so")
     os.replace(tmp, BIND)
     if verbose:
         print(f"built {LIB} and {BIND}", file=sys.stderr)

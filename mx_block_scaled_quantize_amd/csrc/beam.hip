@@ -336,7 +336,10 @@ __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
 }
 
 // A workgroup for each request, several where long histories are copied (each takes the same decision and copies
-// some of the columns).
+// some of the columns).  A wave for each beam joins its segments; then each candidate counts those better than it.
+// One request of four beams takes 5.6 us, nearly all of it latency: 1.7 for what the first launch left in other XCDs' caches,
+// 1 for a beam's best, 1 for the choice, 1 to 2 for a history; 256 requests of eight beams with histories of 2048
+// tokens (33 MB read and written) 13.  One candidate chosen after the other, by a wave, took 700 clocks each.
 __global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const BeamArgs g) {
   __shared__ uint64_t buffers[kMergeWaves][kBuffer];
   extern __shared__ double score[];         // [beams][keep], and the tokens behind them

@@ -12,9 +12,8 @@
 #include <torch/csrc/utils/object_ptr.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/EmptyTensor.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <ATen/ops/empty.h>
-#include <c10/core/Allocator.h>
 #include <c10/hip/HIPStream.h>
 
 #include <cmath>
@@ -337,17 +336,15 @@ int64_t vector_size(const at::Tensor& t, const char* name) {
   return t.size(0);
 }
 
-// A new tensor on the current device, made without the dispatcher's way to the same allocator: these calls make up to
-// seven.
-at::Tensor fresh(at::IntArrayRef shape, at::ScalarType dt) {
-  return at::detail::empty_generic(shape, c10::GetAllocator(at::kCUDA), c10::DispatchKeySet(c10::DispatchKey::CUDA), dt,
-                                   std::nullopt);
+// A new tensor, made without the dispatcher's way to the same function: these calls make up to seven.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType dt, const at::Device& dev) {
+  return at::detail::empty_cuda(shape, dt, dev, std::nullopt);
 }
 
 // The n-th of the tensors to write to, or a new one.
 at::Tensor out_or_new(PyObject* out, Py_ssize_t n, const char* name, at::IntArrayRef shape, at::ScalarType dt,
                       const at::Device& dev) {
-  if (out == Py_None) return fresh(shape, dt);
+  if (out == Py_None) return fresh(shape, dt, dev);
   const at::Tensor& t = tensor(PyTuple_GET_ITEM(out, n), name);
   TORCH_CHECK_VALUE(t.sizes() == shape && t.scalar_type() == dt && t.is_contiguous() && t.device() == dev, name,
                     " must be a contiguous ", dt, " tensor of shape ", shape, " on the device of the other arguments");
@@ -437,7 +434,7 @@ PyObject* kv_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
              t = out_or_new(out, 1, "out's page_table", {children, cols}, at::kInt, dev),
              l = out_or_new(out, 2, "out's lens", {children}, at::kInt, dev),
              s = out_or_new(out, 3, "out's slots", {tokens}, at::kLong, dev),
-             space = fresh({need}, at::kByte);
+             space = fresh({need}, at::kByte, dev);
   // a parents tensor without elements has no address, which would stand for children that continue their own rows
   if (a[5] != Py_None && children == 0) parents = ints(refs);
   check_status(mx_kv_fork(caches.data(), layer_count(caches), ints(refs), ints(table), row_stride(table), table.size(1),
@@ -490,7 +487,7 @@ PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check_status(mx_kv_compact_workspace(pages, &need));
   at::Tensor r = out_or_new(a[4], 0, "out's refs", {pages}, at::kInt, dev),
              t = out_or_new(a[4], 1, "out's page_table", table.sizes(), at::kInt, dev),
-             u = out_or_new(a[4], 2, "out's count", {1}, at::kInt, dev), space = fresh({need}, at::kByte);
+             u = out_or_new(a[4], 2, "out's count", {1}, at::kInt, dev), space = fresh({need}, at::kByte, dev);
   check_status(mx_kv_compact(caches.data(), layer_count(caches), ints(refs), ints(table), row_stride(table), table.size(1),
                              ints(lens), rows, ints_out(r), ints_out(t), ints_out(u), space.data_ptr(), need, on.stream));
   return wrapped({r, t, u});
@@ -538,12 +535,12 @@ PyObject* beam_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
   OnDevice on(dev);
   int64_t need = 0;
   check_status(mx_beam_select_workspace(requests, beams, x.size(2), width, &need));
-  at::Tensor s = fresh({requests, width}, at::kFloat), p = fresh({requests, width}, at::kInt),
-             t = fresh({requests, width}, at::kInt), f = fresh({requests, width}, at::kBool), h, l,
-             space = fresh({need}, at::kByte);
+  at::Tensor s = fresh({requests, width}, at::kFloat, dev), p = fresh({requests, width}, at::kInt, dev),
+             t = fresh({requests, width}, at::kInt, dev), f = fresh({requests, width}, at::kBool, dev), h, l,
+             space = fresh({need}, at::kByte, dev);
   if (a[6] != Py_None) {
-    h = fresh({requests, width, cols}, at::kInt);
-    l = fresh({requests, width}, at::kInt);
+    h = fresh({requests, width, cols}, at::kInt, dev);
+    l = fresh({requests, width}, at::kInt, dev);
   }
   check_status(mx_beam_select(x.data_ptr(), dt, requests, beams, x.size(2), stride_of(x, 0), stride_of(x, 1),
                               static_cast<const float*>(scores.data_ptr()), finished, width, eos, pad, history, lens, cols,

@@ -88,6 +88,7 @@ free = caller(lib.mx_kv_free, "refs pages page table stride cols lens rows keep 
     (SHAPE, {"rows": -1}), (SHAPE, {"rows": (1 << 20) + 1}), (SHAPE, {"cols": -1}), (SHAPE, {"cols": 1 << 28, "stride": 1 << 28}),
     (SHAPE, {"stride": 2}), (NULL, {"refs": None}), (NULL, {"refs_out": None}), (NULL, {"table": None}), (NULL, {"lens": None}),
     (NULL, {"lens_out": None}), (ALIGN, {"refs": FAKE + 1}), (ALIGN, {"table": FAKE + 2}), (ALIGN, {"keep": FAKE + 2}),
+    (ARG, {"keep": FAKE}),
     (OK, {"rows": 0, "lens": None, "table": None})])
 def test_free(status, kw):
     assert free(**kw) == status
