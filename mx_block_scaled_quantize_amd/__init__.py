@@ -125,7 +125,8 @@ lib.mx_kv_copy.argtypes = [_layers_p, _layers_p, _i32, _p, _p, _i64, _p]
 lib.mx_kv_fork.argtypes = [_layers_p, _i32, _p, _p, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _i32, _p, _p, _i64, _p, _p, _p,
                            _i64, _p]
 lib.mx_kv_fork_workspace.argtypes = [_i64, _i64, _i64, _i64, _i32, ctypes.POINTER(_i64)]
-lib.mx_kv_free.argtypes = [_p, _i64, _i32, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p]
+lib.mx_kv_free.argtypes = [_p, _i64, _i32, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p]
+lib.mx_kv_free_workspace.argtypes = [_i64, _i64, _i64, _i32, ctypes.POINTER(_i64)]
 lib.mx_kv_compact.argtypes = [_layers_p, _i32, _p, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p]
 lib.mx_kv_compact_workspace.argtypes = [_i64, ctypes.POINTER(_i64)]
 lib.mx_beam_select.argtypes = [_p, _i32, _i64, _i64, _i64, _i64, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _i64, _p, _p, _p, _p,
@@ -135,7 +136,7 @@ lib.mx_paged_attention_workspace.argtypes = [_i64, _i32, _i32, _i32, _i64, _i64,
 for _f in (lib.mx_quantize, lib.mx_quantize_dual, lib.fp8_quantize_delayed, lib.mx_dequantize, lib.mx_gemm,
            lib.mx_quantize_sr, lib.mm_fp8, lib.mx_gemm_requant, lib.fp8_quantize_delayed_static, lib.mx_rope_table,
            lib.mx_rope, lib.mx_kv_append, lib.mx_paged_attention, lib.mx_paged_attention_workspace, lib.mx_kv_copy,
-           lib.mx_kv_fork, lib.mx_kv_fork_workspace, lib.mx_kv_free, lib.mx_kv_compact, lib.mx_kv_compact_workspace,
+           lib.mx_kv_fork, lib.mx_kv_fork_workspace, lib.mx_kv_free, lib.mx_kv_free_workspace, lib.mx_kv_compact, lib.mx_kv_compact_workspace,
            lib.mx_beam_select, lib.mx_beam_select_workspace):
     _f.restype = ctypes.c_int
 lib.mx_status_str.argtypes = [ctypes.c_int]
@@ -145,7 +146,7 @@ lib.mx_abi_version.restype = ctypes.c_int
 ENTRY_POINTS = ("mx_quantize", "mx_quantize_dual", "fp8_quantize_delayed", "mx_dequantize", "mx_gemm",
                 "mx_quantize_sr", "mm_fp8", "mx_gemm_requant", "fp8_quantize_delayed_static", "mx_rope_table",
                 "mx_rope", "mx_kv_append", "mx_paged_attention", "mx_paged_attention_workspace", "mx_kv_copy",
-                "mx_kv_fork", "mx_kv_fork_workspace", "mx_kv_free", "mx_kv_compact", "mx_kv_compact_workspace",
+                "mx_kv_fork", "mx_kv_fork_workspace", "mx_kv_free", "mx_kv_free_workspace", "mx_kv_compact", "mx_kv_compact_workspace",
                 "mx_beam_select", "mx_beam_select_workspace", "mx_status_str",
                 "mx_abi_version")
 

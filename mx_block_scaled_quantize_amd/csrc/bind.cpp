@@ -464,8 +464,13 @@ PyObject* kv_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
   OnDevice on(dev);
   at::Tensor r = out_or_new(a[5], 0, "out's refs", {pages}, at::kInt, dev),
              l = out_or_new(a[5], 1, "out's lens", {rows}, at::kInt, dev);
-  check_status(mx_kv_free(ints(refs), pages, narrow_int(integer(a[3]), "page"), ints(table), row_stride(table),
-                          table.size(1), ints(lens), rows, keep, ints_out(r), ints_out(l), on.stream));
+  const int page = narrow_int(integer(a[3]), "page");
+  int64_t need = 0;
+  check_status(mx_kv_free_workspace(pages, rows, table.size(1), page, &need));
+  at::Tensor space;
+  if (need) space = fresh({need}, at::kByte, dev);
+  check_status(mx_kv_free(ints(refs), pages, page, ints(table), row_stride(table), table.size(1), ints(lens), rows, keep,
+                          ints_out(r), ints_out(l), need ? space.data_ptr() : nullptr, need, on.stream));
   return wrapped({r, l});
   END_HANDLE_TH_ERRORS
 }

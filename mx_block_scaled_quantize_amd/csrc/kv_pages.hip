@@ -682,6 +682,10 @@ struct FreeArgs {
   int32_t *refs_out, *lens_out;
   int64_t pages, stride, rows;
   int cols, page;
+  // many entries: `tiles` tiles of 8192, buckets of 2^shift pages
+  int tiles, buckets, shift;
+  uint16_t* ends;                           // [tiles][kBuckets + 1]: where a bucket's entries begin in a tile
+  int32_t* sorted;                          // [tiles][8192]: pages that lose a hold, bucket after bucket
 };
 
 __global__ __launch_bounds__(256) void refs_copy_kernel(const int32_t* from, int32_t* to, int64_t n) {
@@ -693,9 +697,8 @@ __device__ __forceinline__ int kept_tokens(const FreeArgs& g, int64_t row, int h
 }
 
 // A workgroup for a row, or for some of its entries.  It is bound by the atomics where the pages of a row lie anywhere:
-// they are worked off behind the L2s, 22 a nanosecond: 790000 entries of 4096 rows over two million pages take 36 us, 3.1
-// million 124.  Of rows whose pages follow each other, 16 counts a line, they take 10 and 16.  Leaving each page to
-// workgroups of one XCD changed nothing.
+// they are worked off behind the L2s, 22 a nanosecond; leaving each page to workgroups of one XCD changed nothing.  So
+// tables of many entries go the way below.
 __global__ __launch_bounds__(256) void free_pages_kernel(const FreeArgs g) {
   for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
     const int had = min(max(g.lens[row], 0), g.cols * g.page), left = kept_tokens(g, row, had);
@@ -705,6 +708,135 @@ __global__ __launch_bounds__(256) void free_pages_kernel(const FreeArgs g) {
       if (page >= 0 && page < g.pages) atomicSub(&g.refs_out[page], 1);
     }
     if (g.lens_out != g.lens && blockIdx.y == 0 && threadIdx.x == 0) g.lens_out[row] = left;
+  }
+}
+
+// Tables of many entries: the pages that lose a hold are put in order of buckets of 2^shift pages, a tile of 8192
+// entries in LDS at a time; then a workgroup for each bucket counts them in LDS and subtracts: no atomics in memory.
+// 4096 rows of 1025 entries over two million pages that lie anywhere, copy of the counts included: 20 us where 790000
+// entries lose a hold, 32 where all 3.1 million do; 38 and 124 by atomics.  Of rows whose pages follow each other, 32 counts
+// a line, 23 and 32, by atomics 10 and 16: pages come in such order from a fresh pool only.
+constexpr int kTile = 8192, kBuckets = 256;
+
+__global__ __launch_bounds__(1024, 8) void free_sort_kernel(const FreeArgs g) {
+  __shared__ int32_t begin[kBuckets + 1];
+  __shared__ int32_t order[kTile];
+  const int t = threadIdx.x;
+  const int64_t base = int64_t(blockIdx.x) * kTile;
+  const int cols = g.cols, last = int(g.rows) - 1, wide = kTile / 8 / cols, rest = kTile / 8 % cols;
+  int at = int((base + t) / cols), place = int(base + t - int64_t(at) * cols);
+  int32_t had[8], keep[8], page[8], j[8];
+  int row[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {             // entry base + t + 1024 u
+    row[u] = at;
+    j[u] = place;
+    had[u] = g.lens[min(at, last)];
+    keep[u] = g.keep ? g.keep[min(at, last)] : 0;
+    at += wide;
+    place += rest;
+    if (place >= cols) {
+      place -= cols;
+      ++at;
+    }
+  }
+  hold(had);
+  hold(keep);
+  if (t <= kBuckets) begin[t] = 0;
+  bool gone[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int n = min(max(had[u], 0), cols * g.page), left = min(n, max(keep[u], 0));
+    const bool real = row[u] <= last;
+    if (real && j[u] == 0 && g.lens_out != g.lens) g.lens_out[row[u]] = left;
+    const int token = j[u] * g.page;        // the page's first
+    gone[u] = real && token >= left && token < n;
+    page[u] = -1;
+    if (__ballot(gone[u])) page[u] = g.table[min(row[u], last) * g.stride + j[u]];
+  }
+  hold(page);
+  __syncthreads();
+  int rank[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    if (!gone[u] || page[u] >= g.pages) page[u] = -1;
+    const bool real = page[u] >= 0;
+    const uint64_t all = __ballot(real);
+    if (all == 0) continue;
+    const int bucket = page[u] >> g.shift, one = __builtin_amdgcn_readlane(bucket, __ffsll((unsigned long long)all) - 1);
+    if (__ballot(real && bucket == one) == all) {
+      // pages that follow each other: one addition for all
+      int start = 0;
+      if ((t & 63) == 0) start = atomicAdd(&begin[one], __popcll(all));
+      rank[u] = uniform(start) + __popcll(all & ((uint64_t(1) << (t & 63)) - 1));
+    } else if (real) {
+      rank[u] = atomicAdd(&begin[bucket], 1);
+    }
+  }
+  __syncthreads();
+  const int mine = t < g.buckets ? begin[t] : 0;
+  int total;
+  const int start = block_scan<16>(mine, total);
+  if (t <= g.buckets) {
+    begin[t] = start;
+    g.ends[int64_t(blockIdx.x) * (kBuckets + 1) + t] = uint16_t(start);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 8; ++u)
+    if (page[u] >= 0) order[begin[page[u] >> g.shift] + rank[u]] = page[u];
+  __syncthreads();
+  for (int i = t; i < total; i += 1024) g.sorted[base + i] = order[i];
+}
+
+__global__ __launch_bounds__(1024) void free_apply_kernel(const FreeArgs g) {
+  extern __shared__ int32_t count[];        // of 2^shift pages
+  const int t = threadIdx.x, span = 1 << g.shift;
+  const int64_t base = int64_t(blockIdx.x) * span;
+  const int pages = int(min(int64_t(span), g.pages - base));
+  int32_t refs[8];                          // those of the first 8192 pages are read meanwhile
+  auto load = [&](int first) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) refs[u] = g.refs[base + min(first + u * 1024 + t, pages - 1)];
+  };
+  load(0);
+  for (int i = t; i < span; i += 1024) count[i] = 0;
+  __syncthreads();
+  // a lane for each tile, the tiles dealt to the waves in turn: its first 64 entries; of tiles that have more, the rest
+  // by the wave together
+  const int lane = t & 63;
+  auto add = [&](const int32_t* from, int i, int step, int hi) {
+    int32_t page[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) page[u] = from[min(i + u * step, hi - 1)];
+    hold(page);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (i + u * step < hi) atomicAdd(&count[page[u] & (span - 1)], 1);
+  };
+  for (int first = 0; first < g.tiles; first += 1024) {
+    const int tile = first + lane * 16 + (t >> 6);
+    const uint16_t* ends = g.ends + int64_t(min(tile, g.tiles - 1)) * (kBuckets + 1) + blockIdx.x;
+    const int lo = ends[0], hi = tile < g.tiles ? ends[1] : lo;
+    const int32_t* from = g.sorted + int64_t(tile) * kTile;
+    const int some = min(hi, lo + 64);
+    for (int i = lo; i < some; i += 8) add(from, i, 1, some);
+    for (uint64_t more = __ballot(some < hi); more; more &= more - 1) {
+      const int who = __ffsll((unsigned long long)more) - 1;
+      const int end = __builtin_amdgcn_readlane(hi, who);
+      const int32_t* it = g.sorted + int64_t(first + who * 16 + (t >> 6)) * kTile;
+      for (int i = __builtin_amdgcn_readlane(some, who) + lane; i < end; i += 8 * 64) add(it, i, 64, end);
+    }
+  }
+  __syncthreads();
+  for (int first = 0; first < pages; first += 8 * 1024) {
+    if (first) load(first);
+    hold(refs);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = first + u * 1024 + t;
+      if (i < pages) g.refs_out[base + i] = refs[u] - count[i];
+    }
   }
 }
 
@@ -976,6 +1108,31 @@ mx_status_t fork_sizes(ForkArgs& g, int64_t pages, int64_t rows, int64_t childre
   return MX_OK;
 }
 
+// Whether the entries of a table are put in order first, and in what: see free_pages_kernel for what it costs not to.
+// From 2^19 entries on the two launches are worth it, up to 2^28 the workspace; buckets of up to 2^15 pages fit LDS.
+bool free_plan(FreeArgs& g, int64_t pages, int64_t rows, int64_t cols) {
+  if (rows * cols < (int64_t(1) << 19) || rows * cols > (int64_t(1) << 28)) return false;
+  if (pages <= kSmallPages || pages > int64_t(kBuckets) << 15) return false;
+  g.shift = 0;
+  while (int64_t(kBuckets) << g.shift < pages) ++g.shift;
+  g.buckets = int((pages + (int64_t(1) << g.shift) - 1) >> g.shift);
+  g.tiles = int((rows * cols + kTile - 1) / kTile);
+  return true;
+}
+
+int64_t free_space(FreeArgs& g, uint8_t* base) {
+  Space s{base};
+  g.sorted = s.take<int32_t>(int64_t(g.tiles) * kTile);
+  g.ends = s.take<uint16_t>(int64_t(kBuckets + 1) * g.tiles);
+  return s.used;
+}
+
+mx_status_t free_sizes(int64_t pages, int64_t rows, int64_t cols, int page) {
+  if (pages < 0 || pages > INT32_MAX || rows < 0 || rows > kMostRows || page < 16 || page > 65536 || page % 16)
+    return MX_ERR_SHAPE;
+  return cols < 0 || cols > INT32_MAX / page ? MX_ERR_SHAPE : MX_OK;
+}
+
 int64_t compact_space(CompactArgs& g, uint8_t* base) {
   Space s{base};
   g.block_used = s.take<int32_t>(g.blocks.count);
@@ -1097,31 +1254,55 @@ extern "C" mx_status_t mx_kv_fork(const mx_kv_cache_t* caches, int layers, const
   return launched();
 }
 
+extern "C" mx_status_t mx_kv_free_workspace(int64_t pages, int64_t rows, int64_t table_cols, int page, int64_t* bytes) {
+  if (!bytes) return MX_ERR_NULL;
+  const mx_status_t st = free_sizes(pages, rows, table_cols, page);
+  if (st != MX_OK) return st;
+  FreeArgs g = {};
+  *bytes = free_plan(g, pages, rows, table_cols) ? free_space(g, nullptr) : 0;
+  return MX_OK;
+}
+
 extern "C" mx_status_t mx_kv_free(const int32_t* refs, int64_t pages, int page, const int32_t* page_table,
                                   int64_t table_stride, int64_t table_cols, const int32_t* lens, int64_t rows,
-                                  const int32_t* keep, int32_t* refs_out, int32_t* lens_out, hipStream_t stream) {
-  if (pages < 0 || pages > INT32_MAX || rows < 0 || rows > kMostRows || page < 16 || page > 65536 || page % 16)
-    return MX_ERR_SHAPE;
-  if (table_cols < 0 || table_cols > INT32_MAX / page || (table_stride < table_cols && rows > 1)) return MX_ERR_SHAPE;
+                                  const int32_t* keep, int32_t* refs_out, int32_t* lens_out, void* workspace,
+                                  int64_t workspace_bytes, hipStream_t stream) {
+  const mx_status_t st = free_sizes(pages, rows, table_cols, page);
+  if (st != MX_OK) return st;
+  if (table_stride < table_cols && rows > 1) return MX_ERR_SHAPE;
   if (pages && (!refs || !refs_out)) return MX_ERR_NULL;
   if (rows && (!lens || !lens_out || (table_cols && !page_table))) return MX_ERR_NULL;
   if (keep && keep == lens_out) return MX_ERR_ARG;
   if (off4(refs) || off4(refs_out) || off4(lens) || off4(lens_out) || off4(page_table) || off4(keep)) return MX_ERR_ALIGN;
+  FreeArgs g = {};
+  const bool many = free_plan(g, pages, rows, table_cols);
+  if (many) {
+    if (workspace_bytes < free_space(g, nullptr)) return MX_ERR_SHAPE;
+    if (!workspace) return MX_ERR_NULL;
+    if (misaligned(workspace)) return MX_ERR_ALIGN;
+    free_space(g, static_cast<uint8_t*>(workspace));
+  }
   if (rows == 0 && (pages == 0 || refs_out == refs)) return MX_OK;
-  FreeArgs g = {refs, page_table, lens, keep, refs_out, lens_out, pages, table_stride, rows, int(table_cols), page};
+  g.refs = refs; g.table = page_table; g.lens = lens; g.keep = keep; g.refs_out = refs_out; g.lens_out = lens_out;
+  g.pages = pages; g.stride = table_stride; g.rows = rows; g.cols = int(table_cols); g.page = page;
   if (refs_out != refs && is_small(pages, rows, table_cols)) {
     free_small_kernel<<<1, 1024, 0, stream>>>(g);
     return launched();
   }
   const int64_t cus = std::max<int64_t>(device_cus(), 1);
-  if (refs_out != refs && pages)
-    refs_copy_kernel<<<unsigned(std::min(8 * cus, (pages + 255) / 256)), 256, 0, stream>>>(refs, refs_out, pages);
-  if (rows) {
-    const int64_t x = std::min(rows, 8 * cus);
-    const int64_t y = std::min(std::max<int64_t>(1, (table_cols + 255) / 256), std::max<int64_t>(1, 8 * cus / x));
-    free_pages_kernel<<<dim3(unsigned(x), unsigned(y)), 256, 0, stream>>>(g);
-    if (lens_out == lens) free_lens_kernel<<<unsigned((rows + 255) / 256), 256, 0, stream>>>(g);
+  if (many) {
+    free_sort_kernel<<<unsigned(g.tiles), 1024, 0, stream>>>(g);
+    free_apply_kernel<<<unsigned(g.buckets), 1024, size_t(4) << g.shift, stream>>>(g);
+  } else {
+    if (refs_out != refs && pages)
+      refs_copy_kernel<<<unsigned(std::min(8 * cus, (pages + 255) / 256)), 256, 0, stream>>>(refs, refs_out, pages);
+    if (rows) {
+      const int64_t x = std::min(rows, 8 * cus);
+      const int64_t y = std::min(std::max<int64_t>(1, (table_cols + 255) / 256), std::max<int64_t>(1, 8 * cus / x));
+      free_pages_kernel<<<dim3(unsigned(x), unsigned(y)), 256, 0, stream>>>(g);
+    }
   }
+  if (rows && lens_out == lens) free_lens_kernel<<<unsigned((rows + 255) / 256), 256, 0, stream>>>(g);
   return launched();
 }
 

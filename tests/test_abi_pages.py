@@ -79,8 +79,9 @@ def test_fork(status, kw):
     assert fork(**kw) == status
 
 
-free = caller(lib.mx_kv_free, "refs pages page table stride cols lens rows keep refs_out lens_out stream",
-              [FAKE, 4, 16, FAKE, 3, 3, FAKE, 2, None, FAKE, FAKE, None])
+free = caller(lib.mx_kv_free, "refs pages page table stride cols lens rows keep refs_out lens_out space bytes stream",
+              [FAKE, 4, 16, FAKE, 3, 3, FAKE, 2, None, FAKE, FAKE, None, 0, None])
+MANY = {"pages": 1 << 17, "rows": 1 << 10, "cols": 1 << 9, "stride": 1 << 9}
 
 
 @pytest.mark.parametrize("status,kw", [
@@ -88,7 +89,8 @@ free = caller(lib.mx_kv_free, "refs pages page table stride cols lens rows keep 
     (SHAPE, {"rows": -1}), (SHAPE, {"rows": (1 << 20) + 1}), (SHAPE, {"cols": -1}), (SHAPE, {"cols": 1 << 28, "stride": 1 << 28}),
     (SHAPE, {"stride": 2}), (NULL, {"refs": None}), (NULL, {"refs_out": None}), (NULL, {"table": None}), (NULL, {"lens": None}),
     (NULL, {"lens_out": None}), (ALIGN, {"refs": FAKE + 1}), (ALIGN, {"table": FAKE + 2}), (ALIGN, {"keep": FAKE + 2}),
-    (ARG, {"keep": FAKE}),
+    (ARG, {"keep": FAKE}), (SHAPE, MANY), (SHAPE, {**MANY, "space": FAKE, "bytes": 1 << 20}),
+    (NULL, {**MANY, "bytes": 1 << 30}), (ALIGN, {**MANY, "space": FAKE + 4, "bytes": 1 << 30}),
     (OK, {"rows": 0, "lens": None, "table": None})])
 def test_free(status, kw):
     assert free(**kw) == status
@@ -138,6 +140,9 @@ def test_workspaces():
     assert lib.mx_kv_fork_workspace(100, 4, 8, 9, 15, at) == SHAPE
     assert lib.mx_kv_fork_workspace(100, 4, 8, 9, 16, None) == NULL
     assert lib.mx_kv_fork_workspace((1 << 31) - 1, 1 << 20, 1 << 20, (1 << 31) - 1, 16, at) == OK and n.value < 1 << 30
+    assert lib.mx_kv_free_workspace(1 << 17, 1 << 10, 1 << 9, 16, at) == OK and n.value >= 4 << 19
+    assert lib.mx_kv_free_workspace(1 << 17, 1 << 10, 1 << 8, 16, at) == OK and n.value == 0
+    assert lib.mx_kv_free_workspace(1 << 17, 1 << 10, 1 << 9, 15, at) == SHAPE
     assert lib.mx_kv_compact_workspace(0, at) == OK and n.value > 0
     assert lib.mx_kv_compact_workspace((1 << 31) - 1, at) == OK and n.value < 1 << 35
     assert lib.mx_kv_compact_workspace(-1, at) == SHAPE

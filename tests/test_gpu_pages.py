@@ -170,7 +170,8 @@ def test_lengths_outside_the_table_are_cut():
 
 
 @pytest.mark.parametrize("pages,page,cols,rows", [(1, 16, 1, 1), (50, 16, 7, 9), (5000, 64, 300, 40), (30000, 16, 33, 3000),
-                                                 (70000, 16, 20000, 3)])
+                                                 (70000, 16, 20000, 3), (16385, 16, 700, 800), (200000, 32, 300, 2000),
+                                                 (1000000, 16, 9001, 60), (300, 16, 2, 300000)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_free(pages, page, cols, rows, in_place):
     r = random.Random(pages + rows)
