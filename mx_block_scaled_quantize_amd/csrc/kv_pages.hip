@@ -398,15 +398,47 @@ __global__ __launch_bounds__(256) void fork_kids_kernel(const ForkArgs g) {
   }
 }
 
-// Every page of a row gains the row's children and loses the row itself if it is released.
+// Every page of a row gains the row's children and loses the row itself if it is released.  A thread takes one column of
+// eight rows: beams of a request lie next to each other and share their first pages, whose gains and losses add up to
+// nothing before they would go to memory (256 x 8 beams of some 380 pages: 22.3 -> 8.6 us).
+constexpr int kRowGroup = 8;
+
 __global__ __launch_bounds__(256) void fork_counts_kernel(const ForkArgs g) {
-  for (int64_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
-    const int d = g.kids[row] - g.release;
-    if (d == 0) continue;
-    const int held = (row_length(g, row) + g.shape.page - 1) / g.shape.page;
-    for (int j = blockIdx.y * 256 + threadIdx.x; j < held; j += gridDim.y * 256) {
-      const int32_t page = g.table[row * g.stride + j];
-      if (in_pool(g, page)) atomicAdd(&g.refs_out[page], d);
+  for (int64_t row0 = int64_t(blockIdx.x) * kRowGroup; row0 < g.rows; row0 += int64_t(gridDim.x) * kRowGroup) {
+    int32_t d[kRowGroup], held[kRowGroup];
+    int most = 0;
+#pragma unroll
+    for (int u = 0; u < kRowGroup; ++u) {
+      const int64_t row = min(row0 + u, g.rows - 1);
+      d[u] = g.kids[row];
+      held[u] = row_length(g, row);
+    }
+#pragma unroll
+    for (int u = 0; u < kRowGroup; ++u) {
+      d[u] = row0 + u < g.rows ? d[u] - g.release : 0;
+      held[u] = d[u] == 0 ? 0 : (held[u] + g.shape.page - 1) / g.shape.page;
+      most = max(most, held[u]);
+    }
+    for (int j = blockIdx.y * 256 + threadIdx.x; j < most; j += gridDim.y * 256) {
+      int32_t page[kRowGroup];
+#pragma unroll
+      for (int u = 0; u < kRowGroup; ++u) {
+        page[u] = -1;
+        if (uniform(held[u]) > 0) page[u] = g.table[(row0 + u) * g.stride + min(j, held[u] - 1)];
+      }
+      hold(page);
+      int32_t last = -1, sum = 0;
+#pragma unroll
+      for (int u = 0; u < kRowGroup; ++u) {
+        if (j >= held[u] || !in_pool(g, page[u])) continue;
+        if (page[u] != last) {
+          if (sum != 0) atomicAdd(&g.refs_out[last], sum);
+          last = page[u];
+          sum = 0;
+        }
+        sum += d[u];
+      }
+      if (sum != 0) atomicAdd(&g.refs_out[last], sum);
     }
   }
 }
@@ -1235,8 +1267,8 @@ extern "C" mx_status_t mx_kv_fork(const mx_kv_cache_t* caches, int layers, const
       if (children) fork_kids_kernel<<<unsigned(g.child_blocks), 256, 0, stream>>>(g);
     }
     if (rows && table_cols) {
-      // a workgroup a row, several where there are few rows
-      const int64_t x = std::min(rows, 8 * cus), y = std::min((table_cols + 255) / 256, std::max<int64_t>(1, 8 * cus / x));
+      // a workgroup for eight rows, several where there are few rows
+      const int64_t x = std::min((rows + kRowGroup - 1) / kRowGroup, 8 * cus), y = std::min((table_cols + 255) / 256, std::max<int64_t>(1, 8 * cus / x));
       fork_counts_kernel<<<dim3(unsigned(x), unsigned(y)), 256, 0, stream>>>(g);
     }
   }
