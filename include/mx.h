@@ -580,7 +580,8 @@ mx_status_t mx_kv_compact_workspace(int64_t pages, int64_t* bytes);
  *              its last one (not for beams that were finished, are empty or are full);
  *              lens_out int32 [requests][width].  None may overlap an input.
  * Exponentials are FP32 and summed in FP32 over 64 logits and FP64 from there on; scores are
- * compared in FP64 and rounded once to FP32.
+ * compared in FP64 and rounded once to FP32.  The order of the sums is fixed by the sizes of
+ * the call, on which the last bits of a score depend.
  * workspace  mx_beam_select_workspace bytes, 16-byte aligned; nothing is kept in it between calls.
  * Errors: MX_ERR_UNSUPPORTED (dtype), MX_ERR_SHAPE (also a workspace too small), MX_ERR_ARG (eos or pad past 32
  * bits), MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */

@@ -156,6 +156,10 @@ def test_large_values_and_narrow_sums():
     """Logits of +-1e30 and of one great value beside thousands of small ones."""
     x = logits((2, 3, 2500), "f32", 6) * 1e30
     check(x, np.zeros((2, 3)) - [[0, 1, 2]], 4)
+    # subnormal logits: all equally likely to 64 bits, but in an order
+    x = torch.randint(-900, 900, (2, 3, 2500), device=dev()) * 2.0 ** -149
+    assert x.abs().max() > 0
+    check(x, np.zeros((2, 3)) - [[0, 1, 2]], 4)
     x = logits((2, 3, 2500), "f32", 7) * 1e-3
     x[:, :, 1234] = 40.0
     check(x, np.zeros((2, 3)) - [[0, 1, 2]], 9)
@@ -169,6 +173,25 @@ def test_strided_logits(dtype):
         x = base[start:start + 4 * 3 * 1207].view(4, 3, 1207)
         for y in (x[:, :, 2:1201], x.transpose(0, 1)[:, :, :1100], x[1:2, :, :5], x[:, 1:2, 7:]):
             check(y, np.random.default_rng(start).uniform(-5, 0, y.shape[:2]), 4)
+
+
+def test_logits_past_32_bits():
+    """2.5e9 logits: the last request's, and histories of 1.2e9 tokens."""
+    r, b, v, c = 300, 64, 131072, 65536
+    x, s = torch.zeros((r, b, v), dtype=torch.bfloat16, device=dev()), torch.zeros((r, b), device=dev())
+    x[-1] = logits((b, v), "bf16", 1)
+    s[-1] = -torch.rand(b, device=dev())
+    history = torch.zeros((r, b, c), dtype=torch.int32, device=dev())
+    history[-1] = torch.arange(b * c, device=dev()).view(b, c) % 50000
+    lens = torch.full((r, b), 7, dtype=torch.int32, device=dev())
+    got = mxa.mx_beam_select(x, s, 16, history=history, lens=lens)
+    want = mxa.mx_beam_select(x[-1:], s[-1:], 16, history=history[-1:], lens=lens[-1:])
+    for name in ("tokens", "finished", "history", "lens"):
+        assert torch.equal(getattr(got, name)[-1:], getattr(want, name)), name
+    # a call of other sizes sums in other segments: each is off by at most NEAR and its rounding (see above)
+    assert ((got.scores[-1:] - want.scores).abs() <= 2 * NEAR + 2.0 ** -23 * want.scores.abs()).all()
+    assert torch.equal(got.parents[-1:], want.parents + (r - 1) * b)
+    assert got.tokens[0].tolist() == list(range(16)) and got.parents[0].tolist() == [0] * 16
 
 
 def test_scores_of_one_beam_add_up():
