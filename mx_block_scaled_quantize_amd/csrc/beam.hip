@@ -20,7 +20,8 @@ namespace mxk {
 constexpr int kMostBeams = 64;              // a lane for each when they are merged
 constexpr int kMostWidth = 64;              // a lane for each of a beam's candidates
 constexpr int kMostSplits = 64;             // a lane for each segment of a beam's logits
-constexpr int kMergeWaves = 8;
+constexpr int kFew = 128;                   // candidates of a request that are all compared with each other
+constexpr int kGood = 512;                  // and of more, those that can be
 constexpr int kBuffer = 512;                // candidates a wave sets aside before it sorts them in
 
 typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));      // of logits, at any place of their type
@@ -340,10 +341,15 @@ __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
 // One request of four beams takes 5.6 us, nearly all of it latency: 1.7 for what the first launch left in other XCDs' caches,
 // 1 for a beam's best, 1 for the choice, 1 to 2 for a history; 256 requests of eight beams with histories of 2048
 // tokens (33 MB read and written) 13.  One candidate chosen after the other, by a wave, took 700 clocks each.
-__global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const BeamArgs g) {
-  __shared__ uint64_t buffers[kMergeWaves][kBuffer];
+// kMany: of more than 128 candidates only those are compared that reach a bound, and 16 waves share the beams: 4
+// requests of 16 beams, 32 to be chosen, take 26 us (39 with eight waves that compare all), where one request of four
+// beams would take 6.6.
+template <int kWaves, bool kMany>
+__global__ __launch_bounds__(64 * kWaves) void beam_merge_kernel(const BeamArgs g) {
+  __shared__ uint64_t buffers[kWaves][kBuffer];
   extern __shared__ double score[];         // [beams][keep], and the tokens behind them
   uint32_t* token = reinterpret_cast<uint32_t*>(score + g.beams * g.keep);
+  __shared__ int passed[32];                // of each bit of a bound: how many reach it; 0: candidates that reach the bound
   __shared__ int chosen_beam[kMostWidth];
   __shared__ int chosen_token[kMostWidth];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -351,13 +357,14 @@ __global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const Beam
   const int64_t row0 = int64_t(request) * g.beams;
   __shared__ int length[kMostBeams];
   __shared__ bool was[kMostBeams];
+  if (kMany && threadIdx.x < 32) passed[threadIdx.x] = 0;
   // all that does not depend on the choice is read before it
   if (int(threadIdx.x) < g.beams) {
     const int n = g.lens ? g.lens[row0 + threadIdx.x] : 0;
     was[threadIdx.x] = g.finished && g.finished[row0 + threadIdx.x];
     length[threadIdx.x] = min(max(n, 0), g.cols);
   }
-  for (int b = wave; b < g.beams; b += kMergeWaves) {
+  for (int b = wave; b < g.beams; b += kWaves) {
     const int64_t row = row0 + b;
     const float before = g.scores[row];
     const bool done = g.finished && g.finished[row];
@@ -424,11 +431,43 @@ __global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const Beam
     chosen_token[place] = t;
     if (blockIdx.y == 0) g.scores_out[int64_t(request) * g.width + place] = float(z);
   };
-  const int candidates = g.beams * g.keep;
-  if (candidates <= 64 * kMergeWaves) {
-    // a candidate's place is the number of better ones: those before it (lower beams, better logits) that are not
-    // worse, and those behind it that are better
-    const int me = threadIdx.x;
+  // A candidate's place is the number of better ones: a higher score, or the same and a lower beam, or a better logit of
+  // the same beam.
+  constexpr int step = 64 * kWaves;
+  const int candidates = g.beams * g.keep, me = threadIdx.x;
+  double* good = reinterpret_cast<double*>(&buffers[0][0]);
+  int* which = reinterpret_cast<int*>(good + kGood);
+  if constexpr (kMany) {
+    // only those that reach a bound which at least width do: the width-th largest score to 20 bits
+    constexpr int kEach = kMostBeams * kMostWidth / step;
+    uint32_t key[kEach], bound = 0;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int i = u * step + me;
+      key[u] = i < candidates && score[i] > -INFINITY ? ordered(float(score[i])) : 0;
+    }
+    for (int bit = 31; bit >= 12; --bit) {
+      const uint32_t next = bound | 1u << bit;
+      int n = 0;
+#pragma unroll
+      for (int u = 0; u < kEach; ++u)
+        if (u * step < candidates) n += __popcll(__ballot(key[u] >= next));
+      if (lane == 0 && n) atomicAdd(&passed[bit], n);
+      __syncthreads();
+      if (passed[bit] >= g.width) bound = next;
+    }
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      if (key[u] == 0 || key[u] < bound) continue;
+      const int to = atomicAdd(&passed[0], 1);             // in any order: their places do not depend on it
+      if (to < kGood) {
+        good[to] = score[u * step + me];
+        which[to] = u * step + me;
+      }
+    }
+    __syncthreads();
+  }
+  if constexpr (!kMany) {
     const double mine = me < candidates ? score[me] : -INFINITY;
     int place = 0;
     if (wave * 64 < candidates) {
@@ -441,8 +480,22 @@ __global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const Beam
     if (mine > -INFINITY && place < g.width) choose(place, me / g.keep, mine, int(token[me]));
     const int real = __syncthreads_count(mine > -INFINITY);
     if (me >= real && me < g.width) choose(me, -1, -INFINITY, g.pad);
+  } else if (passed[0] <= kGood) {
+    const int some = passed[0];
+    if (me < some) {
+      const double mine = good[me];
+      const int at = which[me];
+      int place = 0;
+#pragma unroll 8
+      for (int i = 0; i < some; ++i) {
+        const double other = good[i];
+        place += other > mine || (other == mine && which[i] < at);
+      }
+      if (place < g.width) choose(place, at / g.keep, mine, int(token[at]));
+    }
+    if (me >= some && me < g.width) choose(me, -1, -INFINITY, g.pad);
   } else if (wave == 0) {
-    // one after the other: lane b holds the best candidate of beam b that is left
+    // very many that are nearly alike: one after the other, lane b with the best candidate of beam b that is left
     int at = 0;
     double head = lane < g.beams ? score[lane * g.keep] : -INFINITY;
     for (int j = 0; j < g.width; ++j) {
@@ -472,7 +525,7 @@ __global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(const Beam
     }
   }
   if (!g.history || g.cols == 0) return;
-  for (int j = wave; j < g.width; j += kMergeWaves) {
+  for (int j = wave; j < g.width; j += kWaves) {
     const int b = chosen_beam[j];
     const int64_t row = row0 + max(b, 0);
     const int32_t* from = g.history + row * g.cols;
@@ -595,6 +648,9 @@ extern "C" mx_status_t mx_beam_select(const void* logits, mx_dtype_t dtype, int6
   const int64_t wide = with_history ? g.width * int64_t(g.cols) * 4 / 32768 : 0;
   const int64_t most = std::max<int64_t>(1, 2 * std::max<int64_t>(device_cus(), 1) / requests);
   const unsigned y = unsigned(std::max<int64_t>(1, std::min(wide, most)));
-  beam_merge_kernel<<<dim3(unsigned(requests), y), 64 * kMergeWaves, size_t(g.beams) * g.keep * 12, stream>>>(g);
+  const dim3 grid(static_cast<unsigned>(requests), y);
+  const int64_t candidates = beams * g.keep;
+  if (candidates <= kFew) beam_merge_kernel<8, false><<<grid, 512, size_t(candidates) * 12, stream>>>(g);
+  else beam_merge_kernel<16, true><<<grid, 1024, size_t(candidates) * 12, stream>>>(g);
   return hipGetLastError() == hipSuccess ? MX_OK : MX_ERR_LAUNCH;
 }

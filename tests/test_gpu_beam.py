@@ -106,6 +106,21 @@ def test_equal_scores_go_to_the_lower_beam():
     s = torch.full((2, 5), -3.0, device=dev())
     got = mxa.mx_beam_select(x, s, 10)
     assert got.parents.tolist() == [[0, 1, 2, 3, 4] * 2, [5, 6, 7, 8, 9] * 2]
+    # 4096 candidates: of 64 beams alike (the 64 best logits' score each 64 times), and all of one score
+    x = logits((1, 1, 900), "f32", 5).expand(2, 64, 900)
+    s = torch.full((2, 64), -3.0, device=dev())
+    got = mxa.mx_beam_select(x, s, 64)
+    assert got.parents.tolist() == [list(range(64)), list(range(64, 128))]
+    assert (got.tokens == x[0, 0].argmax()).all()
+    got = mxa.mx_beam_select(x * 0.0, s, 64)
+    assert (got.parents == torch.tensor([[0], [64]], device=dev())).all()
+    assert got.tokens.tolist() == [list(range(64))] * 2
+    # 15 beams, 20 to be chosen: 300 candidates, fewer than 20 of them real
+    x = torch.full((1, 15, 40), -float("inf"), device=dev())
+    x[0, ::2, 7] = 1.0
+    got = mxa.mx_beam_select(x, -torch.arange(15.0, device=dev())[None], 20)
+    assert got.parents[0].tolist() == list(range(0, 15, 2)) + [0] * 12 and got.tokens[0].tolist() == [7] * 8 + [0] * 12
+    assert got.scores[0].tolist() == [-float(i) for i in range(0, 15, 2)] + [-float("inf")] * 12
 
 
 @pytest.mark.parametrize("dtype", list(DT))
