@@ -235,8 +235,8 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // spares 8%); a chunk's maximum moves each lane's own reference before its exponentials are added, in 32 bits within a
 // chunk and in 64 across chunks.  The first chunk's keep-th largest lane maximum is a bound that at least keep logits
 // reach: those that reach it, some more than keep, are set aside and sorted.  2048 rows of 131072 BF16 logits take 109
-// us, 4.9 TB/s, as a copy does, with the vector unit busy half of the time.  Tried: each granule's registers reloaded
-// for the next chunk as soon as it is worked off, 128 us: the compiler waits for all of them at the loop's head.
+// to 112 us, 4.8 to 4.9 TB/s, as a copy does, with the vector unit busy 74% of the time.  Tried: each granule's registers
+// reloaded for the next chunk as soon as it is worked off, 128 us: the compiler waits for all of them at the loop's head.
 template <int DT, int kLoads>
 __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
   using E = Elements<DT>;
