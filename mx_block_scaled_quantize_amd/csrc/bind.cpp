@@ -435,8 +435,9 @@ PyObject* kv_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
              l = out_or_new(out, 2, "out's lens", {children}, at::kInt, dev),
              s = out_or_new(out, 3, "out's slots", {tokens}, at::kLong, dev),
              space = fresh({need}, at::kByte, dev);
-  // a parents tensor without elements has no address, which would stand for children that continue their own rows
-  if (a[5] != Py_None && children == 0) parents = ints(refs);
+  // a parents tensor without elements has no address, which would stand for children that continue their own rows;
+  // nothing is read through this one
+  if (a[5] != Py_None && children == 0) parents = ints(space);
   check_status(mx_kv_fork(caches.data(), layer_count(caches), ints(refs), ints(table), row_stride(table), table.size(1),
                           ints(lens), rows, parents, children, cu, tokens, release, ints_out(r), ints_out(t), cols,
                           ints_out(l), static_cast<int64_t*>(s.data_ptr()), space.data_ptr(), need, on.stream));

@@ -144,6 +144,12 @@ def test_fork_of_nothing():
     assert got.refs.tolist() == [0, 3, 3, 0] and got.lens.tolist() == [20, 20, 20]
 
 
+def test_fork_without_children_in_an_empty_pool():
+    none = torch.empty(0, dtype=torch.int32, device=dev())
+    got = mxa.mx_kv_fork(mxa.new_kv_cache(0, 1, 16, 64), none, ints([[0, 0]]), ints([0]), parents=none)
+    assert got.lens.shape == (0,) and got.page_table.shape == (0, 2)
+
+
 def test_table_of_wider_rows_and_bad_entries():
     """A table that is part of a wider one; pages outside the pool are held by nobody and not written to."""
     wide = ints([[3, 0, 1, 7], [9, 9, 2, 7], [-4, 1, 1, 7]])
