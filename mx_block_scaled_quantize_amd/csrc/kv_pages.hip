@@ -1268,7 +1268,7 @@ extern "C" mx_status_t mx_kv_fork(const mx_kv_cache_t* caches, int layers, const
     if (rows <= kBeginRows && children <= kBeginChildren) {
       fork_begin_kernel<<<unsigned(1 + std::min(2 * cus, (copied + 1023) / 1024)), 1024, 0, stream>>>(g);
     } else {
-      fork_init_kernel<<<unsigned(std::min(8 * cus, (n + 255) / 256)), 256, 0, stream>>>(g);
+      if (n) fork_init_kernel<<<unsigned(std::min(8 * cus, (n + 255) / 256)), 256, 0, stream>>>(g);
       if (children) fork_kids_kernel<<<unsigned(g.child_blocks), 256, 0, stream>>>(g);
     }
     if (rows && table_cols) {

@@ -150,6 +150,18 @@ def test_fork_without_children_in_an_empty_pool():
     assert got.lens.shape == (0,) and got.page_table.shape == (0, 2)
 
 
+@pytest.mark.parametrize("pages", [0, 50])
+def test_fork_of_many_children_without_rows(pages):
+    """Counts changed in place and no rows: there is nothing to begin with."""
+    children, cu = 20000, [0] * 10000 + [30] * 10001
+    refs, lens = ints([0] * pages), ints([1] * children)
+    table, slots = ints([[5, 5]] * children), torch.full((30,), -7, device=dev())
+    mxa.mx_kv_fork(mxa.new_kv_cache(pages, 1, 16, 64), refs, ints([]).view(0, 2), ints([]), ints(cu),
+                   parents=ints([-1] * children), out=(refs, table, lens, slots))
+    want = op.fork([0] * pages, [], [], 16, cu, [-1] * children, tokens=30, cols=2)
+    assert [x.tolist() for x in (refs, table, lens, slots)] == list(want[:4])
+
+
 def test_table_of_wider_rows_and_bad_entries():
     """A table that is part of a wider one; pages outside the pool are held by nobody and not written to."""
     wide = ints([[3, 0, 1, 7], [9, 9, 2, 7], [-4, 1, 1, 7]])
