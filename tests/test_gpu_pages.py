@@ -321,6 +321,27 @@ def test_replayed_graph_and_other_streams():
         assert_caches(cache, content)
 
 
+def test_captured_copy():
+    """The copies of more layers than one launch takes, captured, replayed on changing pages."""
+    caches = new_caches(35, 30, 1, 16, 64, 4)
+    src, dst = ints([0] * 6), ints([1] * 6)
+    r = random.Random(2)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        mxa.mx_kv_copy(caches, src * 0 - 1, caches, dst)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mxa.mx_kv_copy(caches, src, caches, dst)
+    for _ in range(4):
+        a, b = r.sample(range(15), 6), r.sample(range(15, 30), 6)
+        src.copy_(ints(a))
+        dst.copy_(ints(b))
+        want = moved(caches, [(x, y, 16) for x, y in zip(a, b)])
+        graph.replay()
+        assert_caches(caches, want)
+
+
 def test_refusals():
     cache = mxa.new_kv_cache(4, 1, 16, 64)
     refs, table, lens, cu = ints([0] * 4), ints([[0, 1]]), ints([3]), ints([0, 1])
