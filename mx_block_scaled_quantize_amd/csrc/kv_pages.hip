@@ -658,17 +658,18 @@ __device__ __forceinline__ void copy_tails(const ForkArgs& g, int64_t block, int
 // behind them copy the partly filled pages.  64 x 4 beams in eight layers, some 80 pages of 34 KB each: 11 us, of which
 // the copies' bytes need 9.
 __global__ __launch_bounds__(256) void fork_rows_kernel(const ForkArgs g) {
-  if (int64_t(blockIdx.x) >= g.children) {
-    copy_tails(g, int64_t(blockIdx.x) - g.children, int64_t(gridDim.x) - g.children);
+  const int64_t i = blockIdx.x;
+  if (i > 0 && i >= g.children) {
+    copy_tails(g, i - g.children, int64_t(gridDim.x) - g.children);
     return;
   }
-  const int64_t i = blockIdx.x;
   if (i == 0 && g.tokens) {                 // tokens before the first child and behind the last are padding
     const int64_t lo = g.cu ? min(max(int64_t(g.cu[0]), int64_t(0)), g.tokens) : g.tokens;
     const int64_t hi = g.cu ? min(max(int64_t(g.cu[g.children]), int64_t(0)), g.tokens) : g.tokens;
     for (int64_t t = threadIdx.x; t < lo; t += 256) g.slots[t] = -1;
     for (int64_t t = hi + threadIdx.x; t < g.tokens; t += 256) g.slots[t] = -1;
   }
+  if (g.children == 0) return;              // launched for the padding
   const Child c = child_of(g, i);
   const int64_t start = g.start[i];
   const bool fits = start >= 0;
@@ -1278,7 +1279,10 @@ extern "C" mx_status_t mx_kv_fork(const mx_kv_cache_t* caches, int layers, const
     }
   }
   if (!small && both) fork_needs_kernel<<<both, 256, 0, stream>>>(g);
-  if (children == 0) return launched();
+  if (children == 0) {
+    if (tokens) fork_rows_kernel<<<1, 256, 0, stream>>>(g);
+    return launched();
+  }
   if (!small) fork_list_kernel<<<both, 256, 0, stream>>>(g);
   for (int l = 0; l < layers; l += kLayersPerLaunch) {
     const int n = std::min(kLayersPerLaunch, layers - l);

@@ -162,6 +162,17 @@ def test_fork_of_many_children_without_rows(pages):
     assert [x.tolist() for x in (refs, table, lens, slots)] == list(want[:4])
 
 
+@pytest.mark.parametrize("pages", [0, 4, 20000])
+def test_fork_of_tokens_without_children(pages):
+    """A padded batch that has lost its last sequence: every token is of no child."""
+    none = torch.empty(0, dtype=torch.int32, device=dev())
+    slots = torch.full((300,), 7, device=dev())
+    out = (ints([0] * pages), none.view(0, 2), none.clone(), slots)
+    got = mxa.mx_kv_fork(mxa.new_kv_cache(pages, 1, 16, 64), ints([0] * pages), none.view(0, 2), none, ints([0]),
+                         parents=none, tokens=300, out=out)
+    assert slots.tolist() == [-1] * 300 and not got.refs.any()
+
+
 def test_table_of_wider_rows_and_bad_entries():
     """A table that is part of a wider one; pages outside the pool are held by nobody and not written to."""
     wide = ints([[3, 0, 1, 7], [9, 9, 2, 7], [-4, 1, 1, 7]])
