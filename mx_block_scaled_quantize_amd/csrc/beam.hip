@@ -444,7 +444,8 @@ __global__ __launch_bounds__(64 * kWaves) void beam_merge_kernel(const BeamArgs 
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
       const int i = u * step + me;
-      key[u] = i < candidates && score[i] > -INFINITY ? ordered(float(score[i])) : 0;
+      // (+ 0: a score of -0, which a finished beam can have, equals one of 0)
+      key[u] = i < candidates && score[i] > -INFINITY ? ordered(float(score[i]) + 0.0f) : 0;
     }
     for (int bit = 31; bit >= 12; --bit) {
       const uint32_t next = bound | 1u << bit;

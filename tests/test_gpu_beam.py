@@ -123,6 +123,20 @@ def test_equal_scores_go_to_the_lower_beam():
     assert got.scores[0].tolist() == [-float(i) for i in range(0, 15, 2)] + [-float("inf")] * 12
 
 
+@pytest.mark.parametrize("beams", [4, 40])
+def test_a_score_of_minus_zero_equals_zero(beams):
+    """A finished beam's -0 comes before the zeros of higher beams, few candidates or many."""
+    x = torch.full((1, beams, 9), -float("inf"), device=dev())
+    x[:, :, 5] = 0.0
+    scores = torch.zeros(1, beams, device=dev())
+    scores[0, 0] = -0.0
+    finished = torch.zeros(1, beams, dtype=torch.bool, device=dev())
+    finished[0, 0] = True
+    got = mxa.mx_beam_select(x, scores, 4, finished, pad=2)
+    assert got.parents.tolist() == [[0, 1, 2, 3]] and got.tokens.tolist() == [[2, 5, 5, 5]]
+    assert got.scores.tolist() == [[0.0] * 4]
+
+
 @pytest.mark.parametrize("dtype", list(DT))
 def test_masked_and_bad_rows(dtype):
     """Banned tokens, rows with nothing left, NaN and infinities; scores that are none."""
