@@ -570,7 +570,7 @@ mx_status_t mx_kv_compact_workspace(int64_t pages, int64_t* bytes);
  * beams: score -inf, token `pad`, beam 0's history.
  *   logits     [requests][beams][vocab] of type dtype, strides in elements, token stride 1.
  *   scores     FP32 [requests][beams]; finished uint8 (0 or 1), the same shape, or NULL.
- *   width      1 .. 64; beams 1 .. 64; vocab 1 .. 2^30; requests <= 2^24.
+ *   width      1 .. 64; beams 1 .. 64; vocab 1 .. 2^30; requests <= 2^20.
  *   eos        the token that finishes a beam (one outside the vocabulary: none does).
  *   history    int32 [requests][beams][history_cols], lens int32 [requests][beams] (counted as
  *              within 0 .. history_cols), or NULL both: the beams' tokens.

@@ -567,7 +567,7 @@ __global__ __launch_bounds__(64 * kWaves) void beam_merge_kernel(const BeamArgs 
 // launch: 108 us with eight waves on a SIMD, 111 with four.)
 mx_status_t plan(BeamArgs& g, mx_dtype_t dtype, int64_t requests, int64_t beams, int64_t vocab, int64_t width) {
   if (dtype != MX_F32 && dtype != MX_BF16 && dtype != MX_F16) return MX_ERR_UNSUPPORTED;
-  if (requests < 0 || requests > (int64_t(1) << 24) || beams < 1 || beams > kMostBeams || width < 1 || width > kMostWidth ||
+  if (requests < 0 || requests > (int64_t(1) << 20) || beams < 1 || beams > kMostBeams || width < 1 || width > kMostWidth ||
       vocab < 1 || vocab > (int64_t(1) << 30))
     return MX_ERR_SHAPE;
   g.requests = int(requests);

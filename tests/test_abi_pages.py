@@ -148,3 +148,6 @@ def test_workspaces():
     assert lib.mx_kv_compact_workspace(-1, at) == SHAPE
     assert lib.mx_beam_select_workspace(2, 3, 1000, 4, at) == OK and n.value >= 6 * (16 + 32)
     assert lib.mx_beam_select_workspace(2, 3, 1000, 0, at) == SHAPE
+    # a grid has fewer than 2^32 threads
+    assert lib.mx_beam_select_workspace(1 << 20, 64, 1, 64, at) == OK
+    assert lib.mx_beam_select_workspace((1 << 20) + 1, 1, 1, 1, at) == SHAPE
