@@ -553,7 +553,7 @@ __global__ __launch_bounds__(64 * kWaves) void beam_merge_kernel(const BeamArgs 
         reinterpret_cast<Vector*>(to)[at] = v[u];
       }
     }
-    for (int i = vectors * 4 + blockIdx.y * 64 + lane; i < g.cols; i += gridDim.y * 64) to[i] = grows && i == n ? t : from[i];
+    for (int64_t i = int64_t(vectors) * 4 + blockIdx.y * 64 + lane; i < g.cols; i += gridDim.y * 64) to[i] = grows && i == n ? t : from[i];
   }
 }
 

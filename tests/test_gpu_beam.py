@@ -223,6 +223,21 @@ def test_logits_past_32_bits():
     assert got.tokens[0].tolist() == list(range(16)) and got.parents[0].tolist() == [0] * 16
 
 
+def test_a_history_of_the_most_columns():
+    """2^31 - 1 columns: the count of the last step passes 31 bits."""
+    cols = (1 << 31) - 1
+    history = torch.empty(1, 1, cols, dtype=torch.int32, device=dev())
+    at = [0, 63, 64, 65, 1 << 30, cols - 65, cols - 2, cols - 1]
+    history.fill_(-3)
+    history[0, 0, at] = torch.arange(8, dtype=torch.int32, device=dev())
+    x = torch.tensor([[[0.0, 1.0]]], device=dev())
+    got = mxa.mx_beam_select(x, torch.zeros(1, 1, device=dev()), history=history,
+                             lens=torch.tensor([[cols - 1]], dtype=torch.int32, device=dev()))
+    assert got.lens.tolist() == [[cols]] and got.history[0, 0, at].tolist() == [0, 1, 2, 3, 4, 5, 6, 1]
+    history[0, 0, cols - 1] = 1
+    assert torch.equal(got.history, history)
+
+
 def test_scores_of_one_beam_add_up():
     """With the vocabulary as wide as the beam every probability comes back: they sum to one."""
     x = logits((1, 1, 60), "f32", 9)
