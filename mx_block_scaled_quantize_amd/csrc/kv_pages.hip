@@ -692,10 +692,10 @@ __global__ __launch_bounds__(256) void fork_rows_kernel(const ForkArgs g) {
     g.lens_out[i] = c.had + (fits ? c.fresh : 0);
     if (copy) atomicSub(&g.refs_out[row[c.held - 1]], 1);
   }
-  for (int t = threadIdx.x; t < c.fresh; t += 256) {
+  for (int64_t t = threadIdx.x; t < c.fresh; t += 256) {
     int64_t slot = -1;
     if (fits) {
-      const int at = c.had + t, j = at / g.shape.page;
+      const int at = int(c.had + t), j = at / g.shape.page;
       const int32_t page = j < kept ? row[j] : g.list[start + j - kept];
       if (in_pool(g, page)) slot = int64_t(page) * g.shape.page + at % g.shape.page;
     }

@@ -173,6 +173,16 @@ def test_fork_of_tokens_without_children(pages):
     assert slots.tolist() == [-1] * 300 and not got.refs.any()
 
 
+def test_fork_of_the_most_tokens():
+    """2^31 - 1 new tokens of a child that no pool could hold: the count of the last step passes 31 bits."""
+    most = (1 << 31) - 1
+    slots = torch.full((most,), 7, device=dev())
+    got = mxa.mx_kv_fork(mxa.new_kv_cache(4, 1, 16, 64), ints([0] * 4), ints([[0, 0]]), ints([0]), ints([0, most]),
+                         tokens=most, out=(ints([9] * 4), ints([[9, 9]]), ints([9]), slots))
+    assert got.lens.tolist() == [0] and got.refs.tolist() == [0] * 4 and got.page_table.tolist() == [[-1, -1]]
+    assert int(slots.min()) == int(slots.max()) == -1
+
+
 def test_table_of_wider_rows_and_bad_entries():
     """A table that is part of a wider one; pages outside the pool are held by nobody and not written to."""
     wide = ints([[3, 0, 1, 7], [9, 9, 2, 7], [-4, 1, 1, 7]])
