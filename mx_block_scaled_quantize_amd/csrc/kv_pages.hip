@@ -478,7 +478,7 @@ __global__ __launch_bounds__(256) void fork_needs_kernel(const ForkArgs g) {
     }
     need = int(after) - c.held + copy;
     info = 2 * need + copy;
-    if (after > g.out_cols) need = 0, info = -1, copy = false;
+    if (after > g.out_cols) info = -1, copy = false;        // gets none, and what it needs still counts
     g.info[i] = info;
   }
   int64_t total;
@@ -621,8 +621,9 @@ __global__ __launch_bounds__(1024) void fork_small_kernel(const ForkArgs g) {
   // pages that each child needs
   const int64_t after = (int64_t(c.had) + c.fresh + g.shape.page - 1) / g.shape.page;
   const bool wide = after > g.out_cols;
-  const bool copy = !wide && in_pool(g, tail) && !(count[tail] == writers[c.row] && first[c.row] == t);
-  const int64_t need = wide ? 0 : after - c.held + copy;
+  const bool shared = in_pool(g, tail) && !(count[tail] == writers[c.row] && first[c.row] == t);
+  const bool copy = shared && !wide;                      // too many for a row: gets none, and what it needs still counts
+  const int64_t need = after - c.held + shared;
   int64_t sums;                             // of pages, and of copies in the lowest bits (1024 at most)
   const int64_t both = block_scan<16>(need * 2048 + copy, sums);
   const int64_t start = both >> 11;

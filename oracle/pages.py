@@ -45,12 +45,12 @@ def fork(refs, table, lens, page, cu=None, parents=None, release=True, tokens=0,
         row, n = list(at(p)[0]), at(p)[1]
         lo, hi = spans[i]
         after = held(n + hi - lo, page)
-        if hi > lo and after <= cols:
+        if hi > lo:
             mine = writers.get(p, ())
             copy = i in mine and 0 <= row[-1] < pages and not (mine[0] == i and shared[row[-1]] == len(mine))
             need = copy + after - len(row)
-            taken += need
-            if need == 0 or taken <= len(free):
+            taken += need                    # also by a child that gets none of them
+            if after <= cols and (need == 0 or taken <= len(free)):
                 new = free[taken - need:taken]
                 if copy:
                     copies.append((row[-1], new[0], -(-(n % page) // 16) * 16))

@@ -183,6 +183,24 @@ def test_fork_of_the_most_tokens():
     assert int(slots.min()) == int(slots.max()) == -1
 
 
+@pytest.mark.parametrize("more", [0, 20000])
+def test_pages_of_a_child_too_wide_are_not_given_to_later_ones(more):
+    """In one launch and, with pages in use behind the free ones, in several."""
+    def fork(refs, table, lens, *args, **kw):
+        cache = mxa.new_kv_cache(len(refs) + more, 1, 16, 64)
+        got = mxa.mx_kv_fork(cache, ints(refs + [1] * more), ints(table), ints(lens), *args, **kw)
+        assert got.refs[len(refs):].tolist() == [1] * more
+        return got.refs[:len(refs)].tolist(), got.page_table.tolist(), got.lens.tolist(), got.slots.tolist()
+
+    cu, two = ints([0, 40, 41]), [[0, 0]] * 2
+    for parents in (None, ints([0, 1]), ints([-1, -1])):
+        assert fork([0] * 6, two, [0, 0], cu, parents) == \
+            ([0, 0, 0, 1, 0, 0], [[-1, -1], [3, -1]], [0, 1], [-1] * 40 + [48])
+        assert fork([0] * 3, two, [0, 0], cu, parents) == ([0] * 3, [[-1, -1]] * 2, [0, 0], [-1] * 41)
+    assert fork([1, 1] + [0] * 5, [[0, 1]], [20], cu, ints([0, 0]), release=False) == \
+        ([3, 2, 0, 0, 0, 1, 0], [[0, 1], [0, 5]], [20, 21], [-1] * 40 + [84])
+
+
 def test_table_of_wider_rows_and_bad_entries():
     """A table that is part of a wider one; pages outside the pool are held by nobody and not written to."""
     wide = ints([[3, 0, 1, 7], [9, 9, 2, 7], [-4, 1, 1, 7]])

@@ -114,6 +114,18 @@ def test_small_fork_by_hand():
     assert (refs, table, lens, slots) == ([1, 1, 1], [[0, 2], [1, -1]], [17, 16], [32, -1])
 
 
+def test_pages_of_a_child_too_wide_are_not_given_to_later_ones():
+    # the first child would need three pages in a row of two: the second gets the fourth free one
+    assert op.fork([0] * 6, [[0, 0]] * 2, [0, 0], 16, [0, 40, 41], None, True, 41) == \
+        ([0, 0, 0, 1, 0, 0], [[-1, -1], [3, -1]], [0, 1], [-1] * 40 + [48], [])
+    # three free pages: none is left for it
+    assert op.fork([0] * 3, [[0, 0]] * 2, [0, 0], 16, [0, 40, 41], None, True, 41) == \
+        ([0] * 3, [[-1, -1]] * 2, [0, 0], [-1] * 41, [])
+    # a copy that the first asked for counts too: two new pages, and one for the partly filled one
+    assert op.fork([1, 1] + [0] * 5, [[0, 1]], [20], 16, [0, 40, 41], [0, 0], False, 41) == \
+        ([3, 2, 0, 0, 0, 1, 0], [[0, 1], [0, 5]], [20, 21], [-1] * 40 + [84], [(1, 5, 16)])
+
+
 def test_small_compact_by_hand():
     refs, table, used, moves = op.compact([0, 2, 0, 0, 1, 3], [[5, 1, 4], [4, 5, 5]], [33, 10], 16)
     assert (refs, used, moves) == ([3, 2, 1, 0, 0, 0], 3, [(5, 0), (4, 2)])
