@@ -23,6 +23,7 @@ constexpr int kMostSplits = 64;             // a lane for each segment of a beam
 constexpr int kFew = 128;                   // candidates of a request that are all compared with each other
 constexpr int kGood = 512;                  // and of more, those that can be
 constexpr int kBuffer = 512;                // candidates a wave sets aside before it sorts them in
+constexpr int64_t kMostBlocks = 1 << 23;    // of 256 threads in a launch, which has fewer than 2^32 threads
 
 typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));      // of logits, at any place of their type
 typedef int32_t Vector __attribute__((ext_vector_type(4)));
@@ -44,7 +45,7 @@ struct BeamArgs {
   uint8_t* finished_out;
   Part* parts;                              // [rows][splits]
   uint64_t* best;                           // [rows][splits][keep]
-  int64_t request_stride, beam_stride, rows, segment;
+  int64_t request_stride, beam_stride, rows, segment, first;           // first: the workgroup that a launch begins with
   int requests, beams, vocab, width, keep, splits, eos, pad, cols, vector;
 };
 
@@ -245,7 +246,7 @@ __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
   __shared__ uint64_t buffers[4][kBuffer];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   uint64_t* buffer = buffers[wave];
-  const int64_t id = int64_t(blockIdx.x) * 4 + wave;
+  const int64_t id = (g.first + blockIdx.x) * 4 + wave;
   const int64_t row = id / g.splits;
   const int split = int(id - row * g.splits);
   if (row >= g.rows || !live(g, row)) return;
@@ -633,17 +634,22 @@ extern "C" mx_status_t mx_beam_select(const void* logits, mx_dtype_t dtype, int6
   g.best = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(workspace) + parts_bytes(g));
   g.request_stride = request_stride; g.beam_stride = beam_stride;
   g.eos = int(eos); g.pad = int(pad); g.cols = int(history_cols);
-  const unsigned blocks = unsigned((g.rows * g.splits + 3) / 4);
+  const int64_t all_blocks = (g.rows * g.splits + 3) / 4;
   auto scan = [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     const int64_t loads = (g.segment + 64 * Elements<DT>::kVec - 1) / (64 * Elements<DT>::kVec);
+    const unsigned blocks = unsigned(std::min(kMostBlocks, all_blocks - g.first));
     if (loads <= 2) beam_scan_kernel<DT, 2><<<blocks, 256, 0, stream>>>(g);
     else if (loads <= 4) beam_scan_kernel<DT, 4><<<blocks, 256, 0, stream>>>(g);
     else beam_scan_kernel<DT, 8><<<blocks, 256, 0, stream>>>(g);
   };
-  if (dtype == MX_F32) scan(std::integral_constant<int, MX_F32>{});
-  else if (dtype == MX_BF16) scan(std::integral_constant<int, MX_BF16>{});
-  else scan(std::integral_constant<int, MX_F16>{});
+  for (; g.first < all_blocks; g.first += kMostBlocks) {
+    if (dtype == MX_F32) scan(std::integral_constant<int, MX_F32>{});
+    else if (dtype == MX_BF16) scan(std::integral_constant<int, MX_BF16>{});
+    else scan(std::integral_constant<int, MX_F16>{});
+    // what was not scanned is not merged
+    if (hipGetLastError() != hipSuccess) return MX_ERR_LAUNCH;
+  }
   g.vector = g.cols % 4 == 0 && !misaligned(history) && !misaligned(history_out);
   // 32 KiB of history a workgroup, up to two of them on a CU
   const int64_t wide = with_history ? g.width * int64_t(g.cols) * 4 / 32768 : 0;

@@ -238,6 +238,21 @@ def test_a_history_of_the_most_columns():
     assert torch.equal(got.history, history)
 
 
+def test_the_most_rows():
+    """2^20 requests of 64 beams, a wave for each: 2^32 threads, more than a launch can have."""
+    requests, beams, width = 1 << 20, 64, 3
+    g = torch.Generator(device=dev()).manual_seed(8)
+    # sixteenths, so that beams of a request tie
+    scores = torch.randint(-2000, 0, (requests, beams), generator=g, device=dev()).float() / 16
+    x = torch.randn(requests, beams, 1, generator=g, device=dev()).bfloat16()
+    got = mxa.mx_beam_select(x, scores, width, pad=7)
+    # of one token the log-probability is 0
+    want, parents = scores.sort(dim=1, descending=True, stable=True)
+    assert torch.equal(got.scores, want[:, :width])
+    first = torch.arange(requests, device=dev())[:, None] * beams
+    assert torch.equal(got.parents.long(), parents[:, :width] + first) and not got.tokens.any() and not got.finished.any()
+
+
 def test_scores_of_one_beam_add_up():
     """With the vocabulary as wide as the beam every probability comes back: they sum to one."""
     x = logits((1, 1, 60), "f32", 9)
