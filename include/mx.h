@@ -531,8 +531,8 @@ mx_status_t mx_kv_fork_workspace(int64_t pages, int64_t rows, int64_t children, 
 /* Cuts sequences to keep[r] tokens (those not longer stay; NULL: all end): each page behind
  * the last kept one loses a hold, and is free when none is left.
  *   refs_out, lens_out  counts and lengths after the call; may be refs and lens (lens_out not keep).
- * workspace  mx_kv_free_workspace bytes, 16-byte aligned (may be NULL when that is 0, as it is up to 2^19
- *              entries of the table); nothing is kept in it between calls.
+ * workspace  mx_kv_free_workspace bytes, 16-byte aligned (may be NULL when that is 0, as it is for fewer than
+ *              2^19 entries of the table); nothing is kept in it between calls.
  * Errors: MX_ERR_SHAPE (also a workspace too small), MX_ERR_ARG (lens_out is keep), MX_ERR_NULL, MX_ERR_ALIGN; MX_ERR_LAUNCH. */
 mx_status_t mx_kv_free(const int32_t* refs, int64_t pages, int page, const int32_t* page_table, int64_t table_stride,
                        int64_t table_cols, const int32_t* lens, int64_t rows, const int32_t* keep, int32_t* refs_out,

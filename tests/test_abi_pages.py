@@ -133,6 +133,13 @@ def test_select(status, kw):
     assert select(**kw) == status
 
 
+def test_frees_of_fewer_than_2_19_entries_need_no_workspace():
+    n = ctypes.c_int64(-1)
+    for rows, cols, none in ((1, (1 << 19) - 1, True), ((1 << 19) - 1, 1, True), (1 << 10, (1 << 9) - 1, True),
+                             (1 << 19, 1, False), (1, 1 << 19, False)):
+        assert lib.mx_kv_free_workspace(1 << 20, rows, cols, 16, ctypes.byref(n)) == OK and (n.value == 0) == none
+
+
 def test_workspaces():
     n = ctypes.c_int64(-1)
     at = ctypes.byref(n)
