@@ -235,9 +235,10 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // A wave for each segment of each beam's logits.  Eight loads of 16 bytes a lane are in flight, past the caches (which
 // spares 8%); a chunk's maximum moves each lane's own reference before its exponentials are added, in 32 bits within a
 // chunk and in 64 across chunks.  The first chunk's keep-th largest lane maximum is a bound that at least keep logits
-// reach: those that reach it, some more than keep, are set aside and sorted.  2048 rows of 131072 BF16 logits take 109
-// to 112 us, 4.8 to 4.9 TB/s, as a copy does, with the vector unit busy 74% of the time.  Tried: each granule's registers
-// reloaded for the next chunk as soon as it is worked off, 128 us: the compiler waits for all of them at the loop's head.
+// reach: those that reach it, some more than keep, are set aside and sorted.  2048 rows of 131072 BF16 logits take 100 us
+// at best and 108 to 112 on average over 30 calls, 5.4 and 4.8 to 5.0 TB/s, as a copy does, with the vector unit busy 74% of
+// the time.  Tried: each granule's registers reloaded for the next chunk as soon as it is worked off, 128 us: the compiler
+// waits for all of them at the loop's head.
 template <int DT, int kLoads>
 __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
   using E = Elements<DT>;
@@ -341,10 +342,11 @@ __global__ __launch_bounds__(256) void beam_scan_kernel(const BeamArgs g) {
 // some of the columns).  A wave for each beam joins its segments; then each candidate counts those better than it.
 // One request of four beams takes 5.6 us, nearly all of it latency: 1.7 for what the first launch left in other XCDs' caches,
 // 1 for a beam's best, 1 for the choice, 1 to 2 for a history; 256 requests of eight beams with histories of 2048
-// tokens (33 MB read and written) 13.  One candidate chosen after the other, by a wave, took 700 clocks each.
+// tokens (33 MB read and written) 12 to 13.  One candidate chosen after the other, by a wave, took 700 clocks each.
 // kMany: of more than 128 candidates only those are compared that reach a bound, and 16 waves share the beams: 4
-// requests of 16 beams, 32 to be chosen, take 26 us (39 with eight waves that compare all), where one request of four
-// beams would take 6.6.
+// requests of 16 beams, 32 to be chosen, take 25 us (39 with eight waves that compare all), where one request of four
+// beams would take 6.6.  The segments' lists come in order; that order is not used, and of more than 64 candidates that
+// reach the bound each 64 are sorted again.
 template <int kWaves, bool kMany>
 __global__ __launch_bounds__(64 * kWaves) void beam_merge_kernel(const BeamArgs g) {
   __shared__ uint64_t buffers[kWaves][kBuffer];

@@ -748,7 +748,7 @@ __global__ __launch_bounds__(256) void free_pages_kernel(const FreeArgs g) {
 
 // Tables of many entries: the pages that lose a hold are put in order of buckets of 2^shift pages, a tile of 8192
 // entries in LDS at a time; then a workgroup for each bucket counts them in LDS and subtracts: no atomics in memory.
-// 4096 rows of 1025 entries over two million pages that lie anywhere, copy of the counts included: 20 us where 790000
+// 4096 rows of 1025 entries over 1.4 million pages that lie anywhere, copy of the counts included: 20 us where 790000
 // entries lose a hold, 32 where all 3.1 million do; 38 and 124 by atomics.  Of rows whose pages follow each other, 32 counts
 // a line, 23 and 32, by atomics 10 and 16: pages come in such order from a fresh pool only.
 constexpr int kTile = 8192, kBuckets = 256;
@@ -1147,8 +1147,18 @@ mx_status_t fork_sizes(ForkArgs& g, int64_t pages, int64_t rows, int64_t childre
   return MX_OK;
 }
 
-// Whether the entries of a table are put in order first, and in what: see free_pages_kernel for what it costs not to.
-// From 2^19 entries on the two launches are worth it, up to 2^28 the workspace; buckets of up to 2^15 pages fit LDS.
+// Whether the entries of a table are put in order first, and in what.  The host knows the table's size alone, not how many
+// rows end nor where their pages lie.  Microseconds by atomics and in order, rows of 512 entries over 100000 pages, counts
+// copied, captured (those of 1.5 million pages within 9 of these):
+//   entries                            2^18          2^19          2^20          2^21          2^22
+//   pages anywhere, all rows end       14.4   14.6   24.8   15.6   45.6   17.2   86.9   21.8   171    32.4
+//                   a quarter           6.8   10.7   10.4   11.1   15.7   11.8   27.1   13.3   48.9   19.5
+//                   8 rows              5.0    8.3    5.5    8.5    5.7    8.4    6.4    8.7    7.9   11.1
+//   pages in a row, all rows end        4.9   15.9    5.8   17.9    7.0   19.8   10.2   21.6   17.5   29.0
+//                   8 rows              4.4   11.6    4.9   11.4    5.2   11.6    5.9   11.7    7.4   14.2
+// In place the atomics take 1 to 5 less (8 rows, anywhere: 3.9 against 8.3 with 2^19, 6.6 against 11.0 with 2^22).  So from 2^19
+// entries on, where all rows that end first gain: what it can save grows with the table, what it can cost stays at 3 to 18.
+// Up to 2^28 entries for the workspace's sake; buckets of up to 2^15 pages fit LDS.
 bool free_plan(FreeArgs& g, int64_t pages, int64_t rows, int64_t cols) {
   if (rows * cols < (int64_t(1) << 19) || rows * cols > (int64_t(1) << 28)) return false;
   if (pages <= kSmallPages || pages > int64_t(kBuckets) << 15) return false;
